@@ -536,6 +536,135 @@ int mfsdp_checkpoint_read(const char* path, mfsdp_checkpoint_header* header,
                           float* momentum, int64_t momentum_capacity,
                           float* tail_p, float* tail_m, float* tail_v, int64_t tail_capacity_elems);
 
+/* ------------------------------------------------------------------------
+ * Operators next to the owner step (no counterpart in the paper: additions of
+ * this library).  They make and condition the gradients the step reads: the
+ * tokens' embedding rows and the embedding's gradient (a tail tensor), the
+ * products of a mixture-of-experts layer and their weight gradients (the
+ * expert matrices), and the global norm that clips all of them.  The
+ * conventions at the top of this file hold: host checks first, asynchronous on
+ * `stream`, no allocation, workspaces scratch only.  Every result is
+ * reproducible bit for bit: no sum's order depends on timing.
+ * ------------------------------------------------------------------------ */
+
+/* One tensor of a gradient set: numel contiguous elements at src, aligned to
+ * their own size (a shard of a flat buffer at any offset). */
+typedef struct {
+  const void* src;
+  void* dst;            /* mfsdp_grad_clip: where the clipped gradient goes; ignored by mfsdp_grad_norm */
+  int64_t numel;        /* >= 0; 0: skipped */
+  int32_t src_dtype;
+  int32_t dst_dtype;    /* ignored by mfsdp_grad_norm */
+} mfsdp_grad_tensor;
+
+/* Bytes of workspace both calls below need for a set of n tensors (0 for n < 0). */
+size_t mfsdp_grad_clip_workspace_bytes(int32_t n);
+
+/* Global gradient norm over any number of tensors:
+ *   norm = sqrt(sum over all tensors and elements of g^2)
+ *   coef = min(1, max_norm / (norm + eps));  1 for an infinite max_norm or norm + eps = 0
+ *   out[0] = norm, out[1] = coef            (device, two floats, 8-byte aligned)
+ * A NaN anywhere gives NaN for both; an Inf gives norm Inf and coef 0.  Sums
+ * run in fp32 over 64 elements and in double above that, and a sum that leaves
+ * fp32's accurate range is taken again in double: any finite gradient has a
+ * right norm (rounded to fp32, so Inf above its range; coef uses the double).
+ * n = 0 gives norm 0.  Errors: INVALID_ARG (max_norm < 0 or NaN, eps < 0 or not finite,
+ * NULL pointer, negative count), UNSUPPORTED_DTYPE, MISALIGNED, OVERLAP (out or
+ * workspace with a tensor), WORKSPACE_TOO_SMALL, UNSUPPORTED_SHAPE, CUDA. */
+int mfsdp_grad_norm(const mfsdp_grad_tensor* tensors, int32_t n, double max_norm, double eps, float* out,
+                    void* workspace, size_t workspace_bytes, void* stream);
+
+/* mfsdp_grad_norm, then dst = coef * src for every tensor (fp32 product,
+ * rounded once to dst_dtype).  dst may be src with the same dtype (in place:
+ * nothing is written when coef is 1); otherwise a dst must not overlap any
+ * tensor (OVERLAP). */
+int mfsdp_grad_clip(const mfsdp_grad_tensor* tensors, int32_t n, double max_norm, double eps, float* out,
+                    void* workspace, size_t workspace_bytes, void* stream);
+
+/* Ids are signed integers, contiguous and aligned to their size.  An id outside
+ * [0, n_keys) (or [0, vocab)) is masked: it is no error. */
+#define MFSDP_ID_I32 0
+#define MFSDP_ID_I64 1
+
+size_t mfsdp_sort_ids_workspace_bytes(int64_t n, int64_t n_keys);
+
+/* Stable sort of n positions by id: order[i] is the i-th position, equal ids in
+ * ascending position, masked ids last (in ascending position); the positions of
+ * id k are order[starts[k]] .. order[starts[k + 1] - 1], and starts[n_keys] is
+ * the number of unmasked ids.  With expert numbers as ids, `starts` is what the
+ * grouped products take.
+ *   order[n], starts[n_keys + 1]   out, device int32.
+ * n <= 2^31 - 1, n_keys < 2^31 - 1 (UNSUPPORTED_SHAPE).  Other errors:
+ * INVALID_ARG, UNSUPPORTED_DTYPE (id_type), MISALIGNED, OVERLAP,
+ * WORKSPACE_TOO_SMALL, CUDA. */
+int mfsdp_sort_ids(const void* ids, int32_t id_type, int64_t n, int64_t n_keys, int32_t* order, int32_t* starts,
+                   void* workspace, size_t workspace_bytes, void* stream);
+
+/* Embedding lookup with scaling: out[t, :] = scale * weight[ids[t], :], zeros
+ * for a masked id; fp32 product, rounded once to out_dtype.
+ *   weight   vocab rows of dim elements, weight_ld >= dim elements apart.
+ *   out      n rows of dim elements, out_ld >= dim apart; only those elements
+ *            are written.
+ * weight and out 16-byte aligned.  n = 0 is a no-op.  Errors: INVALID_ARG
+ * (scale not finite), UNSUPPORTED_DTYPE, UNSUPPORTED_SHAPE (dim > 2^24, a
+ * leading dimension below dim), MISALIGNED, OVERLAP, CUDA. */
+int mfsdp_embedding_lookup(const void* weight, int32_t weight_dtype, int64_t vocab, int64_t dim, int64_t weight_ld,
+                           const void* ids, int32_t id_type, int64_t n, double scale, void* out, int32_t out_dtype,
+                           int64_t out_ld, void* stream);
+
+size_t mfsdp_embedding_grad_workspace_bytes(int64_t n, int64_t vocab, int64_t dim);
+
+/* Gradient of the lookup by sorted tokens:
+ *   grad[v, :] = scale * sum over t with ids[t] = v of dout[t, :]
+ * summed in fp32 in a fixed order, rounded once to grad_dtype.  accumulate = 0 writes
+ * every row (zeros where no id names it); accumulate = 1 adds to the rows that
+ * ids name (read in grad_dtype, added in fp32) and leaves the others alone.
+ *   dout   n rows of dim elements, dout_ld apart;  grad  vocab rows, grad_ld
+ *          apart; both 16-byte aligned.
+ * Errors as for the lookup, plus WORKSPACE_TOO_SMALL. */
+int mfsdp_embedding_grad(const void* dout, int32_t dout_dtype, int64_t dout_ld, const void* ids, int32_t id_type,
+                         int64_t n, double scale, void* grad, int32_t grad_dtype, int64_t vocab, int64_t dim,
+                         int64_t grad_ld, int32_t accumulate, void* workspace, size_t workspace_bytes, void* stream);
+
+#define MFSDP_MAX_EXPERTS 1024
+
+/* Workspace of the grouped products for n_experts matrices of rows x cols,
+ * w_stride elements apart, and n_rows activations whose `rows`-wide side has
+ * leading dimension rows_ld and whose `cols`-wide side cols_ld (0 on invalid input). */
+size_t mfsdp_expert_workspace_bytes(int32_t n_experts, int64_t n_rows, int64_t rows, int64_t cols, int64_t w_stride,
+                                    int64_t rows_ld, int64_t cols_ld);
+
+/* Products grouped by expert.  Expert e owns the matrix W_e (rows x cols, row
+ * major, at w + e * w_stride: the flat layout of the owner step's matrices) and
+ * the activation rows starts[e] .. starts[e + 1] - 1:
+ *   input_grad = 0:  y[t, :] = W_e x[t, :]      x n_rows x cols, y n_rows x rows
+ *   input_grad = 1:  y[t, :] = W_e^T x[t, :]    x n_rows x rows, y n_rows x cols
+ * bf16 operands (in_dtype must be BF16), fp32 accumulation, one rounding to
+ * y_dtype.
+ *   starts[n_experts + 1]  device int32, starts[0] = 0, ascending; read on the
+ *          device (values outside [0, n_rows] are clamped).  Rows from
+ *          starts[n_experts] on belong to no expert: their y is zero.
+ *   x, w, y 16-byte aligned; leading dimensions x_ld, y_ld at least the widths,
+ *          w_stride >= rows * cols.
+ * n_rows = 0 is a no-op.  n_experts <= MFSDP_MAX_EXPERTS, n_rows <= 2^30, rows,
+ * cols <= 2^24.  Errors: INVALID_ARG, UNSUPPORTED_DTYPE, UNSUPPORTED_SHAPE,
+ * MISALIGNED, OVERLAP, WORKSPACE_TOO_SMALL, CUDA. */
+int mfsdp_expert_matmul(const void* x, int64_t x_ld, const void* w, int64_t w_stride, int32_t in_dtype,
+                        const int32_t* starts, int32_t n_experts, int64_t n_rows, int64_t rows, int64_t cols,
+                        int32_t input_grad, void* y, int32_t y_dtype, int64_t y_ld, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/* Weight gradient of the grouped product: dw_e = sum over the expert's rows t
+ * of dy[t, :]^T x[t, :] (rows x cols at dw + e * dw_stride, so dw may be the flat
+ * gradient buffer of the owner step), in fp32, rounded once to dw_dtype.
+ * accumulate = 0 writes every expert's matrix (zeros for one without rows);
+ * accumulate = 1 adds to it.  Other arguments and errors as above; the
+ * workspace as for w_stride = rows * cols. */
+int mfsdp_expert_weight_grad(const void* dy, int64_t dy_ld, const void* x, int64_t x_ld, int32_t in_dtype,
+                             const int32_t* starts, int32_t n_experts, int64_t n_rows, int64_t rows, int64_t cols,
+                             void* dw, int32_t dw_dtype, int64_t dw_stride, int32_t accumulate, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
 /* Static description of a status code (never NULL). */
 const char* mfsdp_status_string(int status);
 

@@ -45,7 +45,10 @@ EXPORTED = ("mfsdp_plan_owners", "mfsdp_muon_workspace_bytes", "mfsdp_muon_owner
             "mfsdp_model_layout", "mfsdp_placement_segments", "mfsdp_segment_copy", "mfsdp_test_inject_stall",
             "mfsdp_host_step_groups", "mfsdp_muon_static_scratch_status", "mfsdp_checkpoint_bytes",
             "mfsdp_checkpoint_write", "mfsdp_checkpoint_read_header", "mfsdp_checkpoint_read",
-            "mfsdp_muon_gram_space_layout")
+            "mfsdp_muon_gram_space_layout", "mfsdp_grad_clip_workspace_bytes", "mfsdp_grad_norm", "mfsdp_grad_clip",
+            "mfsdp_sort_ids_workspace_bytes", "mfsdp_sort_ids", "mfsdp_embedding_lookup",
+            "mfsdp_embedding_grad_workspace_bytes", "mfsdp_embedding_grad", "mfsdp_expert_workspace_bytes",
+            "mfsdp_expert_matmul", "mfsdp_expert_weight_grad")
 
 SEGMENT_REDUCE = 0
 SEGMENT_GATHER = 1
@@ -519,6 +522,220 @@ def checkpoint_load(path: str) -> Checkpoint:
                                       mom.ctypes.data, h.matrix_elems, *[t.ctypes.data for t in tail], h.tail_elems),
            "checkpoint_read")
     return Checkpoint(h, [marr[i] for i in range(h.n_matrix)], [tarr[i] for i in range(h.n_tail)], mom, *tail)
+
+
+# --------------------------------------------------- operators next to the step
+ID_I32 = 0
+ID_I64 = 1
+MAX_EXPERTS = 1024
+
+
+class GradTensor(ctypes.Structure):
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("numel", ctypes.c_int64),
+                ("src_dtype", ctypes.c_int32), ("dst_dtype", ctypes.c_int32)]
+
+
+_lib.mfsdp_grad_clip_workspace_bytes.argtypes = [_i32]
+_lib.mfsdp_grad_clip_workspace_bytes.restype = _sz
+for _f in (_lib.mfsdp_grad_norm, _lib.mfsdp_grad_clip):
+    _f.argtypes = [ctypes.POINTER(GradTensor), _i32, _d, _d, _vp, _vp, _sz, _vp]
+    _f.restype = ctypes.c_int
+_lib.mfsdp_sort_ids_workspace_bytes.argtypes = [_i64, _i64]
+_lib.mfsdp_sort_ids_workspace_bytes.restype = _sz
+_lib.mfsdp_sort_ids.argtypes = [_vp, _i32, _i64, _i64, _vp, _vp, _vp, _sz, _vp]
+_lib.mfsdp_sort_ids.restype = ctypes.c_int
+_lib.mfsdp_embedding_lookup.argtypes = [_vp, _i32, _i64, _i64, _i64, _vp, _i32, _i64, _d, _vp, _i32, _i64, _vp]
+_lib.mfsdp_embedding_lookup.restype = ctypes.c_int
+_lib.mfsdp_embedding_grad_workspace_bytes.argtypes = [_i64, _i64, _i64]
+_lib.mfsdp_embedding_grad_workspace_bytes.restype = _sz
+_lib.mfsdp_embedding_grad.argtypes = [_vp, _i32, _i64, _vp, _i32, _i64, _d, _vp, _i32, _i64, _i64, _i64, _i32, _vp,
+                                      _sz, _vp]
+_lib.mfsdp_embedding_grad.restype = ctypes.c_int
+_lib.mfsdp_expert_workspace_bytes.argtypes = [_i32, _i64, _i64, _i64, _i64, _i64, _i64]
+_lib.mfsdp_expert_workspace_bytes.restype = _sz
+_lib.mfsdp_expert_matmul.argtypes = [_vp, _i64, _vp, _i64, _i32, _vp, _i32, _i64, _i64, _i64, _i32, _vp, _i32, _i64,
+                                     _vp, _sz, _vp]
+_lib.mfsdp_expert_matmul.restype = ctypes.c_int
+_lib.mfsdp_expert_weight_grad.argtypes = [_vp, _i64, _vp, _i64, _i32, _vp, _i32, _i64, _i64, _i64, _vp, _i32, _i64,
+                                          _i32, _vp, _sz, _vp]
+_lib.mfsdp_expert_weight_grad.restype = ctypes.c_int
+
+
+def _flat(t, what: str):
+    """A contiguous CUDA tensor (any shape), as the library reads it."""
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return t
+
+
+def _rows_of(t, what: str) -> int:
+    """Leading dimension of a 2D CUDA tensor with contiguous rows."""
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what} must be 2D with contiguous rows")
+    ld = t.stride(0)
+    return ld if t.shape[0] > 1 else max(ld, t.shape[1])
+
+
+def _id_code(t) -> int:
+    import torch
+    return {torch.int32: ID_I32, torch.int64: ID_I64}.get(t.dtype, 99)
+
+
+def _int32(t, n: int, what: str):
+    import torch
+    _flat(t, what)
+    if t.dtype != torch.int32 or t.numel() != n:
+        raise ValueError(f"{what} must be {n} int32 elements")
+    return t
+
+
+def _ws(workspace):
+    return _ptr(workspace), int(workspace.numel() if workspace is not None else 0)
+
+
+class GradSet:
+    """The tensors of a gradient set with their clipped copies, marshalled once
+    (the tensors are kept alive; their addresses must not change)."""
+
+    def __init__(self, srcs, dsts=None):
+        self.srcs = list(srcs)
+        self.dsts = list(dsts) if dsts is not None else self.srcs
+        if len(self.srcs) != len(self.dsts):
+            raise ValueError("as many destinations as sources")
+        self.array = (GradTensor * max(len(self.srcs), 1))()
+        for a, s, d in zip(self.array, self.srcs, self.dsts):
+            _flat(s, "a gradient tensor")
+            _flat(d, "a clipped tensor")
+            if s.numel() != d.numel():
+                raise ValueError("a clipped tensor must be as long as its source")
+            a.src, a.dst, a.numel = _ptr(s), _ptr(d), int(s.numel())
+            a.src_dtype, a.dst_dtype = _dtype_code(s), _dtype_code(d)
+
+    def __len__(self) -> int:
+        return len(self.srcs)
+
+
+def grad_set(srcs, dsts=None) -> GradSet:
+    """A gradient set from contiguous CUDA tensors; dsts (default: srcs, in
+    place) receive the clipped gradients."""
+    return GradSet(srcs, dsts)
+
+
+def grad_clip_workspace_bytes(tensors: GradSet) -> int:
+    return int(_lib.mfsdp_grad_clip_workspace_bytes(len(tensors)))
+
+
+def _norm_out(out):
+    import torch
+    _flat(out, "out")
+    if out.dtype != torch.float32 or out.numel() < 2:
+        raise ValueError("out must be two float32 elements")
+    return _ptr(out)
+
+
+def grad_norm(tensors: GradSet, out, workspace, *, max_norm: float = float("inf"), eps: float = 1e-6,
+              stream=None) -> None:
+    """out[0] = the global norm of the set's sources, out[1] = the clipping
+    coefficient min(1, max_norm / (norm + eps)) (see include/mfsdp.h)."""
+    _check(_lib.mfsdp_grad_norm(tensors.array, len(tensors), float(max_norm), float(eps), _norm_out(out),
+                                *_ws(workspace), _stream(stream)), "grad_norm")
+
+
+def grad_clip(tensors: GradSet, out, workspace, *, max_norm: float, eps: float = 1e-6, stream=None) -> None:
+    """grad_norm, then every destination = coefficient * source."""
+    _check(_lib.mfsdp_grad_clip(tensors.array, len(tensors), float(max_norm), float(eps), _norm_out(out),
+                                *_ws(workspace), _stream(stream)), "grad_clip")
+
+
+def sort_ids_workspace_bytes(n: int, n_keys: int) -> int:
+    return int(_lib.mfsdp_sort_ids_workspace_bytes(int(n), int(n_keys)))
+
+
+def sort_ids(ids, n_keys: int, order, starts, workspace, *, stream=None) -> None:
+    """Stable sort of positions by id (int32 or int64): order[n] and starts[n_keys + 1],
+    both int32; ids outside [0, n_keys) come last (see include/mfsdp.h)."""
+    n = int(_flat(ids, "ids").numel())
+    _check(_lib.mfsdp_sort_ids(_ptr(ids), _id_code(ids), n, int(n_keys), _ptr(_int32(order, n, "order")),
+                               _ptr(_int32(starts, int(n_keys) + 1, "starts")), *_ws(workspace), _stream(stream)),
+           "sort_ids")
+
+
+def embedding_lookup(weight, ids, out, *, scale: float = 1.0, stream=None) -> None:
+    """out[t, :] = scale * weight[ids[t], :]; zeros for an id outside the vocabulary."""
+    w_ld, o_ld = _rows_of(weight, "weight"), _rows_of(out, "out")
+    n, (vocab, dim) = int(_flat(ids, "ids").numel()), weight.shape
+    if tuple(out.shape) != (n, dim):
+        raise ValueError(f"out must be {n} x {dim}")
+    _check(_lib.mfsdp_embedding_lookup(_ptr(weight), _dtype_code(weight), vocab, dim, w_ld, _ptr(ids), _id_code(ids),
+                                       n, float(scale), _ptr(out), _dtype_code(out), o_ld, _stream(stream)),
+           "embedding_lookup")
+
+
+def embedding_grad_workspace_bytes(n: int, vocab: int, dim: int) -> int:
+    return int(_lib.mfsdp_embedding_grad_workspace_bytes(int(n), int(vocab), int(dim)))
+
+
+def embedding_grad(dout, ids, grad, workspace, *, scale: float = 1.0, accumulate: bool = False,
+                   stream=None) -> None:
+    """grad[v, :] = (grad[v, :] +) scale * sum of dout[t, :] over ids[t] = v (see include/mfsdp.h)."""
+    d_ld, g_ld = _rows_of(dout, "dout"), _rows_of(grad, "grad")
+    n, (vocab, dim) = int(_flat(ids, "ids").numel()), grad.shape
+    if tuple(dout.shape) != (n, dim):
+        raise ValueError(f"dout must be {n} x {dim}")
+    _check(_lib.mfsdp_embedding_grad(_ptr(dout), _dtype_code(dout), d_ld, _ptr(ids), _id_code(ids), n, float(scale),
+                                     _ptr(grad), _dtype_code(grad), vocab, dim, g_ld, int(bool(accumulate)),
+                                     *_ws(workspace), _stream(stream)), "embedding_grad")
+
+
+def expert_workspace_bytes(n_experts: int, rows: int, cols: int, n_rows: int, *, w_stride: Optional[int] = None,
+                           rows_ld: Optional[int] = None, cols_ld: Optional[int] = None) -> int:
+    """Workspace of the grouped products; strides default to contiguous tensors."""
+    return int(_lib.mfsdp_expert_workspace_bytes(int(n_experts), int(n_rows), int(rows), int(cols),
+                                                 int(rows * cols if w_stride is None else w_stride),
+                                                 int(rows if rows_ld is None else rows_ld),
+                                                 int(cols if cols_ld is None else cols_ld)))
+
+
+def _stack(t, what: str) -> int:
+    """Element stride between the matrices of a 3D CUDA tensor, each contiguous."""
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1) or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise ValueError(f"{what} must be 3D with contiguous matrices")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def expert_matmul(x, w, starts, y, workspace, *, input_grad: bool = False, stream=None) -> None:
+    """y[t, :] = W_e x[t, :] (input_grad: W_e^T x[t, :]) for the rows t of each expert e, with w of
+    shape (experts, rows, cols) and starts int32 (see include/mfsdp.h)."""
+    x_ld, y_ld, w_stride = _rows_of(x, "x"), _rows_of(y, "y"), _stack(w, "w")
+    e, rows, cols = w.shape
+    n = x.shape[0]
+    xw, yw = (rows, cols) if input_grad else (cols, rows)
+    if x.shape[1] != xw or tuple(y.shape) != (n, yw):
+        raise ValueError(f"x must be n x {xw} and y n x {yw}")
+    in_dtype = _dtype_code(x) if x.dtype == w.dtype else 99
+    _check(_lib.mfsdp_expert_matmul(_ptr(x), x_ld, _ptr(w), w_stride, in_dtype, _ptr(_int32(starts, e + 1, "starts")),
+                                    e, n, rows, cols, int(bool(input_grad)), _ptr(y), _dtype_code(y), y_ld,
+                                    *_ws(workspace), _stream(stream)), "expert_matmul")
+
+
+def expert_weight_grad(dy, x, starts, dw, workspace, *, accumulate: bool = False, stream=None) -> None:
+    """dw[e] = (dw[e] +) dy_e^T x_e over each expert's rows (see include/mfsdp.h)."""
+    dy_ld, x_ld, dw_stride = _rows_of(dy, "dy"), _rows_of(x, "x"), _stack(dw, "dw")
+    e, rows, cols = dw.shape
+    n = x.shape[0]
+    if tuple(dy.shape) != (n, rows) or x.shape[1] != cols:
+        raise ValueError(f"dy must be n x {rows} and x n x {cols}")
+    in_dtype = _dtype_code(x) if x.dtype == dy.dtype else 99
+    _check(_lib.mfsdp_expert_weight_grad(_ptr(dy), dy_ld, _ptr(x), x_ld, in_dtype,
+                                         _ptr(_int32(starts, e + 1, "starts")), e, n, rows, cols, _ptr(dw),
+                                         _dtype_code(dw), dw_stride, int(bool(accumulate)), *_ws(workspace),
+                                         _stream(stream)), "expert_weight_grad")
 
 
 def library_path() -> str:

@@ -1,0 +1,189 @@
+// Stable sort of ids by value: the order that groups token positions by token
+// (the embedding gradient's sums) or rows by expert (the grouped products).
+//
+// Least-significant-digit radix sort, 8 bits a pass, ceil(bits / 8) passes over
+// (key, position) pairs.  The n ids are cut into at most kMaxTiles tiles, one
+// CTA each, whose warps take consecutive runs of it, so that "earlier" is
+// (tile, warp, step, lane) order.  A pass is two launches: every tile counts
+// its digits; then every tile adds up the counts that come before it -- all
+// smaller digits of every tile, and its own digit in earlier tiles -- and
+// moves its pairs.  A pair's place among its warp's equal digits comes from a
+// warp match, so the sort is stable and its result does not depend on timing.
+// An id outside [0, n_keys) sorts as n_keys, after all valid ones.
+#include "ops_internal.h"
+
+namespace mfsdp {
+namespace ops {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kDigits = 256;
+constexpr int kMaxTiles = 256;
+constexpr int kMinSteps = 8;            // a warp's steps of 32 ids a tile, at least
+
+struct SortPlan {
+  int tiles;
+  int steps;                            // steps of 32 ids a warp takes
+  int passes;
+};
+
+SortPlan plan_sort(int64_t n, int64_t n_keys) {
+  SortPlan p;
+  int bits = 0;
+  while (bits < 32 && (n_keys >> bits) != 0) ++bits;     // keys are 0 .. n_keys
+  p.passes = std::max(1, (bits + 7) / 8);
+  const int64_t per_step = kWarps * 32;
+  const int64_t steps_all = (n + per_step - 1) / per_step;
+  const int64_t steps = std::max<int64_t>(kMinSteps, (steps_all + kMaxTiles - 1) / kMaxTiles);
+  p.steps = (int)steps;
+  p.tiles = (int)std::max<int64_t>(1, (steps_all + steps - 1) / steps);
+  return p;
+}
+
+struct PassArgs {
+  const void* ids;          // first pass: the ids; later ones: null
+  int32_t ids64;
+  int32_t n_keys;
+  const int2* in;           // (key, position) pairs of the last pass
+  int2* out;                // pairs, or in the last pass null:
+  int32_t* keys_out;
+  int32_t* order_out;
+  int32_t* counts;          // [tile][digit]
+  int64_t n;
+  int32_t tiles, steps, shift;
+};
+
+__device__ __forceinline__ int2 load_pair(const PassArgs& a, int64_t i) {
+  if (!a.ids) return a.in[i];
+  const int64_t v = a.ids64 ? static_cast<const int64_t*>(a.ids)[i] : static_cast<const int32_t*>(a.ids)[i];
+  return make_int2(v >= 0 && v < a.n_keys ? (int)v : a.n_keys, (int)i);
+}
+
+// Counts of each digit, per warp, over the tile's run of each warp.
+__device__ __forceinline__ void count_digits(const PassArgs& a, int (*cnt)[kDigits]) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int d = threadIdx.x; d < kWarps * kDigits; d += kThreads) (&cnt[0][0])[d] = 0;
+  __syncthreads();
+  const int64_t base = ((int64_t)blockIdx.x * kWarps + warp) * a.steps * 32;
+  for (int k = 0; k < a.steps; ++k) {
+    const int64_t i = base + k * 32 + lane;
+    if (i < a.n) atomicAdd(&cnt[warp][(load_pair(a, i).x >> a.shift) & (kDigits - 1)], 1);
+  }
+  __syncthreads();
+}
+
+__global__ void __launch_bounds__(kThreads) sort_count_kernel(const __grid_constant__ PassArgs a) {
+  __shared__ int cnt[kWarps][kDigits];
+  count_digits(a, cnt);
+  int s = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) s += cnt[w][threadIdx.x];
+  a.counts[(int64_t)blockIdx.x * kDigits + threadIdx.x] = s;
+}
+
+__global__ void __launch_bounds__(kThreads) sort_move_kernel(const __grid_constant__ PassArgs a) {
+  __shared__ int cnt[kWarps][kDigits];       // counts, then the next place of each warp's digit
+  __shared__ int scan[kDigits];
+  count_digits(a, cnt);
+  const int d = threadIdx.x;
+  int before = 0, total = 0;
+  for (int t = 0; t < a.tiles; ++t) {
+    const int c = a.counts[(int64_t)t * kDigits + d];
+    total += c;
+    if (t < (int)blockIdx.x) before += c;
+  }
+  scan[d] = total;
+  __syncthreads();
+  for (int o = 1; o < kDigits; o <<= 1) {     // inclusive scan over the digits
+    const int v = d >= o ? scan[d - o] : 0;
+    __syncthreads();
+    scan[d] += v;
+    __syncthreads();
+  }
+  int at = scan[d] - total + before;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const int c = cnt[w][d];
+    cnt[w][d] = at;
+    at += c;
+  }
+  __syncthreads();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t base = ((int64_t)blockIdx.x * kWarps + warp) * a.steps * 32;
+  for (int k = 0; k < a.steps; ++k) {
+    const int64_t i = base + k * 32 + lane;
+    const bool in = i < a.n;
+    const unsigned live = __ballot_sync(0xffffffffu, in);
+    if (in) {
+      const int2 p = load_pair(a, i);
+      const int digit = (p.x >> a.shift) & (kDigits - 1);
+      const unsigned same = __match_any_sync(live, digit);
+      const int place = cnt[warp][digit] + __popc(same & ((1u << lane) - 1));
+      __syncwarp(live);
+      if ((same >> lane) == 1u) cnt[warp][digit] = place + 1;     // the last of them moves the next place on
+      if (a.out) {
+        a.out[place] = p;
+      } else {
+        a.keys_out[place] = p.x;
+        a.order_out[place] = p.y;
+      }
+    }
+    __syncwarp();
+  }
+}
+
+// starts[k] = the number of sorted keys below k, for k = 0 .. n_keys.
+__global__ void __launch_bounds__(kThreads) key_starts_kernel(const int32_t* keys, int64_t n, int64_t n_keys,
+                                                              int32_t* starts) {
+  const int64_t k = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (k > n_keys) return;
+  int64_t lo = 0, hi = n;
+  while (lo < hi) {
+    const int64_t mid = (lo + hi) >> 1;
+    if (keys[mid] < k) lo = mid + 1; else hi = mid;
+  }
+  starts[k] = (int32_t)lo;
+}
+
+}  // namespace
+
+size_t sort_scratch_bytes(int64_t n, int64_t n_keys) {
+  const SortPlan p = plan_sort(n, n_keys);
+  return round_up((size_t)p.tiles * kDigits * 4, 256) + 2 * round_up((size_t)n * 8, 256);
+}
+
+cudaError_t launch_sort(const SortArgs& s, cudaStream_t stream) {
+  if (s.n <= 0) return cudaSuccess;
+  const SortPlan p = plan_sort(s.n, s.n_keys);
+  uint8_t* base = static_cast<uint8_t*>(s.scratch);
+  int2* buf[2];
+  buf[0] = reinterpret_cast<int2*>(base + round_up((size_t)p.tiles * kDigits * 4, 256));
+  buf[1] = reinterpret_cast<int2*>(reinterpret_cast<uint8_t*>(buf[0]) + round_up((size_t)s.n * 8, 256));
+  for (int k = 0; k < p.passes; ++k) {
+    PassArgs a{};
+    a.ids = k == 0 ? s.ids : nullptr;
+    a.ids64 = s.ids64;
+    a.n_keys = (int32_t)s.n_keys;
+    a.in = k == 0 ? nullptr : buf[(k - 1) & 1];
+    a.out = k == p.passes - 1 ? nullptr : buf[k & 1];
+    a.keys_out = s.keys_out;
+    a.order_out = s.order_out;
+    a.counts = reinterpret_cast<int32_t*>(base);
+    a.n = s.n;
+    a.tiles = p.tiles;
+    a.steps = p.steps;
+    a.shift = 8 * k;
+    sort_count_kernel<<<p.tiles, kThreads, 0, stream>>>(a);
+    sort_move_kernel<<<p.tiles, kThreads, 0, stream>>>(a);
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t launch_key_starts(const int32_t* keys, int64_t n, int64_t n_keys, int32_t* starts, cudaStream_t s) {
+  key_starts_kernel<<<(unsigned)((n_keys + kThreads) / kThreads), kThreads, 0, s>>>(keys, n, n_keys, starts);
+  return cudaGetLastError();
+}
+
+}  // namespace ops
+}  // namespace mfsdp
