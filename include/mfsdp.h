@@ -639,15 +639,17 @@ size_t mfsdp_expert_workspace_bytes(int32_t n_experts, int64_t n_rows, int64_t r
  * the activation rows starts[e] .. starts[e + 1] - 1:
  *   input_grad = 0:  y[t, :] = W_e x[t, :]      x n_rows x cols, y n_rows x rows
  *   input_grad = 1:  y[t, :] = W_e^T x[t, :]    x n_rows x rows, y n_rows x cols
- * bf16 operands (in_dtype must be BF16), fp32 accumulation, one rounding to
- * y_dtype.
+ * bf16 operands (in_dtype must be BF16), fp32 accumulation on tensor cores, one
+ * rounding to y_dtype.
  *   starts[n_experts + 1]  device int32, starts[0] = 0, ascending; read on the
  *          device (values outside [0, n_rows] are clamped).  Rows from
  *          starts[n_experts] on belong to no expert: their y is zero.
  *   x, w, y 16-byte aligned; leading dimensions x_ld, y_ld at least the widths,
  *          w_stride >= rows * cols.
- * n_rows = 0 is a no-op.  n_experts <= MFSDP_MAX_EXPERTS, n_rows <= 2^30, rows,
- * cols <= 2^24.  Errors: INVALID_ARG, UNSUPPORTED_DTYPE, UNSUPPORTED_SHAPE,
+ * A layout whose rows all start on 16-byte boundaries (cols, w_stride and x_ld
+ * multiples of 8) is read in place; any other is first copied, padded, into the
+ * workspace.  n_rows = 0 is a no-op.  n_experts <= MFSDP_MAX_EXPERTS, n_rows <=
+ * 2^30, rows, cols <= 2^24, and 2^30 tiles of 256 x 256 in each product.  Errors: INVALID_ARG, UNSUPPORTED_DTYPE, UNSUPPORTED_SHAPE,
  * MISALIGNED, OVERLAP, WORKSPACE_TOO_SMALL, CUDA. */
 int mfsdp_expert_matmul(const void* x, int64_t x_ld, const void* w, int64_t w_stride, int32_t in_dtype,
                         const int32_t* starts, int32_t n_experts, int64_t n_rows, int64_t rows, int64_t cols,
@@ -664,6 +666,14 @@ int mfsdp_expert_weight_grad(const void* dy, int64_t dy_ld, const void* x, int64
                              const int32_t* starts, int32_t n_experts, int64_t n_rows, int64_t rows, int64_t cols,
                              void* dw, int32_t dw_dtype, int64_t dw_stride, int32_t accumulate, void* workspace,
                              size_t workspace_bytes, void* stream);
+
+/* The status word a grouped product left in its workspace (synchronises
+ * `stream`): MFSDP_OK, or MFSDP_ERR_DEVICE_TIMEOUT if one of its bounded waits
+ * gave up (its outputs are then undefined); *detail (may be NULL) receives the
+ * role that waited (1 a pipeline stage, 2 its operands, 3 a drained and 4 a
+ * finished accumulator, 5 a group's zeroed end).  A wait gives up after 2 s plus 64 ns for each
+ * element of the contraction.  Every call that launches clears the word. */
+int mfsdp_expert_device_status(const void* workspace, void* stream, int32_t* detail);
 
 /* Static description of a status code (never NULL). */
 const char* mfsdp_status_string(int status);

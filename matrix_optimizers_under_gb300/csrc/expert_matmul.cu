@@ -1,93 +1,709 @@
-// Matrix products grouped by expert: rows [starts[e], starts[e + 1]) of the
-// activations meet expert e's matrix W_e (rows x cols).
-//   forward:          Y[t, :]  = X[t, :] W_e^T
-//   input gradient:   dX[t, :] = dY[t, :] W_e
+// Matrix products grouped by expert, on 5th-generation tensor cores: rows
+// [starts[e], starts[e + 1]) of the activations meet expert e's matrix W_e
+// (rows x cols).
+//   forward:          Y[t, :]  = W_e X[t, :]
+//   input gradient:   dX[t, :] = W_e^T dY[t, :]
 //   weight gradient:  dW_e (+)= dY_e^T X_e         (zero for an expert without rows)
-// bf16 operands, fp32 accumulation.
+//
+// Groups are ragged, and a mixture-of-experts layer has many small ones, so
+// the forward products put the matrix on the MMA's M side (always full: 256
+// rows of W_e, or of W_e^T, a CTA pair) and the tokens on its N side, which goes in steps
+// of 32: a group of 40 tokens costs 64 columns, not 256.  The weight gradient
+// has the matrix on both sides and contracts over the tokens.  Operands, as
+// the tensor copies find them in memory (K: the contraction):
+//   forward          A = W_e    K-major       B = X     K-major
+//   input gradient   A = W_e^T  MN-major      B = dY    K-major
+//   weight gradient  A = dY^T   MN-major      B = X^T   MN-major
+// No operand is transposed or copied first.  A matrix edge needs no code: the
+// maps are bounded by the matrix (three dimensions, the expert the last) and
+// fill with zeros.  A group's edge does: on the N side the extra tokens are
+// computed and not stored; on the K side (weight gradient) the MMAs stop at
+// the last 16 tokens, and the rows of those past the group's end, which hold
+// the next group's tokens, are zeroed in shared memory in both operands.
+//
+// CTA pairs (one CTA per SM, cta_group::2) take tiles of 256 x up to 256
+// round-robin from a list that every CTA works out from `starts`, expert by
+// expert, so a wave's tiles share their operands in L2.  A CTA loads its 128
+// rows of A and its half of B, 32 KB per 64 of K: 64 bytes a clock at the full
+// MMA rate, where a CTA alone on 128 x 256 would need 96.  Warp roles: 0
+// producer, 1 MMA issuer (even CTA), 2 zeroes group ends (weight gradient),
+// 4-11 epilogue; two accumulators in TMEM let the epilogue overlap the next
+// tile.  The pipeline has as many stages as shared memory holds at the
+// launch's widest tile: 6 of 32 KB for 256 tokens, 9 of 20 KB for a few tokens,
+// where the product is bound by reading W and bytes in flight count.
+#include <cuda.h>
 #include <cuda_bf16.h>
 
+#include <mutex>
+
 #include "ops_internal.h"
+#include "ops_ptx.cuh"
 
 namespace mfsdp {
 namespace ops {
 namespace {
 
-constexpr int kT = 32;       // output tile edge and K step
+constexpr int kPairM = 256;               // rows of a pair's tile
+constexpr int kCtaM = 128;                // rows of one CTA's half: its TMEM lanes
+constexpr int kMaxN = 256;                // columns of a tile
+constexpr int kStepN = 32;                // N granularity of the pair MMA
+constexpr int kBlockK = 64;               // K of a stage: one 128-byte swizzle row of bf16
+constexpr int kBytesA = kCtaM * kBlockK * 2;          // 16 KB
+constexpr int kMnBlock = 64 * kBlockK * 2;            // 8 KB: 64 MN elements x 64 K rows (MN-major)
+constexpr int kSmemStages = 6 * 32768;
+constexpr int kMaxStages = 9;               // of 20 KB
+constexpr int kEpiWarps = 8;
+constexpr int kFirstEpiWarp = 4;
+constexpr int kThreads = 32 * (kFirstEpiWarp + kEpiWarps);
+constexpr int kAccCols = 256;
+constexpr int kTmemCols = 512;
+constexpr uint64_t kDrainNs = 2000000000ull;          // limit of the waits that end a CTA
 
-__device__ __forceinline__ float bf(const void* p, int64_t i) {
-  return __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[i] << 16);
-}
-__device__ __forceinline__ int64_t clamp_row(int64_t s, int64_t n) { return s < 0 ? 0 : (s > n ? n : s); }
+struct Maps {
+  CUtensorMap a;      // box 64 x 128 (K-major A) or 64 x 64
+  CUtensorMap b;      // box 64 x 32 (K-major B) or 64 x 64
+  CUtensorMap b128;   // box 64 x 128 (K-major B of a full tile)
+};
 
-__device__ __forceinline__ void put(const ExpertArgs& p, int64_t at, float v) {
-  if (p.out_bf16) {
-    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + at;
-    *o = __float2bfloat16_rn(p.accumulate ? v + __bfloat162float(*o) : v);
-  } else {
-    float* o = static_cast<float*>(p.out) + at;
-    *o = p.accumulate ? v + *o : v;
+// First failing wait of a launch: (role << 0); the wait's limit.
+struct Abort {
+  volatile int* flag;
+  int32_t* status;
+  uint64_t limit_ns;
+};
+enum Role : int32_t { kRoleStage = 1, kRoleOperands = 2, kRoleAccFree = 3, kRoleAccFull = 4, kRoleTail = 5 };
+
+template <bool kCluster>
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const Abort& ab, int32_t role) {
+  auto poll = [&] { return kCluster ? ptx::mbar_try_wait_cluster(bar, parity) : ptx::mbar_try_wait(bar, parity); };
+  if (poll()) return true;
+  const uint64_t t0 = ptx::globaltimer_ns();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i)
+      if (poll()) return true;
+    if (*ab.flag) return false;
+    if (ptx::globaltimer_ns() - t0 > ab.limit_ns) {
+      *ab.flag = 1;
+      atomicCAS(ab.status, 0, role);
+      return false;
+    }
   }
 }
 
-// One CTA: a 32 x 32 tile of expert blockIdx.z's product; a group with more
-// row tiles than the grid has takes several turns.
-__global__ void __launch_bounds__(kT * kT) expert_kernel(const __grid_constant__ ExpertArgs p) {
-  __shared__ float sa[kT][kT + 1], sb[kT][kT + 1];
-  const int tx = threadIdx.x % kT, ty = threadIdx.x / kT;
-  const int64_t width = p.mode == kExpertForward ? p.rows : p.cols;       // columns of the output
-  for (int e = blockIdx.z; e <= p.n_experts; e += gridDim.z) {
-    if (e == p.n_experts && p.mode == kExpertWeightGrad) break;
-    const int64_t lo = clamp_row(p.starts[e], p.n_rows);
-    const int64_t hi = e == p.n_experts ? p.n_rows : clamp_row(p.starts[e + 1], p.n_rows);
-    const int64_t height = p.mode == kExpertWeightGrad ? p.rows : hi - lo;
-    const int64_t k_end = p.mode == kExpertForward ? p.cols : (p.mode == kExpertInputGrad ? p.rows : hi - lo);
-    for (int64_t r0 = (int64_t)blockIdx.y * kT; r0 < height; r0 += (int64_t)gridDim.y * kT)
-      for (int64_t c0 = (int64_t)blockIdx.x * kT; c0 < width; c0 += (int64_t)gridDim.x * kT) {
-        const int64_t r = r0 + ty, c = c0 + tx;
-        float acc = 0.f;
-        if (e < p.n_experts)
-          for (int64_t k0 = 0; k0 < k_end; k0 += kT) {
-            // sa[i][k] = A(r0 + i, k0 + k), sb[k][j] = B(k0 + k, c0 + j)
-            float va = 0.f, vb = 0.f;
-            if (p.mode == kExpertWeightGrad) {
-              if (r0 + tx < height && k0 + ty < k_end) va = bf(p.a, (lo + k0 + ty) * p.a_ld + r0 + tx);
-              if (c < width && k0 + ty < k_end) vb = bf(p.b, (lo + k0 + ty) * p.b_ld + c);
-              sa[tx][ty] = va;
-              sb[ty][tx] = vb;
-            } else {
-              if (r < height && k0 + tx < k_end) va = bf(p.a, (lo + r) * p.a_ld + k0 + tx);
-              sa[ty][tx] = va;
-              if (p.mode == kExpertForward) {
-                if (c0 + ty < width && k0 + tx < k_end) vb = bf(p.b, e * p.b_stride + (c0 + ty) * p.b_ld + k0 + tx);
-                sb[tx][ty] = vb;
-              } else {
-                if (c < width && k0 + ty < k_end) vb = bf(p.b, e * p.b_stride + (k0 + ty) * p.b_ld + c);
-                sb[ty][tx] = vb;
-              }
-            }
-            __syncthreads();
+// One tile: `rows` [m0, m0 + 256) of the M side, columns [n0, n0 + n) of the N
+// side (n_mma of them in the MMA), k_len of contraction.
+struct Tile {
+  int32_t e;
+  int32_t group;      // first token of the group
+  int32_t m0, n0;
+  int32_t n, n_mma;
+  int32_t k_len;
+};
+
+struct Shape {
+  int32_t m;          // M side of every tile: rows (forward, weight gradient) or cols
+  int32_t tiles_m;
+  int32_t n;          // weight gradient: N side (cols)
+  int32_t tiles_n, width_n;
+};
+
+__device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+// n split over `parts` tiles, each a multiple of 32 wide.
+__device__ __forceinline__ int even_width(int n, int parts) {
+  return (ceil_div(n, parts) + kStepN - 1) / kStepN * kStepN;
+}
+
+template <int kMode>
+__device__ __forceinline__ Tile decode(const ExpertArgs& p, const Shape& sh, const int32_t* start,
+                                       const int32_t* first, int t) {
+  Tile r;
+  if (kMode == kExpertWeightGrad) {
+    const int per = sh.tiles_m * sh.tiles_n;
+    r.e = t / per;
+    const int i = t - r.e * per, j = i / sh.tiles_m;
+    r.m0 = (i - j * sh.tiles_m) * kPairM;
+    r.n0 = j * sh.width_n;
+    r.n = min(sh.width_n, sh.n - r.n0);
+    r.group = start[r.e];
+    r.k_len = max(0, start[r.e + 1] - start[r.e]);
+  } else {
+    int lo = 0, hi = p.n_experts - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (first[mid] <= t) lo = mid; else hi = mid - 1;
+    }
+    r.e = lo;
+    const int len = start[lo + 1] - start[lo];
+    const int width = even_width(len, ceil_div(len, kMaxN));
+    const int i = t - first[lo], j = i / sh.tiles_m;
+    r.m0 = (i - j * sh.tiles_m) * kPairM;
+    r.n0 = j * width;
+    r.n = min(width, len - r.n0);
+    r.group = start[lo];
+    r.k_len = (int)(kMode == kExpertForward ? p.cols : p.rows);
+  }
+  r.n_mma = (r.n + kStepN - 1) / kStepN * kStepN;
+  return r;
+}
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// 32 consecutive columns of one row of a weight gradient.
+__device__ __forceinline__ void store_row(const ExpertArgs& p, int64_t at, int n, const float (&v)[32]) {
+  if (p.out_vec && n == 32) {
+    if (p.out_bf16) {
+      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + at;
 #pragma unroll
-            for (int k = 0; k < kT; ++k) acc = fmaf(sa[ty][k], sb[k][tx], acc);
-            __syncthreads();
+      for (int h = 0; h < 2; ++h) {
+        uint32_t w[8], old[8];
+        if (p.accumulate) ptx::ld_v8(o + 16 * h, old);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          float a = v[16 * h + 2 * k], b = v[16 * h + 2 * k + 1];
+          if (p.accumulate) { a += bf16_lo(old[k]); b += bf16_hi(old[k]); }
+          const __nv_bfloat162 q = __floats2bfloat162_rn(a, b);
+          w[k] = *reinterpret_cast<const uint32_t*>(&q);
+        }
+        ptx::st_v8(o + 16 * h, w);
+      }
+    } else {
+      float* o = static_cast<float*>(p.out) + at;
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        uint32_t w[8], old[8];
+        if (p.accumulate) ptx::ld_v8(o + 8 * h, old);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          w[k] = __float_as_uint(p.accumulate ? v[8 * h + k] + __uint_as_float(old[k]) : v[8 * h + k]);
+        ptx::st_v8(o + 8 * h, w);
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int k = 0; k < 32; ++k) {
+    if (k >= n) continue;
+    if (p.out_bf16) {
+      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + at + k;
+      *o = __float2bfloat16_rn(p.accumulate ? v[k] + __bfloat162float(*o) : v[k]);
+    } else {
+      float* o = static_cast<float*>(p.out) + at + k;
+      *o = p.accumulate ? v[k] + *o : v[k];
+    }
+  }
+}
+
+template <int kMode>
+__global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_constant__ ExpertArgs p,
+                                                             const __grid_constant__ Maps maps) {
+  constexpr bool kWgrad = kMode == kExpertWeightGrad;
+  constexpr bool kAmn = kMode != kExpertForward;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ int32_t start[MFSDP_MAX_EXPERTS + 1];      // first token of each group, clamped
+  __shared__ int32_t first[MFSDP_MAX_EXPERTS + 1];      // first tile of each expert (forward products)
+  __shared__ int32_t widest;                            // columns of the launch's widest tile
+  __shared__ __align__(8) uint64_t full_bar[kMaxStages];    // even CTA: both CTAs' operands have landed
+  __shared__ __align__(8) uint64_t empty_bar[kMaxStages];
+  __shared__ __align__(8) uint64_t tail_bar[kMaxStages];    // this CTA's operands of a group's ragged end
+  __shared__ __align__(8) uint64_t fixed_bar[kMaxStages];   // even CTA: both CTAs have zeroed past the end
+  __shared__ __align__(8) uint64_t tfull_bar[2], tempty_bar[2], drain_bar;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = ptx::cluster_ctarank();
+  const uint32_t smem_base = (ptx::smem_u32(smem_raw) + 1023u) & ~1023u;
+  const int n_rows = (int)p.n_rows;
+
+  Shape sh;
+  sh.m = (int)(kMode == kExpertInputGrad ? p.cols : p.rows);
+  sh.tiles_m = ceil_div(sh.m, kPairM);
+  sh.n = (int)p.cols;
+  sh.tiles_n = ceil_div(sh.n, kMaxN);
+  sh.width_n = even_width(sh.n, sh.tiles_n);
+
+  for (int i = threadIdx.x; i <= p.n_experts; i += kThreads) {
+    const int s = i == 0 ? 0 : p.starts[i];
+    start[i] = min(max(s, 0), n_rows);
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc_pair(ptx::smem_u32(&tmem_slot), kTmemCols);
+    ptx::tmem_relinquish_pair();
+  }
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kMaxStages; ++s) {
+      ptx::mbar_init(ptx::smem_u32(&full_bar[s]), 1);
+      ptx::mbar_init(ptx::smem_u32(&empty_bar[s]), 1);
+      ptx::mbar_init(ptx::smem_u32(&tail_bar[s]), 1);
+      ptx::mbar_init(ptx::smem_u32(&fixed_bar[s]), 2);
+    }
+    for (int a = 0; a < 2; ++a) {
+      ptx::mbar_init(ptx::smem_u32(&tfull_bar[a]), 1);
+      ptx::mbar_init(ptx::smem_u32(&tempty_bar[a]), 2 * kEpiWarps);
+    }
+    ptx::mbar_init(ptx::smem_u32(&drain_bar), 1);
+    abort_flag = 0;
+    // No wait of this launch can have run out yet (2 s at least), so nothing
+    // recorded is lost here.
+    if (blockIdx.x == 0) *p.status = 0;
+    ptx::fence_barrier_init();
+    ptx::fence_proxy_async_smem();
+  }
+  __syncthreads();
+  if (warp == 0 && !kWgrad) {
+    // tiles before each expert, and the widest tile
+    int base = 0, wide = kStepN;
+    for (int e0 = 0; e0 < p.n_experts; e0 += 32) {
+      const int e = e0 + lane;
+      const int len = e < p.n_experts ? max(0, start[e + 1] - start[e]) : 0;
+      const int nt = ceil_div(len, kMaxN);
+      if (nt) wide = max(wide, even_width(len, nt));
+      int sum = nt * sh.tiles_m;
+      const int own = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += v;
+      }
+      if (e < p.n_experts) first[e] = base + sum - own;
+      base += __shfl_sync(0xffffffffu, sum, 31);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) wide = max(wide, __shfl_xor_sync(0xffffffffu, wide, o));
+    if (lane == 0) {
+      first[p.n_experts] = base;
+      widest = wide;
+    }
+  }
+  ptx::tc_fence_before();
+  ptx::cluster_sync();
+  ptx::tc_fence_after();
+  const uint32_t tmem_base = tmem_slot;
+  const Abort ab{&abort_flag, p.status, p.wait_limit_ns};
+  const int n_tiles = kWgrad ? p.n_experts * sh.tiles_m * sh.tiles_n : first[p.n_experts];
+  const int pair0 = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  // Shared memory of a stage: A, then this CTA's half of B.
+  const int wide = kWgrad ? sh.width_n : widest;
+  const int bytes_b_max = kWgrad ? ceil_div(wide / 2, 64) * kMnBlock : (wide / 2 > 96 ? 128 : ceil_div(wide / 2, 32) * 32) * 128;
+  const uint32_t stage_bytes = kBytesA + bytes_b_max;
+  const int stages = min(kMaxStages, kSmemStages / (int)stage_bytes);
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ------------------------------------------------------------ producer
+      if (n_rows > 0) {
+        ptx::prefetch_tensormap(&maps.a);
+        ptx::prefetch_tensormap(&maps.b);
+      }
+      uint32_t s = 0, use = 0;
+      bool ok = true;
+      for (int t = pair0; t < n_tiles && ok; t += pairs) {
+        const Tile tl = decode<kMode>(p, sh, start, first, t);
+        const int blocks = ceil_div(tl.k_len, kBlockK);
+        const int nh = tl.n_mma >> 1;                         // this CTA's columns of B
+        const int mc = tl.m0 + (int)rank * kCtaM;
+        // rows wholly past the matrix are not loaded (their output is not stored)
+        const bool a_in = mc < sh.m;
+        const int copies_b = kWgrad ? ceil_div(nh, 64) : (nh > 96 ? 1 : ceil_div(nh, 32));
+        const uint32_t bytes_b = kWgrad ? copies_b * kMnBlock : (nh > 96 ? 128u : 32u * copies_b) * 128u;
+        const uint32_t own_bytes = (a_in ? kBytesA : 0) + bytes_b;
+        const uint32_t pair_bytes = (tl.m0 + kCtaM < sh.m ? 2u : 1u) * kBytesA + 2u * bytes_b;
+        const bool ragged = kWgrad && (tl.k_len & 15) != 0;   // the last block needs its end zeroed
+        for (int kb = 0; kb < blocks; ++kb) {
+          ok = wait_bar<false>(ptx::smem_u32(&empty_bar[s]), (use & 1) ^ 1, ab, kRoleStage);
+          if (!ok) break;
+          const uint32_t full = ptx::smem_u32(&full_bar[s]);
+          uint32_t bar = ptx::mapa_shared(full, 0);
+          if (ragged && kb == blocks - 1) {
+            // lands on this CTA's own barrier, for its zeroing warp
+            bar = ptx::mapa_shared(ptx::smem_u32(&tail_bar[s]), rank);
+            ptx::mbar_arrive_expect_tx(ptx::smem_u32(&tail_bar[s]), own_bytes);
+            if (rank == 0) ptx::mbar_arrive(full);
+          } else if (rank == 0) {
+            ptx::mbar_arrive_expect_tx(full, pair_bytes);
           }
-        if (r < height && c < width) {
-          if (p.mode == kExpertWeightGrad) put(p, e * p.out_stride + r * p.out_ld + c, acc);
-          else put(p, (lo + r) * p.out_ld + c, acc);
+          const uint32_t sa = smem_base + s * stage_bytes, sb = sa + kBytesA;
+          const int k0 = kb * kBlockK;
+          if (a_in) {
+            if (!kAmn) {
+              ptx::tma_load_3d_pair(sa, &maps.a, k0, mc, tl.e, bar);
+            } else {
+              const int y = kWgrad ? tl.group + k0 : k0, z = kWgrad ? 0 : tl.e;
+              ptx::tma_load_3d_pair(sa, &maps.a, mc, y, z, bar);
+              ptx::tma_load_3d_pair(sa + kMnBlock, &maps.a, mc + 64, y, z, bar);
+            }
+          }
+          const int nc = tl.n0 + (int)rank * nh;
+          if (kWgrad) {
+            for (int j = 0; j < copies_b; ++j)
+              ptx::tma_load_3d_pair(sb + j * kMnBlock, &maps.b, nc + 64 * j, tl.group + k0, 0, bar);
+          } else if (nh > 96) {
+            ptx::tma_load_3d_pair(sb, &maps.b128, k0, tl.group + nc, 0, bar);
+          } else {
+            for (int j = 0; j < copies_b; ++j)
+              ptx::tma_load_3d_pair(sb + j * 4096, &maps.b, k0, tl.group + nc + 32 * j, 0, bar);
+          }
+          if (++s == (uint32_t)stages) { s = 0; ++use; }
         }
       }
+      // Drain: every stage this CTA filled has been read, so no copy into its
+      // shared memory is in flight (bounded).
+      for (int i = 0; i < stages; ++i) {
+        if (use > 0 || s > 0) {
+          const uint32_t last = s == 0 ? stages - 1 : s - 1, luse = s == 0 ? use - 1 : use;
+          if (!ptx::mbar_wait(ptx::smem_u32(&empty_bar[last]), luse & 1, kDrainNs)) break;
+          s = last;
+          use = luse;
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      // --------------------------------------------------------- MMA issuer
+      uint32_t s = 0, use = 0, acc_it = 0, fix_use = 0;
+      bool ok = true;
+      for (int t = pair0; t < n_tiles && ok; t += pairs) {
+        const Tile tl = decode<kMode>(p, sh, start, first, t);
+        const int blocks = ceil_div(tl.k_len, kBlockK);
+        if (blocks == 0) continue;
+        const bool ragged = kWgrad && (tl.k_len & 15) != 0;
+        const uint32_t a = acc_it & 1;
+        ok = wait_bar<true>(ptx::smem_u32(&tempty_bar[a]), ((acc_it >> 1) & 1) ^ 1, ab, kRoleAccFree);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        const uint32_t d_tmem = tmem_base + a * kAccCols;
+        const uint32_t idesc = ptx::idesc_bf16_f32(kPairM, (uint32_t)tl.n_mma, kWgrad ? 1u : 0u, kAmn ? 1u : 0u);
+        for (int kb = 0; kb < blocks; ++kb) {
+          ok = wait_bar<true>(ptx::smem_u32(&full_bar[s]), use & 1, ab, kRoleOperands);
+          if (ok && ragged && kb == blocks - 1) {
+            ok = wait_bar<true>(ptx::smem_u32(&fixed_bar[s]), (fix_use >> s) & 1, ab, kRoleTail);
+            fix_use ^= 1u << s;
+          }
+          if (!ok) break;
+          ptx::tc_fence_after();
+          const uint32_t sa = smem_base + s * stage_bytes, sb = sa + kBytesA;
+          const int steps = min(kBlockK / 16, ceil_div(tl.k_len - kb * kBlockK, 16));
+          for (int k = 0; k < steps; ++k) {
+            // K-major: 16 elements (32 bytes) along the swizzle row, 8-row groups
+            // 1 KB apart.  MN-major: 16 K rows (2 KB), 64-element blocks 8 KB
+            // apart (leading offset), 8-row K groups 1 KB apart (stride offset).
+            const uint64_t adesc = kAmn ? ptx::smem_desc_sw128(sa + k * 2048, kMnBlock, 1024)
+                                        : ptx::smem_desc_sw128(sa + k * 32, 16, 1024);
+            const uint64_t bdesc = kWgrad ? ptx::smem_desc_sw128(sb + k * 2048, kMnBlock, 1024)
+                                          : ptx::smem_desc_sw128(sb + k * 32, 16, 1024);
+            ptx::umma_bf16_pair(d_tmem, adesc, bdesc, idesc, kb > 0 || k > 0 ? 1u : 0u);
+          }
+          ptx::umma_commit_pair_multicast(ptx::smem_u32(&empty_bar[s]), 0x3);
+          if (++s == (uint32_t)stages) { s = 0; ++use; }
+        }
+        if (!ok) break;
+        ptx::umma_commit_pair_multicast(ptx::smem_u32(&tfull_bar[a]), 0x3);
+        ++acc_it;
+      }
+      // every MMA issued has completed before TMEM is released
+      ptx::umma_commit_pair_multicast(ptx::smem_u32(&drain_bar), 0x1);
+      ptx::mbar_wait(ptx::smem_u32(&drain_bar), 0, kDrainNs);
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    // ---------------------------------------------- zeroing of group ends
+    // The last block of a group whose length is no multiple of 16 holds, after
+    // its own tokens, the next group's: the MMA stops at the next multiple of
+    // 16, and the rows up to there are zeroed in both operands (not in one: a
+    // NaN of the other would survive a product with zero).
+    if (kWgrad) {
+      uint32_t s = 0, tail_use = 0;
+      bool ok = true;
+      for (int t = pair0; t < n_tiles && ok; t += pairs) {
+        const Tile tl = decode<kMode>(p, sh, start, first, t);
+        const int blocks = ceil_div(tl.k_len, kBlockK);
+        if (blocks == 0) continue;
+        const uint32_t st = (s + blocks - 1) % stages;
+        s = (s + blocks) % stages;
+        if ((tl.k_len & 15) == 0) continue;
+        ok = __all_sync(0xffffffffu, wait_bar<false>(ptx::smem_u32(&tail_bar[st]), (tail_use >> st) & 1, ab, kRoleTail));
+        if (!ok) break;
+        tail_use ^= 1u << st;
+        const int valid = tl.k_len - (blocks - 1) * kBlockK, pad = (16 - (valid & 15)) & 15;
+        uint8_t* base = smem_raw + (smem_base - ptx::smem_u32(smem_raw)) + (size_t)st * stage_bytes;
+        const int mn_blocks = 2 + ceil_div(tl.n_mma >> 1, 64);     // A's two, then B's
+        for (int i = lane; i < mn_blocks * pad * 8; i += 32) {
+          const int blk = i / (pad * 8), r = i - blk * pad * 8;
+          *reinterpret_cast<uint4*>(base + (size_t)blk * kMnBlock + (valid + (r >> 3)) * 128 + (r & 7) * 16) =
+              make_uint4(0, 0, 0, 0);
+        }
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_u32(&fixed_bar[st]), 0));
+      }
+    }
+  } else if (warp >= kFirstEpiWarp) {
+    // -------------------------------------------------------------- epilogue
+    // Warp w reads TMEM lane quadrant w % 4; the two warps of a quadrant take
+    // alternate chunks of 32 columns.
+    const int quad = warp & 3, half = (warp - kFirstEpiWarp) >> 2;
+    uint32_t acc_it = 0;
+    for (int t = pair0; t < n_tiles; t += pairs) {
+      const Tile tl = decode<kMode>(p, sh, start, first, t);
+      const int m = tl.m0 + (int)rank * kCtaM + quad * 32 + lane;
+      if (kWgrad && tl.k_len == 0) {
+        if (!p.accumulate && m < sh.m) {
+          float z[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) z[j] = 0.f;
+          for (int c = 32 * half; c < tl.n; c += 64)
+            store_row(p, tl.e * p.out_stride + m * p.out_ld + tl.n0 + c, min(32, tl.n - c), z);
+        }
+        continue;
+      }
+      const uint32_t a = acc_it & 1;
+      if (!__all_sync(0xffffffffu, wait_bar<false>(ptx::smem_u32(&tfull_bar[a]), (acc_it >> 1) & 1, ab, kRoleAccFull)))
+        break;
+      ptx::tc_fence_after();
+      const uint32_t t_row = tmem_base + a * kAccCols + ((uint32_t)(quad * 32) << 16);
+      for (int c = 32 * half; c < tl.n_mma; c += 64) {
+        uint32_t r[32];
+        __syncwarp();
+        ptx::tmem_ld_32x32b_x32(t_row + (uint32_t)c, r);
+        ptx::tmem_ld_wait();
+        if (c + 64 >= tl.n_mma) {
+          // this warp's last read of the accumulator: hand it back
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive_signal(ptx::mapa_shared(ptx::smem_u32(&tempty_bar[a]), 0));
+        }
+        if (m >= sh.m) continue;                  // the warp meets again at the next chunk
+        const int cnt = min(32, tl.n - c);
+        if (kWgrad) {
+          float v[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+          store_row(p, tl.e * p.out_stride + m * p.out_ld + tl.n0 + c, cnt, v);
+        } else {
+          // lanes are neighbours in memory: 64 (bf16) or 128 bytes a token
+          const int64_t at = (int64_t)(tl.group + tl.n0 + c) * p.out_ld + m;
+          if (p.out_bf16) {
+            __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + at;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (j < cnt) o[j * p.out_ld] = __float2bfloat16_rn(__uint_as_float(r[j]));
+          } else {
+            float* o = static_cast<float*>(p.out) + at;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (j < cnt) o[j * p.out_ld] = __uint_as_float(r[j]);
+          }
+        }
+      }
+      if (32 * half >= tl.n_mma) {
+        // no chunk for this warp
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive_signal(ptx::mapa_shared(ptx::smem_u32(&tempty_bar[a]), 0));
+      }
+      ++acc_it;
+    }
+    if (!kWgrad) {
+      // rows of no expert
+      const int64_t lo = start[p.n_experts], width = sh.m;
+      const int64_t step = (int64_t)gridDim.x * (32 * kEpiWarps);
+      for (int64_t i = (int64_t)blockIdx.x * (32 * kEpiWarps) + threadIdx.x - 32 * kFirstEpiWarp;
+           i < (n_rows - lo) * width; i += step) {
+        const int64_t at = (lo + i / width) * p.out_ld + i % width;
+        if (p.out_bf16) static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(0.f);
+        else static_cast<float*>(p.out)[at] = 0.f;
+      }
+    }
   }
+
+  // No CTA of the pair leaves, or frees TMEM, while its peer may still arrive
+  // on its barriers.
+  __syncwarp();
+  ptx::tc_fence_before();
+  ptx::cluster_sync();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc_pair(tmem_base, kTmemCols);
+  }
+}
+
+// Rows of `width` elements, ld apart, into rows of `width8` (width rounded up
+// to 8, zero-filled): the form whose rows start on 16-byte boundaries.  With
+// `starts`, matrix e (its `rows` rows) is copied only if its group has a token.
+__global__ void __launch_bounds__(256) pack_kernel(const uint16_t* src, int64_t stride, int64_t ld, uint16_t* dst,
+                                                   int64_t rows, int width, int width8, const int32_t* starts) {
+  if (starts && starts[blockIdx.y + 1] <= (blockIdx.y ? starts[blockIdx.y] : 0)) return;
+  const int per = width8 >> 3;
+  src += blockIdx.y * stride;
+  dst += (int64_t)blockIdx.y * rows * width8;
+  const int64_t total = rows * per;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / per;
+    const int c = (int)(i - r * per) * 8;
+    const uint16_t* s = src + r * ld + c;
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t lo = c + 2 * k < width ? s[2 * k] : 0, hi = c + 2 * k + 1 < width ? s[2 * k + 1] : 0;
+      w[k] = lo | (hi << 16);
+    }
+    *reinterpret_cast<uint4*>(dst + r * width8 + c) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static EncodeTiledFn fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<EncodeTiledFn>(f);
+  }();
+  return fn;
+}
+
+// A stack of n matrices (width x height, rows ld apart, matrices `stride`
+// apart) in boxes of 64 x box_rows x 1.
+bool encode(CUtensorMap* map, const void* base, int64_t width, int64_t height, int64_t ld, int64_t n, int64_t stride,
+            int box_rows) {
+  const EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)height, (cuuint64_t)n};
+  const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)stride * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
+  const cuuint32_t one[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, one,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr size_t kSmemBytes = kSmemStages + 1024;
+
+template <int kMode>
+cudaError_t launch_mode(const ExpertArgs& a, const Maps& maps, int64_t max_tiles, cudaStream_t s) {
+  constexpr int kMaxDevices = 64;
+  static std::mutex mu;
+  static int resident[kMaxDevices] = {};      // CTA pairs on the device at once
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 2;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int pairs = 0;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (resident[dev] == 0) {
+      e = cudaFuncSetAttribute(expert_kernel<kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+      if (e != cudaSuccess) return e;
+      cfg.gridDim = dim3((unsigned)(2 * (sm_count() / 2)), 1, 1);
+      int n = 0;
+      e = cudaOccupancyMaxActiveClusters(&n, expert_kernel<kMode>, &cfg);
+      if (e != cudaSuccess) return e;
+      if (n < 1) return cudaErrorInvalidConfiguration;
+      resident[dev] = n;
+    }
+    pairs = resident[dev];
+  }
+  cfg.stream = s;
+  cfg.gridDim = dim3((unsigned)(2 * std::max<int64_t>(1, std::min<int64_t>(pairs, max_tiles))), 1, 1);
+  e = cudaLaunchKernelEx(&cfg, expert_kernel<kMode>, a, maps);
+  return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+int64_t up8(int64_t x) { return (x + 7) / 8 * 8; }
+
+cudaError_t pack(const void* src, int64_t stride, int64_t ld, void* dst, int64_t rows, int64_t width, int n,
+                 const int32_t* starts, cudaStream_t s) {
+  const int64_t blocks = std::min<int64_t>((rows * (up8(width) / 8) + 255) / 256, (int64_t)sm_count() * 8);
+  pack_kernel<<<dim3((unsigned)blocks, (unsigned)n), 256, 0, s>>>(static_cast<const uint16_t*>(src), stride, ld,
+                                                                  static_cast<uint16_t*>(dst), rows, (int)width,
+                                                                  (int)up8(width), starts);
+  return cudaGetLastError();
+}
+
+// Activations n x width, ld apart, ready for the tensor copies: in place when
+// every row starts on a 16-byte boundary (a single row always does), else
+// packed at *at.
+cudaError_t aligned_rows(const void** x, int64_t* ld, int64_t n, int64_t width, uint8_t** at, cudaStream_t s) {
+  if (n <= 1) {
+    *ld = up8(width);
+    return cudaSuccess;
+  }
+  if (*ld % 8 == 0) return cudaSuccess;
+  const cudaError_t e = pack(*x, 0, *ld, *at, n, width, 1, nullptr, s);
+  *x = *at;
+  *ld = up8(width);
+  *at += packed_bytes(n, width);
+  return e;
 }
 
 }  // namespace
 
-cudaError_t launch_expert(const ExpertArgs& a, cudaStream_t s) {
-  const int64_t width = a.mode == kExpertForward ? a.rows : a.cols;
-  const int64_t height = a.mode == kExpertWeightGrad ? a.rows : a.n_rows;
-  const unsigned z = (unsigned)(a.mode == kExpertWeightGrad ? a.n_experts : a.n_experts + 1);
-  const unsigned x = (unsigned)std::min<int64_t>((width + kT - 1) / kT, 64);
-  const unsigned y = (unsigned)std::max<int64_t>(1, std::min<int64_t>((height + kT - 1) / kT, 16));
-  expert_kernel<<<dim3(x, y, z), kT * kT, 0, s>>>(a);
-  return cudaGetLastError();
+cudaError_t launch_expert(const ExpertArgs& in, cudaStream_t s) {
+  ExpertArgs a = in;
+  const int64_t n = a.n_rows, mt = ((a.mode == kExpertInputGrad ? a.cols : a.rows) + kPairM - 1) / kPairM;
+  uint8_t* at = a.packs;
+  Maps maps;
+  cudaError_t e;
+  bool ok;
+  // The longest wait is the epilogue's for a tile's whole contraction: 2 s, and
+  // 64 ns for each of its K (8 clocks at the MMA's rate, at 1 GHz, 8 times over).
+  const int64_t k_max = a.mode == kExpertWeightGrad ? n : (a.mode == kExpertForward ? a.cols : a.rows);
+  a.wait_limit_ns = 2000000000ull + 64ull * (uint64_t)k_max;
+  if (a.mode == kExpertWeightGrad) {
+    if (n > 0) {
+      e = aligned_rows(&a.a, &a.a_ld, n, a.rows, &at, s);
+      if (e != cudaSuccess) return e;
+      e = aligned_rows(&a.b, &a.b_ld, n, a.cols, &at, s);
+      if (e != cudaSuccess) return e;
+      ok = encode(&maps.a, a.a, a.rows, n, a.a_ld, 1, n * a.a_ld, 64) &&
+           encode(&maps.b, a.b, a.cols, n, a.b_ld, 1, n * a.b_ld, 64);
+      if (!ok) return cudaErrorInvalidValue;
+      maps.b128 = maps.b;
+    } else {
+      maps = Maps{};       // no tile has a contraction: no copy is issued
+    }
+    const int64_t esz = a.out_bf16 ? 2 : 4;
+    a.out_vec = aligned(a.out, 32) && a.cols * esz % 32 == 0 && a.out_stride * esz % 32 == 0;
+    const int64_t nt = (a.cols + kMaxN - 1) / kMaxN;
+    return launch_mode<kExpertWeightGrad>(a, maps, a.n_experts * mt * nt, s);
+  }
+  const int64_t k = a.mode == kExpertForward ? a.cols : a.rows;
+  if (a.cols % 8 != 0 || (a.n_experts > 1 && a.b_stride % 8 != 0)) {
+    e = pack(a.b, a.b_stride, a.b_ld, at, a.rows, a.cols, a.n_experts, a.starts, s);
+    if (e != cudaSuccess) return e;
+    a.b = at;
+    a.b_ld = up8(a.cols);
+    a.b_stride = a.rows * a.b_ld;
+    at += packed_bytes(a.n_experts * a.rows, a.cols);
+  }
+  e = aligned_rows(&a.a, &a.a_ld, n, k, &at, s);
+  if (e != cudaSuccess) return e;
+  const int64_t w_stride = a.n_experts > 1 ? a.b_stride : a.rows * a.b_ld;
+  ok = encode(&maps.a, a.b, a.cols, a.rows, a.b_ld, a.n_experts, w_stride, a.mode == kExpertForward ? 128 : 64) &&
+       encode(&maps.b, a.a, k, n, a.a_ld, 1, n * a.a_ld, 32) &&
+       encode(&maps.b128, a.a, k, n, a.a_ld, 1, n * a.a_ld, 128);
+  if (!ok) return cudaErrorInvalidValue;
+  const int64_t tiles = mt * (n / kMaxN + std::min<int64_t>(a.n_experts, n));
+  return a.mode == kExpertForward ? launch_mode<kExpertForward>(a, maps, tiles, s)
+                                  : launch_mode<kExpertInputGrad>(a, maps, tiles, s);
 }
 
 }  // namespace ops

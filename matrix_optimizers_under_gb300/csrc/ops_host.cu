@@ -223,6 +223,9 @@ int check_expert_shape(int32_t n_experts, int64_t n_rows, int64_t rows, int64_t 
   if (n_experts < 1 || n_rows < 0 || rows < 1 || cols < 1) return MFSDP_ERR_INVALID_ARG;
   if (n_experts > MFSDP_MAX_EXPERTS || n_rows > (1 << 30) || rows > (1 << 24) || cols > (1 << 24))
     return MFSDP_ERR_UNSUPPORTED_SHAPE;
+  // the kernels count 256 x 256 tiles in int32, in each of the three products
+  const int64_t tr = (rows + 255) / 256, tc = (cols + 255) / 256, tn = n_rows / 256 + n_experts;
+  if (std::max(n_experts * tr * tc, std::max(tr, tc) * tn) > (1 << 30)) return MFSDP_ERR_UNSUPPORTED_SHAPE;
   return MFSDP_OK;
 }
 
@@ -408,7 +411,15 @@ extern "C" size_t mfsdp_expert_workspace_bytes(int32_t n_experts, int64_t n_rows
       stack_extent(n_experts, w_stride, rows, cols) == 0 || !rows_fit(n_rows, rows_ld, rows) ||
       !rows_fit(n_rows, cols_ld, cols))
     return 0;
-  return 256;
+  size_t bytes = 256;                                       // the status word
+  if (cols % 8 != 0 || (n_experts > 1 && w_stride % 8 != 0)) bytes += packed_bytes(n_experts * rows, cols);
+  if (n_rows > 1 && rows_ld % 8 != 0) bytes += packed_bytes(n_rows, rows);
+  if (n_rows > 1 && cols_ld % 8 != 0) bytes += packed_bytes(n_rows, cols);
+  return bytes;
+}
+
+extern "C" int mfsdp_expert_device_status(const void* workspace, void* stream, int32_t* detail) {
+  return mfsdp_muon_device_status(workspace, stream, detail);
 }
 
 extern "C" int mfsdp_expert_matmul(const void* x, int64_t x_ld, const void* w, int64_t w_stride, int32_t in_dtype,
@@ -450,6 +461,7 @@ extern "C" int mfsdp_expert_matmul(const void* x, int64_t x_ld, const void* w, i
   a.out_ld = y_ld;
   a.out_bf16 = y_dtype == MFSDP_DTYPE_BF16;
   a.status = static_cast<int32_t*>(workspace);
+  a.packs = static_cast<uint8_t*>(workspace) + 256;
   const OpRange range(input_grad ? "mfsdp expert input gradient" : "mfsdp expert matmul");
   return cuda_status(launch_expert(a, static_cast<cudaStream_t>(stream)));
 }
@@ -494,6 +506,7 @@ extern "C" int mfsdp_expert_weight_grad(const void* dy, int64_t dy_ld, const voi
   a.out_bf16 = dw_dtype == MFSDP_DTYPE_BF16;
   a.accumulate = accumulate;
   a.status = static_cast<int32_t*>(workspace);
+  a.packs = static_cast<uint8_t*>(workspace) + 256;
   const OpRange range("mfsdp expert weight gradient");
   return cuda_status(launch_expert(a, static_cast<cudaStream_t>(stream)));
 }

@@ -1,0 +1,39 @@
+// Inline-PTX wrappers of the operators next to the owner step, beside those
+// of ptx.cuh.
+#pragma once
+
+#include <cstdint>
+
+#include "ptx.cuh"
+
+namespace mfsdp {
+namespace ptx {
+
+// 3-D tensor copy global -> shared for a CTA pair: lands in this CTA's shared
+// memory at `dst` and completes its bytes on the mbarrier at `bar` (a
+// shared::cluster address, this CTA's or the peer's).  The box's first
+// coordinate must be 16-byte aligned.
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const void* tmap, int32_t x, int32_t y, int32_t z,
+                                                 uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+
+// 32-byte global store (the address 32-byte aligned).
+__device__ __forceinline__ void st_v8(void* p, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+__device__ __forceinline__ void ld_v8(const void* p, uint32_t (&v)[8]) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+               : "l"(p)
+               : "memory");
+}
+
+}  // namespace ptx
+}  // namespace mfsdp
