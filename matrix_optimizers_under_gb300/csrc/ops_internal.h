@@ -87,11 +87,13 @@ struct EmbedGradArgs {
   void* grad;
   const int32_t* keys;   // sorted
   const int32_t* order;
-  float* partials;       // two rows of `dim` floats per slab (below)
+  float* partials;       // embed_grad_partial_bytes(n, vocab, dim)
   int64_t n, vocab, dim, dout_ld, grad_ld;
   int32_t dout_bf16, grad_bf16, accumulate;
   float scale;
 };
+// Slabs the embedding gradient's work is cut into, about (8 CTAs an SM).
+constexpr int kSlabTarget = 1216;
 size_t embed_grad_partial_bytes(int64_t n, int64_t vocab, int64_t dim);
 cudaError_t launch_embed_grad(const EmbedGradArgs& a, cudaStream_t s);
 
