@@ -155,16 +155,17 @@ SlabPlan plan_slabs(int64_t n, int64_t vocab) {
   return s;
 }
 
-struct SlabInfo {
-  int32_t row;         // the row cut by earlier slab ends that ends in this slab, or -1
-  int32_t first;       // the slab it starts in
+// A row cut by slab ends: the slabs its positions start and end in.
+struct CutRow {
+  int32_t row, first, last;
 };
 
 struct GradKernelArgs {
   EmbedGradArgs a;
   int64_t slab;
   int64_t part_ld;     // floats of a partial row
-  SlabInfo* info;      // one a slab
+  int32_t* n_cut;      // how many `cut` holds (zeroed by the sort)
+  CutRow* cut;         // in no fixed order: each is added by itself
   float* parts;        // two rows a slab: [0] the row cut at its start, [1] the row cut at its end
 };
 
@@ -213,13 +214,14 @@ template <bool kInBf16, bool kOutBf16, bool kVec>
 __global__ void __launch_bounds__(kMaxThreads) embed_grad_kernel(const __grid_constant__ GradKernelArgs p) {
   __shared__ int32_t keys[kStage], order[kStage];
   __shared__ int64_t split[2];
-  constexpr int kBatch = kInBf16 ? 8 : 4;              // positions in flight
+  constexpr int kBatch = kInBf16 && kVec ? 8 : 4;      // positions in flight
   const EmbedGradArgs& a = p.a;
   const int tid = threadIdx.x, threads = blockDim.x;
   const int64_t c0 = (int64_t)blockIdx.y * threads * kCols;
   const int cols = (int)min((int64_t)threads * kCols, a.dim - c0);
   const int64_t s = blockIdx.x;
   const int64_t d0 = s * p.slab, d1 = min(d0 + p.slab, a.n + a.vocab);
+  ptx::wait_dependencies();
   if (tid < 32) {
     int64_t v0, v1;
     merge_search(a.keys, a.n, a.vocab, d0, d1, v0, v1);
@@ -229,26 +231,23 @@ __global__ void __launch_bounds__(kMaxThreads) embed_grad_kernel(const __grid_co
     }
   }
   __syncthreads();
+  ptx::launch_dependents();
   const int64_t v0 = split[0], v1 = split[1], i0 = d0 - v0, i1 = d1 - v1;
   const bool cut = v0 < a.vocab && i0 > 0 && a.keys[i0 - 1] == v0;      // row v0 starts in an earlier slab
-  if (tid < 32 && blockIdx.y == 0) {
-    // Where a row cut at the start and ended here begins: the slab of its first position.
-    int64_t first = -1;
-    if (cut && v1 > v0) {
-      int64_t lo = 0, hi = i0;                        // first position with key v0
-      while (lo < hi) {
-        const int64_t step = (hi - lo + 31) / 32, i = lo + tid * step;
-        const int cnt = __popc(__ballot_sync(0xffffffffu, i < hi && a.keys[i] < v0));
-        if (cnt == 0) {
-          hi = lo;
-        } else {
-          hi = min(hi, lo + cnt * step);
-          lo = lo + (cnt - 1) * step + 1;
-        }
+  if (tid < 32 && blockIdx.y == 0 && cut && v1 > v0) {
+    // a row cut at the start ends here: it begins in the slab of its first position
+    int64_t lo = 0, hi = i0;
+    while (lo < hi) {
+      const int64_t step = (hi - lo + 31) / 32, i = lo + tid * step;
+      const int cnt = __popc(__ballot_sync(0xffffffffu, i < hi && a.keys[i] < v0));
+      if (cnt == 0) {
+        hi = lo;
+      } else {
+        hi = min(hi, lo + cnt * step);
+        lo = lo + (cnt - 1) * step + 1;
       }
-      first = (lo + v0) / p.slab;
     }
-    if (tid == 0) p.info[s] = {first < 0 ? -1 : (int32_t)v0, (int32_t)first};
+    if (tid == 0) p.cut[atomicAdd(p.n_cut, 1)] = {(int32_t)v0, (int32_t)((lo + v0) / p.slab), (int32_t)s};
   }
 
   float acc[kCols] = {};
@@ -313,48 +312,56 @@ __global__ void __launch_bounds__(kMaxThreads) embed_grad_kernel(const __grid_co
     store8<false, kVec>(v1 == v0 && cut ? part0 : part0 + p.part_ld, 0, tid, threads, cols, acc);
 }
 
-// Adds the partial rows of a row cut by slab ends: slab `first` holds its start
-// (second row of its pair), the following slabs up to this one the rest.
+// Adds the partial rows of the rows cut by slab ends: slab `first` holds a
+// row's start (second row of its pair), the following slabs up to `last` the rest.
+// A CTA takes 128 columns of one row at a time, each warp an eighth of the
+// slabs (a token that fills the batch has one partial row in every slab).
 template <bool kOutBf16>
 __global__ void __launch_bounds__(32 * kFixParts) embed_fix_kernel(const __grid_constant__ GradKernelArgs p) {
   __shared__ float4 sum[kFixParts][32];
   const EmbedGradArgs& a = p.a;
-  const SlabInfo info = p.info[blockIdx.x];
-  if (info.row < 0) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t c = (int64_t)blockIdx.y * kFixCols + 4 * lane;
-  const int64_t first = info.first, slabs = blockIdx.x - first + 1;
-  const int64_t lo = first + slabs * warp / kFixParts, hi = first + slabs * (warp + 1) / kFixParts;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (c < p.part_ld) {
+  const int blocks = (int)((a.dim + kFixCols - 1) / kFixCols);
+  ptx::wait_dependencies();
+  const int items = *p.n_cut * blocks;
+  for (int it = blockIdx.x; it < items; it += gridDim.x) {
+    const CutRow cut = p.cut[it / blocks];
+    const int64_t c = (int64_t)(it % blocks) * kFixCols + 4 * lane;
+    const int slabs = cut.last - cut.first + 1;
+    const int lo = cut.first + (int)((int64_t)slabs * warp / kFixParts);
+    const int hi = cut.first + (int)((int64_t)slabs * (warp + 1) / kFixParts);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (c < p.part_ld) {
 #pragma unroll 8
-    for (int64_t s = lo; s < hi; ++s) {
-      const float4 x = *reinterpret_cast<const float4*>(p.parts + (2 * s + (s == first ? 1 : 0)) * p.part_ld + c);
+      for (int s = lo; s < hi; ++s) {
+        const float4 x = *reinterpret_cast<const float4*>(p.parts + (2 * (int64_t)s + (s == cut.first)) * p.part_ld + c);
+        acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
+      }
+    }
+    __syncthreads();
+    sum[warp][lane] = acc;
+    __syncthreads();
+    if (warp != 0) continue;
+#pragma unroll
+    for (int w = 1; w < kFixParts; ++w) {
+      const float4 x = sum[w][lane];
       acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
     }
-  }
-  sum[warp][lane] = acc;
-  __syncthreads();
-  if (warp != 0) return;
+    const float v[4] = {acc.x, acc.y, acc.z, acc.w};
 #pragma unroll
-  for (int w = 1; w < kFixParts; ++w) {
-    const float4 x = sum[w][lane];
-    acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
-  }
-  const float v[4] = {acc.x, acc.y, acc.z, acc.w};
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    if (c + k >= a.dim) break;
-    const int64_t at = info.row * a.grad_ld + c + k;
-    float x = v[k] * a.scale;
-    if constexpr (kOutBf16) {
-      __nv_bfloat16* g = static_cast<__nv_bfloat16*>(a.grad) + at;
-      if (a.accumulate) x += __bfloat162float(*g);
-      *g = __float2bfloat16_rn(x);
-    } else {
-      float* g = static_cast<float*>(a.grad) + at;
-      if (a.accumulate) x += *g;
-      *g = x;
+    for (int k = 0; k < 4; ++k) {
+      if (c + k >= a.dim) break;
+      const int64_t at = cut.row * a.grad_ld + c + k;
+      float x = v[k] * a.scale;
+      if constexpr (kOutBf16) {
+        __nv_bfloat16* g = static_cast<__nv_bfloat16*>(a.grad) + at;
+        if (a.accumulate) x += __bfloat162float(*g);
+        *g = __float2bfloat16_rn(x);
+      } else {
+        float* g = static_cast<float*>(a.grad) + at;
+        if (a.accumulate) x += *g;
+        *g = x;
+      }
     }
   }
 }
@@ -373,8 +380,8 @@ void lookup_launch(const LookupArgs& a, dim3 grid, dim3 block, cudaStream_t s) {
   lookup_kernel<kA, kB, kVec><<<grid, block, 0, s>>>(a);
 }
 template <bool kA, bool kB, bool kVec>
-void grad_launch(const GradKernelArgs& p, dim3 grid, int threads, cudaStream_t s) {
-  embed_grad_kernel<kA, kB, kVec><<<grid, threads, 0, s>>>(p);
+cudaError_t grad_launch(const GradKernelArgs& p, dim3 grid, int threads, cudaStream_t s) {
+  return launch_overlapped(embed_grad_kernel<kA, kB, kVec>, grid, dim3((unsigned)threads), s, p);
 }
 
 }  // namespace
@@ -395,7 +402,7 @@ cudaError_t launch_lookup(const LookupArgs& a, cudaStream_t s) {
 
 size_t embed_grad_partial_bytes(int64_t n, int64_t vocab, int64_t dim) {
   const SlabPlan sp = plan_slabs(n, vocab);
-  return round_up(sp.slabs * sizeof(SlabInfo), 256) + (size_t)sp.slabs * 2 * round_up((size_t)dim, 8) * sizeof(float);
+  return 256 + round_up(sp.slabs * sizeof(CutRow), 256) + (size_t)sp.slabs * 2 * round_up((size_t)dim, 8) * sizeof(float);
 }
 
 cudaError_t launch_embed_grad(const EmbedGradArgs& a, cudaStream_t s) {
@@ -404,8 +411,10 @@ cudaError_t launch_embed_grad(const EmbedGradArgs& a, cudaStream_t s) {
   p.a = a;
   p.slab = sp.slab;
   p.part_ld = (int64_t)round_up((size_t)a.dim, 8);
-  p.info = reinterpret_cast<SlabInfo*>(a.partials);
-  p.parts = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(a.partials) + round_up(sp.slabs * sizeof(SlabInfo), 256));
+  uint8_t* at = reinterpret_cast<uint8_t*>(a.partials);
+  p.n_cut = a.partials_count();
+  p.cut = reinterpret_cast<CutRow*>(at + 256);
+  p.parts = reinterpret_cast<float*>(at + 256 + round_up(sp.slabs * sizeof(CutRow), 256));
   const bool vec = vec_rows(a.dout, a.dout_ld, a.dim, a.dout_bf16) && vec_rows(a.grad, a.grad_ld, a.dim, a.grad_bf16);
   const int threads = threads_for(a.dim);
   const dim3 grid((unsigned)sp.slabs, (unsigned)((a.dim + threads * kCols - 1) / (threads * kCols)));
@@ -413,13 +422,11 @@ cudaError_t launch_embed_grad(const EmbedGradArgs& a, cudaStream_t s) {
                                      : (a.grad_bf16 ? grad_launch<false, true, true> : grad_launch<false, false, true>))
                       : (a.dout_bf16 ? (a.grad_bf16 ? grad_launch<true, true, false> : grad_launch<true, false, false>)
                                      : (a.grad_bf16 ? grad_launch<false, true, false> : grad_launch<false, false, false>));
-  go(p, grid, threads, s);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = go(p, grid, threads, s);
   if (e != cudaSuccess || a.n == 0) return e;
-  const dim3 fix((unsigned)sp.slabs, (unsigned)((a.dim + kFixCols - 1) / kFixCols));
-  if (a.grad_bf16) embed_fix_kernel<true><<<fix, 32 * kFixParts, 0, s>>>(p);
-  else embed_fix_kernel<false><<<fix, 32 * kFixParts, 0, s>>>(p);
-  return cudaGetLastError();
+  const int64_t items = sp.slabs * ((a.dim + kFixCols - 1) / kFixCols);      // at most
+  const dim3 fix((unsigned)std::min<int64_t>(items, 4 * std::max(1, sm_count())));
+  return launch_overlapped(a.grad_bf16 ? embed_fix_kernel<true> : embed_fix_kernel<false>, fix, dim3(32 * kFixParts), s, p);
 }
 
 }  // namespace ops

@@ -589,7 +589,6 @@ constexpr size_t kSmemBytes = kSmemStages + 1024;
 
 template <int kMode>
 cudaError_t launch_mode(const ExpertArgs& a, const Maps& maps, int64_t max_tiles, cudaStream_t s) {
-  constexpr int kMaxDevices = 64;
   static std::mutex mu;
   static int resident[kMaxDevices] = {};      // CTA pairs on the device at once
   int dev = 0;

@@ -17,7 +17,6 @@ namespace mfsdp {
 namespace ops {
 
 int sm_count() {
-  constexpr int kMaxDevices = 64;
   static std::mutex mu;
   static int sms[kMaxDevices] = {};
   int dev = 0;
@@ -398,6 +397,7 @@ extern "C" int mfsdp_embedding_grad(const void* dout, int32_t dout_dtype, int64_
   a.grad_bf16 = grad_dtype == MFSDP_DTYPE_BF16;
   a.accumulate = accumulate;
   a.scale = (float)scale;
+  s.zero = a.partials_count();
   const OpRange range("mfsdp embedding gradient");
   cudaError_t e = launch_sort(s, stream);
   if (e == cudaSuccess) e = launch_embed_grad(a, stream);

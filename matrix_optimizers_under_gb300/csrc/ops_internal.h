@@ -28,6 +28,24 @@ inline size_t dtype_size(int32_t dt) { return dt == MFSDP_DTYPE_BF16 ? 2 : 4; }
 inline size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 inline int cuda_status(cudaError_t e) { return e == cudaSuccess ? MFSDP_OK : MFSDP_ERR_CUDA; }
 
+// Launch whose prologue may overlap the end of the kernel before it in the
+// stream; it calls ptx::wait_dependencies() before it reads that one's results.
+template <typename... P, typename... A>
+cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, dim3 block, cudaStream_t s, A&&... args) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<A&&>(args)...);
+}
+
+constexpr int kMaxDevices = 64;
+
 // SM count of the current device, looked up once per device (0: no device).
 int sm_count();
 
@@ -66,6 +84,7 @@ struct SortArgs {
   int32_t* keys_out;     // sorted keys [n]
   int32_t* order_out;    // the position each came from [n]
   void* scratch;         // sort_scratch_bytes(n, n_keys)
+  int32_t* zero;         // a counter the sort sets to 0 (may be null)
 };
 size_t sort_scratch_bytes(int64_t n, int64_t n_keys);
 cudaError_t launch_sort(const SortArgs& a, cudaStream_t s);
@@ -91,6 +110,8 @@ struct EmbedGradArgs {
   int64_t n, vocab, dim, dout_ld, grad_ld;
   int32_t dout_bf16, grad_bf16, accumulate;
   float scale;
+  // Counter at the head of `partials`: the sort that runs before the gradient zeroes it.
+  int32_t* partials_count() const { return reinterpret_cast<int32_t*>(partials); }
 };
 // Slabs the embedding gradient's work is cut into, about (8 CTAs an SM).
 constexpr int kSlabTarget = 1216;

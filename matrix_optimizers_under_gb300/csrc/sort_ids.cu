@@ -2,15 +2,24 @@
 // (the embedding gradient's sums) or rows by expert (the grouped products).
 //
 // Least-significant-digit radix sort, 8 bits a pass, ceil(bits / 8) passes over
-// (key, position) pairs.  The n ids are cut into at most kMaxTiles tiles, one
-// CTA each, whose warps take consecutive runs of it, so that "earlier" is
-// (tile, warp, step, lane) order.  A pass is two launches: every tile counts
-// its digits; then every tile adds up the counts that come before it -- all
-// smaller digits of every tile, and its own digit in earlier tiles -- and
-// moves its pairs.  A pair's place among its warp's equal digits comes from a
-// warp match, so the sort is stable and its result does not depend on timing.
-// An id outside [0, n_keys) sorts as n_keys, after all valid ones.
+// (key, position) pairs.  The n ids are cut into tiles, one CTA each, whose
+// warps take consecutive runs of it, so that "earlier" is (tile, warp, step,
+// lane) order.  A pass counts every tile's digits, adds up the counts that
+// come before a tile's -- all smaller digits of every tile, and its own digit
+// in earlier tiles -- and moves the pairs.  A pair's place among its warp's
+// equal digits comes from a warp match, so the sort is stable and its result
+// does not depend on timing.  An id outside [0, n_keys) sorts as n_keys, after
+// all valid ones.
+//
+// Up to 65536 ids are sorted by one cluster of up to 8 CTAs in one launch: the
+// pairs stay in shared memory, the counts and the moves go through distributed
+// shared memory.  The work is latency, not bandwidth (32768 ids are 256 KB): two passes
+// as separate launches took 36 us with cold caches.  More ids take two launches a
+// pass, on up to kMaxTiles CTAs.
+#include <atomic>
+
 #include "ops_internal.h"
+#include "ops_ptx.cuh"
 
 namespace mfsdp {
 namespace ops {
@@ -19,6 +28,162 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kDigits = 256;
+
+// ------------------------------------------------------------- one cluster
+constexpr int kClusterThreads = 1024;
+constexpr int kClusterWarps = kClusterThreads / 32;
+constexpr int kClusterSteps = 8;                                // pairs of a thread
+constexpr int kClusterTile = kClusterThreads * kClusterSteps;   // pairs of a CTA
+constexpr int kMaxCluster = 8;
+constexpr size_t kClusterSmem = (size_t)kClusterTile * 8 + (size_t)kClusterWarps * kDigits * 4;
+
+struct ClusterArgs {
+  const void* ids;
+  int32_t ids64, n_keys, n;
+  int32_t steps;            // pairs a thread takes: the tile is 1024 steps
+  int32_t passes;
+  int32_t* keys_out;
+  int32_t* order_out;
+  int32_t* zero;
+};
+
+__global__ void __launch_bounds__(kClusterThreads, 1) sort_cluster_kernel(const __grid_constant__ ClusterArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  uint64_t* pairs = reinterpret_cast<uint64_t*>(smem);                       // (position << 32) | key
+  int (*cnt)[kDigits] = reinterpret_cast<int (*)[kDigits]>(smem + (size_t)kClusterTile * 8);
+  __shared__ int hist[kDigits];                                              // this CTA's digits
+  __shared__ int scan[kDigits / 32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = blockIdx.x, ctas = gridDim.x;                             // the grid is one cluster
+  const int tile = a.steps * kClusterThreads;
+  ptx::launch_dependents();
+  if (rank == 0 && threadIdx.x == 0 && a.zero) *a.zero = 0;
+  const int local0 = warp * a.steps * 32 + lane;                             // this thread's first pair in the tile
+  uint64_t pr[kClusterSteps];
+#pragma unroll
+  for (int k = 0; k < kClusterSteps; ++k) {
+    const int i = rank * tile + local0 + 32 * k;
+    if (k < a.steps && i < a.n) {
+      const int64_t v = a.ids64 ? static_cast<const int64_t*>(a.ids)[i] : static_cast<const int32_t*>(a.ids)[i];
+      pr[k] = ((uint64_t)(uint32_t)i << 32) | (uint32_t)(v >= 0 && v < a.n_keys ? (int)v : a.n_keys);
+    }
+  }
+  for (int pass = 0; pass < a.passes; ++pass) {
+    const int shift = 8 * pass;
+    if (pass > 0) {
+#pragma unroll
+      for (int k = 0; k < kClusterSteps; ++k)
+        if (k < a.steps && rank * tile + local0 + 32 * k < a.n) pr[k] = pairs[local0 + 32 * k];
+    }
+    for (int d = threadIdx.x; d < kClusterWarps * kDigits; d += kClusterThreads) (&cnt[0][0])[d] = 0;
+    __syncthreads();
+    int place[kClusterSteps];            // among the warp's pairs of its digit
+#pragma unroll
+    for (int k = 0; k < kClusterSteps; ++k) {
+      if (k >= a.steps) break;
+      const bool in = rank * tile + local0 + 32 * k < a.n;
+      const int digit = in ? (int)((uint32_t)pr[k] >> shift) & (kDigits - 1) : kDigits;
+      const unsigned same = __match_any_sync(0xffffffffu, digit);
+      if (in) place[k] = cnt[warp][digit] + __popc(same & ((1u << lane) - 1));
+      __syncwarp();
+      if (in && (same >> lane) == 1u) cnt[warp][digit] = place[k] + 1;
+      __syncwarp();
+    }
+    __syncthreads();
+    const int d = threadIdx.x;
+    if (d < kDigits) {
+      int s = 0;
+#pragma unroll
+      for (int w = 0; w < kClusterWarps; ++w) {
+        const int c = cnt[w][d];
+        cnt[w][d] = s;
+        s += c;
+      }
+      hist[d] = s;
+    }
+    ptx::cluster_sync();                 // every CTA's counts stand, and its pairs are in registers
+    int total = 0, before = 0, run = 0;
+    if (d < kDigits) {
+      const uint32_t mine = ptx::smem_u32(&hist[d]);
+      for (int c = 0; c < ctas; ++c) {
+        const int h = ptx::ld_shared_cluster_s32(ptx::mapa_shared(mine, (uint32_t)c));
+        total += h;
+        if (c < rank) before += h;
+      }
+      run = total;                       // inclusive scan over the digits
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, run, o);
+        if (lane >= o) run += v;
+      }
+      if (lane == 31) scan[warp] = run;
+    }
+    __syncthreads();
+    if (d < kDigits) {
+      int at = run - total + before;
+      for (int w = 0; w < warp; ++w) at += scan[w];
+#pragma unroll 8
+      for (int w = 0; w < kClusterWarps; ++w) cnt[w][d] += at;
+    }
+    __syncthreads();
+    const bool last = pass == a.passes - 1;
+#pragma unroll
+    for (int k = 0; k < kClusterSteps; ++k) {
+      if (k >= a.steps || rank * tile + local0 + 32 * k >= a.n) break;
+      const int to = cnt[warp][((uint32_t)pr[k] >> shift) & (kDigits - 1)] + place[k];
+      if (last) {
+        a.keys_out[to] = (int32_t)(uint32_t)pr[k];
+        a.order_out[to] = (int32_t)(pr[k] >> 32);
+      } else {
+        const int c = to / tile;
+        ptx::st_shared_cluster_u64(ptx::mapa_shared(ptx::smem_u32(&pairs[to - c * tile]), (uint32_t)c), pr[k]);
+      }
+    }
+    if (!last) ptx::cluster_sync();      // every pair has arrived, and no CTA still reads these counts
+  }
+  ptx::cluster_sync();                   // no CTA leaves while another reads its counts
+}
+
+cudaError_t launch_cluster(const SortArgs& s, int passes, cudaStream_t stream) {
+  static std::atomic<bool> ready[kMaxDevices];          // the kernel's shared memory is allowed, per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  if (!ready[dev].load()) {
+    e = cudaFuncSetAttribute(sort_cluster_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kClusterSmem);
+    if (e != cudaSuccess) return e;
+    ready[dev].store(true);
+  }
+  ClusterArgs a{};
+  a.ids = s.ids;
+  a.ids64 = s.ids64;
+  a.n_keys = (int32_t)s.n_keys;
+  a.n = (int32_t)s.n;
+  a.passes = passes;
+  a.keys_out = s.keys_out;
+  a.order_out = s.order_out;
+  a.zero = s.zero;
+  int ctas = 1;
+  // a CTA an SM, up to 8, before a thread takes a second pair
+  while (ctas < kMaxCluster && s.n > (int64_t)ctas * kClusterThreads) ctas *= 2;
+  a.steps = (int)((s.n + (int64_t)ctas * kClusterThreads - 1) / ((int64_t)ctas * kClusterThreads));
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = (unsigned)ctas;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(kClusterThreads);
+  cfg.dynamicSmemBytes = kClusterSmem;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, sort_cluster_kernel, a);
+}
+
+// ---------------------------------------------------------- two launches a pass
 constexpr int kMaxTiles = 256;
 constexpr int kMinSteps = 8;            // a warp's steps of 32 ids a tile, at least
 
@@ -29,7 +194,7 @@ struct SortPlan {
 };
 
 SortPlan plan_sort(int64_t n, int64_t n_keys) {
-  SortPlan p;
+  SortPlan p{};
   int bits = 0;
   while (bits < 32 && (n_keys >> bits) != 0) ++bits;     // keys are 0 .. n_keys
   p.passes = std::max(1, (bits + 7) / 8);
@@ -52,6 +217,7 @@ struct PassArgs {
   int32_t* counts;          // [tile][digit]
   int64_t n;
   int32_t tiles, steps, shift;
+  int32_t* zero;            // first pass
 };
 
 __device__ __forceinline__ int2 load_pair(const PassArgs& a, int64_t i) {
@@ -75,6 +241,7 @@ __device__ __forceinline__ void count_digits(const PassArgs& a, int (*cnt)[kDigi
 
 __global__ void __launch_bounds__(kThreads) sort_count_kernel(const __grid_constant__ PassArgs a) {
   __shared__ int cnt[kWarps][kDigits];
+  if (a.zero && blockIdx.x == 0 && threadIdx.x == 0) *a.zero = 0;
   count_digits(a, cnt);
   int s = 0;
 #pragma unroll
@@ -149,6 +316,7 @@ __global__ void __launch_bounds__(kThreads) key_starts_kernel(const int32_t* key
 }  // namespace
 
 size_t sort_scratch_bytes(int64_t n, int64_t n_keys) {
+  if (n <= kMaxCluster * kClusterTile) return 0;
   const SortPlan p = plan_sort(n, n_keys);
   return round_up((size_t)p.tiles * kDigits * 4, 256) + 2 * round_up((size_t)n * 8, 256);
 }
@@ -156,6 +324,7 @@ size_t sort_scratch_bytes(int64_t n, int64_t n_keys) {
 cudaError_t launch_sort(const SortArgs& s, cudaStream_t stream) {
   if (s.n <= 0) return cudaSuccess;
   const SortPlan p = plan_sort(s.n, s.n_keys);
+  if (s.n <= kMaxCluster * kClusterTile) return launch_cluster(s, p.passes, stream);
   uint8_t* base = static_cast<uint8_t*>(s.scratch);
   int2* buf[2];
   buf[0] = reinterpret_cast<int2*>(base + round_up((size_t)p.tiles * kDigits * 4, 256));
@@ -174,6 +343,7 @@ cudaError_t launch_sort(const SortArgs& s, cudaStream_t stream) {
     a.tiles = p.tiles;
     a.steps = p.steps;
     a.shift = 8 * k;
+    a.zero = k == 0 ? s.zero : nullptr;
     sort_count_kernel<<<p.tiles, kThreads, 0, stream>>>(a);
     sort_move_kernel<<<p.tiles, kThreads, 0, stream>>>(a);
   }
