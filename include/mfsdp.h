@@ -667,13 +667,15 @@ int mfsdp_expert_weight_grad(const void* dy, int64_t dy_ld, const void* x, int64
                              void* dw, int32_t dw_dtype, int64_t dw_stride, int32_t accumulate, void* workspace,
                              size_t workspace_bytes, void* stream);
 
-/* The status word a grouped product left in its workspace (synchronises
- * `stream`): MFSDP_OK, or MFSDP_ERR_DEVICE_TIMEOUT if one of its bounded waits
- * gave up (its outputs are then undefined); *detail (may be NULL) receives the
- * role that waited (1 a pipeline stage, 2 its operands, 3 a drained and 4 a
- * finished accumulator, 5 a group's zeroed end).  A wait gives up after 2 s plus 64 ns for each
- * element of the contraction.  Every call that launches clears the word. */
-int mfsdp_expert_device_status(const void* workspace, void* stream, int32_t* detail);
+/* The status word that a grouped product or an embedding gradient left in its
+ * workspace (synchronises `stream`): MFSDP_OK, or MFSDP_ERR_DEVICE_TIMEOUT if
+ * one of its bounded waits gave up (its outputs are then undefined); *detail (may
+ * be NULL) receives the role that waited.  Products: 1 a pipeline stage, 2 its
+ * operands, 3 a drained and 4 a finished accumulator, 5 a group's zeroed end; a
+ * wait gives up after 2 s plus 64 ns for each element of the contraction.
+ * Embedding gradient: 1 a pipeline stage, 2 its rows; 2 s.  Every call that
+ * launches clears the word. */
+int mfsdp_op_device_status(const void* workspace, void* stream, int32_t* detail);
 
 /* Static description of a status code (never NULL). */
 const char* mfsdp_status_string(int status);

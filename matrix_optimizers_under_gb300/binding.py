@@ -48,7 +48,7 @@ EXPORTED = ("mfsdp_plan_owners", "mfsdp_muon_workspace_bytes", "mfsdp_muon_owner
             "mfsdp_muon_gram_space_layout", "mfsdp_grad_clip_workspace_bytes", "mfsdp_grad_norm", "mfsdp_grad_clip",
             "mfsdp_sort_ids_workspace_bytes", "mfsdp_sort_ids", "mfsdp_embedding_lookup",
             "mfsdp_embedding_grad_workspace_bytes", "mfsdp_embedding_grad", "mfsdp_expert_workspace_bytes",
-            "mfsdp_expert_matmul", "mfsdp_expert_weight_grad", "mfsdp_expert_device_status")
+            "mfsdp_expert_matmul", "mfsdp_expert_weight_grad", "mfsdp_op_device_status")
 
 SEGMENT_REDUCE = 0
 SEGMENT_GATHER = 1
@@ -559,8 +559,8 @@ _lib.mfsdp_expert_matmul.restype = ctypes.c_int
 _lib.mfsdp_expert_weight_grad.argtypes = [_vp, _i64, _vp, _i64, _i32, _vp, _i32, _i64, _i64, _i64, _vp, _i32, _i64,
                                           _i32, _vp, _sz, _vp]
 _lib.mfsdp_expert_weight_grad.restype = ctypes.c_int
-_lib.mfsdp_expert_device_status.argtypes = [_vp, _vp, ctypes.POINTER(_i32)]
-_lib.mfsdp_expert_device_status.restype = ctypes.c_int
+_lib.mfsdp_op_device_status.argtypes = [_vp, _vp, ctypes.POINTER(_i32)]
+_lib.mfsdp_op_device_status.restype = ctypes.c_int
 
 
 def _flat(t, what: str):
@@ -740,10 +740,11 @@ def expert_weight_grad(dy, x, starts, dw, workspace, *, accumulate: bool = False
                                          _stream(stream)), "expert_weight_grad")
 
 
-def expert_device_status(workspace, stream=None) -> Tuple[int, int]:
-    """(status, raw word) of the last grouped product that ran with this workspace (synchronises)."""
+def op_device_status(workspace, stream=None) -> Tuple[int, int]:
+    """(status, raw word) of the last grouped product or embedding gradient that ran with this
+    workspace (synchronises)."""
     detail = _i32(0)
-    st = _lib.mfsdp_expert_device_status(_ptr(workspace), _stream(stream), ctypes.byref(detail))
+    st = _lib.mfsdp_op_device_status(_ptr(workspace), _stream(stream), ctypes.byref(detail))
     return st, detail.value
 
 

@@ -12,16 +12,24 @@
 // a row (layouts whose rows do not start on such a boundary: 8 columns a block
 // apart, so a warp's scalar accesses are still contiguous).
 //
-// Gradient.  Positions come sorted by token (stable).  Text repeats a few tokens
-// thousands of times and leaves most of the vocabulary unnamed, so neither a
-// row nor a position is a fair share of work; the merge of both is: the list
-// in which every row's positions are followed by the row itself has vocab + n
-// entries of about one row's traffic each, and every CTA takes an equal run of
-// it (a slab), found by a search along its diagonal.  A row that lies in one slab is written there.
-// A row cut by slab ends leaves one partial row a slab in the workspace, and a
-// second kernel adds them in slab order.  The slabs depend on the sizes alone, so every
-// sum has a fixed order: no atomics, bitwise reproducible, in fp32.
+// Gradient, in three launches: the sort of positions by token (stable), the rows, and the
+// rows that the division of work cut.
+//   - Most of the vocabulary is unnamed in a batch, and its rows' zeros need no
+//     order: the second kernel starts while the sort runs (on 8 SMs, ~15 us),
+//     finds the unnamed ones among its share of the rows from the ids
+//     themselves, and writes them.
+//   - Then every CTA adds up an equal run of the sorted positions (a slab): a token may
+//     be named once or fill the batch, so rows are no fair share of work.  A row
+//     whose positions lie in one slab is written there; a row cut by slab ends leaves one partial
+//     row a slab in the workspace, and the third kernel adds them in slab
+//     order.  The slabs depend on the sizes alone, so every sum has a fixed
+//     order: no atomics on sums, bitwise reproducible, in fp32.
+//   - Rows of dout arrive in shared memory as bulk copies, an instruction a row,
+//     and a zero row leaves as one: with plain loads and stores in one kernel after the
+//     sort, the rows took 72 us for 32768 x 2048 (34 M warp instructions).
 #include <cuda_bf16.h>
+
+#include <atomic>
 
 #include "ops_internal.h"
 #include "ops_ptx.cuh"
@@ -64,6 +72,17 @@ struct Row8 {
           w[k] = kBf16 ? (uint32_t)static_cast<const uint16_t*>(base)[at + c] << 16
                        : static_cast<const uint32_t*>(base)[at + c];
       }
+    }
+  }
+  // From a row in shared memory whose first column is the block's.
+  __device__ __forceinline__ void load_shared(const uint8_t* row, int tid, int cols) {
+    static_assert(kVec, "rows in shared memory are read in vectors");
+    if (kCols * tid >= cols) return;
+    const uint4* q = reinterpret_cast<const uint4*>(row) + (kBf16 ? tid : 2 * tid);
+#pragma unroll
+    for (int k = 0; k < (kBf16 ? 1 : 2); ++k) {
+      const uint4 u = q[k];
+      w[4 * k] = u.x; w[4 * k + 1] = u.y; w[4 * k + 2] = u.z; w[4 * k + 3] = u.w;
     }
   }
   __device__ __forceinline__ void get(float (&x)[8]) const {
@@ -137,21 +156,31 @@ __global__ void __launch_bounds__(kMaxThreads) lookup_kernel(const __grid_consta
 }
 
 // -------------------------------------------------------------------- gradient
-constexpr int kStage = 256;                // positions of a slab staged at a time
+constexpr int kStage = 256;                // scalar rows: positions of a slab staged at a time
 constexpr int kFixCols = 128;              // columns of a CTA that adds partial rows
 constexpr int kFixParts = 8;               // its warps: each adds an eighth of the slabs
 
-// Slabs of the merged list of vocab rows and n positions: enough CTAs to fill
-// the GPU a few times over, at least 16 entries each.
+// Threads that cover `dim` columns, 8 each, in whole warps.
+int threads_for(int64_t dim) {
+  return (int)std::min<int64_t>(kMaxThreads, (dim + 32 * kCols - 1) / (32 * kCols) * 32);
+}
+
+// CTAs an SM holds at once: their rings share 192 KB.
+int ctas_per_sm(int64_t dim) { return std::max(2, std::min(8, 512 / threads_for(dim))); }
+
+// Equal runs of the n sorted positions, one for each CTA that the GPU holds at
+// once, at least 16 each; and the CTAs, which share the vocabulary's rows too.
 struct SlabPlan {
-  int64_t slab;        // entries of a slab
+  int64_t slab;        // positions of a slab
   int64_t slabs;
+  int64_t ctas;
 };
-SlabPlan plan_slabs(int64_t n, int64_t vocab) {
-  const int64_t units = n + vocab, want = (int64_t)kSlabTarget;
+SlabPlan plan_slabs(int64_t n, int64_t vocab, int64_t dim) {
+  const int64_t want = 152 * ctas_per_sm(dim);
   SlabPlan s;
-  s.slab = std::max<int64_t>(16, (units + want - 1) / want);
-  s.slabs = (units + s.slab - 1) / s.slab;
+  s.slab = std::max<int64_t>(16, (n + want - 1) / want);
+  s.slabs = (n + s.slab - 1) / s.slab;
+  s.ctas = std::max(s.slabs, std::min(want, (vocab + 15) / 16));
   return s;
 }
 
@@ -166,156 +195,367 @@ struct GradKernelArgs {
   int64_t part_ld;     // floats of a partial row
   int32_t* n_cut;      // how many `cut` holds (zeroed by the sort)
   CutRow* cut;         // in no fixed order: each is added by itself
-  float* parts;        // two rows a slab: [0] the row cut at its start, [1] the row cut at its end
+  int32_t* status;     // first wait that gave up (0: none)
+  int32_t batch, stages, zero_bytes;   // rows of a batch, stages of the ring, bytes before it
+  uint32_t row_slot;   // bytes of a row in the ring
+  float* parts;        // two rows a slab: [0] of the row that began before it, [1] of the row that goes on after it
 };
 
-// Rows whose own entry is among the first d of the merged list: the number of
-// v with positions(key <= v) + v + 1 <= d.  A warp narrows [lo, hi) 32 ways a
-// step; the same for d1 at once.
-__device__ __forceinline__ void merge_search(const int32_t* keys, int64_t n, int64_t vocab, int64_t d0, int64_t d1,
-                                             int64_t& v0, int64_t& v1) {
+// First sorted position whose key is not below v; the whole warp narrows
+// [0, n) 32 ways a step.
+__device__ __forceinline__ int64_t warp_lower_bound(const int32_t* keys, int64_t n, int64_t v) {
   const int lane = threadIdx.x & 31;
-  int64_t lo[2] = {max((int64_t)0, d0 - n), max((int64_t)0, d1 - n)};
-  int64_t hi[2] = {min(d0, vocab), min(d1, vocab)};       // first v not among them is in [lo, hi]
-  lo[0] = min(lo[0], hi[0]);
-  lo[1] = min(lo[1], hi[1]);
-  while (hi[0] > lo[0] || hi[1] > lo[1]) {
-    bool in[2];
-    int64_t step[2];
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const int64_t d = q ? d1 : d0;
-      step[q] = (hi[q] - lo[q] + 31) / 32;
-      const int64_t v = lo[q] + lane * step[q];
-      const int64_t i = d - v - 1;
-      in[q] = v < hi[q] && (i >= n || keys[i] > v);
-    }
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      if (hi[q] <= lo[q]) {
-        __ballot_sync(0xffffffffu, in[q]);
-        continue;
-      }
-      const int cnt = __popc(__ballot_sync(0xffffffffu, in[q]));   // probes 0 .. cnt-1 hold
-      if (cnt == 0) {
-        hi[q] = lo[q];
-      } else {
-        hi[q] = min(hi[q], lo[q] + cnt * step[q]);
-        lo[q] = lo[q] + (cnt - 1) * step[q] + 1;
-        if (lo[q] > hi[q]) lo[q] = hi[q];
-      }
+  int64_t lo = 0, hi = n;
+  while (lo < hi) {
+    const int64_t step = (hi - lo + 31) / 32, i = lo + lane * step;
+    const int below = __popc(__ballot_sync(0xffffffffu, i < hi && keys[i] < v));   // a prefix of the probes
+    if (below == 0) {
+      hi = lo;
+    } else {
+      hi = min(hi, lo + below * step);
+      lo = lo + (below - 1) * step + 1;
     }
   }
-  v0 = lo[0];
-  v1 = lo[1];
+  return lo;
 }
 
-template <bool kInBf16, bool kOutBf16, bool kVec>
-__global__ void __launch_bounds__(kMaxThreads) embed_grad_kernel(const __grid_constant__ GradKernelArgs p) {
+// Calls zero(row) for the unnamed rows of this CTA's share of the vocabulary,
+// each from one thread (or one whole warp), and waits for the sort: a short list of ids is read
+// before the wait by every CTA; a long one would take longer than the sort, so then each
+// CTA looks up its part of the sorted keys.  All threads call it.
+constexpr int kWindow = 8192;              // rows marked at a time
+constexpr int64_t kScanIds = 65536;
+
+template <bool kWarpRow, typename Zero>
+__device__ __forceinline__ void zero_unnamed(const EmbedGradArgs& a, Zero zero) {
+  __shared__ uint32_t named[kWindow / 32];
+  __shared__ int64_t range[2];
+  const int64_t share = (a.vocab + gridDim.x - 1) / gridDim.x;
+  const int64_t r0 = blockIdx.x * share, r1 = min(a.vocab, r0 + share);
+  const bool early = a.n <= kScanIds && share <= kWindow;
+  if (a.accumulate || !early) ptx::wait_dependencies();
+  if (!a.accumulate) {
+    for (int64_t w0 = r0; w0 < r1; w0 += kWindow) {
+      const int len = (int)min((int64_t)kWindow, r1 - w0);
+      __syncthreads();
+      for (int i = threadIdx.x; i < (len + 31) / 32; i += blockDim.x) named[i] = 0;
+      if (!early && threadIdx.x < 32) {
+        const int64_t lo = warp_lower_bound(a.keys, a.n, w0), hi = warp_lower_bound(a.keys, a.n, w0 + len);
+        if (threadIdx.x == 0) {
+          range[0] = lo;
+          range[1] = hi;
+        }
+      }
+      __syncthreads();
+      if (early) {
+        constexpr int kAhead = 16;
+        const int n = (int)a.n, step = blockDim.x;
+        for (int i0 = threadIdx.x; i0 < n; i0 += kAhead * step) {
+          int64_t id[kAhead];
+#pragma unroll
+          for (int k = 0; k < kAhead; ++k) {
+            const int i = i0 + k * step;
+            id[k] = -1;
+            if (i < n) id[k] = a.ids64 ? static_cast<const int64_t*>(a.ids)[i] : static_cast<const int32_t*>(a.ids)[i];
+          }
+#pragma unroll
+          for (int k = 0; k < kAhead; ++k) {
+            const uint64_t r = (uint64_t)(id[k] - w0);
+            if (r < (uint64_t)len) atomicOr(&named[r >> 5], 1u << (r & 31));
+          }
+        }
+      } else {
+        for (int64_t i = range[0] + threadIdx.x; i < range[1]; i += blockDim.x) {
+          const int r = (int)(a.keys[i] - w0);
+          atomicOr(&named[r >> 5], 1u << (r & 31));
+        }
+      }
+      __syncthreads();
+      for (int r = kWarpRow ? threadIdx.x >> 5 : threadIdx.x; r < len; r += kWarpRow ? blockDim.x >> 5 : blockDim.x)
+        if (!(named[r >> 5] >> (r & 31) & 1)) zero(w0 + r);
+    }
+  }
+  if (!a.accumulate && early) ptx::wait_dependencies();
+}
+
+// Where a slab's first and last rows reach beyond it.
+struct Slab {
+  int64_t i0, i1;      // its positions
+  bool began;          // its first row has positions in earlier slabs
+  bool goes_on;        // its last row has positions in later slabs
+};
+__device__ __forceinline__ Slab slab_of(const GradKernelArgs& p, int64_t s) {
+  const EmbedGradArgs& a = p.a;
+  Slab r;
+  r.i0 = min(s * p.slab, a.n);
+  r.i1 = min(r.i0 + p.slab, a.n);
+  r.began = r.i0 > 0 && r.i0 < a.n && a.keys[r.i0 - 1] == a.keys[r.i0];
+  r.goes_on = r.i1 > r.i0 && r.i1 < a.n && a.keys[r.i1 - 1] == a.keys[r.i1];
+  return r;
+}
+
+// Notes a row that began in an earlier slab and ends in this one (whole warp).
+__device__ __forceinline__ void note_cut(const GradKernelArgs& p, const Slab& sl, int64_t s) {
+  const EmbedGradArgs& a = p.a;
+  if (!sl.began) return;
+  const int32_t v = a.keys[sl.i0];
+  if (v >= a.vocab || (sl.goes_on && a.keys[sl.i1 - 1] == v)) return;
+  const int64_t first = warp_lower_bound(a.keys, sl.i0, v) / p.slab;
+  if ((threadIdx.x & 31) == 0) p.cut[atomicAdd(p.n_cut, 1)] = {v, (int32_t)first, (int32_t)s};
+}
+
+// A row's sum leaves the slab: into dW, or as a partial row.
+template <bool kOutBf16, bool kVec>
+__device__ __forceinline__ void put_row(const GradKernelArgs& p, const Slab& sl, int64_t s, int64_t c0, int64_t v,
+                                        bool first, bool last, int tid, int threads, int cols, float (&acc)[kCols]) {
+  const EmbedGradArgs& a = p.a;
+  const bool began = first && sl.began;
+  if (began || (last && sl.goes_on)) {
+    store8<false, kVec>(p.parts + (2 * s + (began ? 0 : 1)) * p.part_ld + c0, 0, tid, threads, cols, acc);
+    return;
+  }
+  const int64_t at = v * a.grad_ld + c0;
+  if (a.accumulate) {
+    Row8<kOutBf16, kVec> old;
+    float x[8];
+    old.load(a.grad, at, tid, threads, cols);
+    old.get(x);
+#pragma unroll
+    for (int k = 0; k < kCols; ++k) acc[k] += x[k];
+  }
+  store8<kOutBf16, kVec>(a.grad, at, tid, threads, cols, acc);
+}
+
+// Layouts whose rows do not start on vector boundaries.
+template <bool kInBf16, bool kOutBf16>
+__global__ void __launch_bounds__(kMaxThreads, 2) embed_grad_kernel(const __grid_constant__ GradKernelArgs p) {
   __shared__ int32_t keys[kStage], order[kStage];
-  __shared__ int64_t split[2];
-  constexpr int kBatch = kInBf16 && kVec ? 8 : 4;      // positions in flight
+  constexpr int kAhead = 4;                            // positions in flight
   const EmbedGradArgs& a = p.a;
   const int tid = threadIdx.x, threads = blockDim.x;
   const int64_t c0 = (int64_t)blockIdx.y * threads * kCols;
   const int cols = (int)min((int64_t)threads * kCols, a.dim - c0);
   const int64_t s = blockIdx.x;
-  const int64_t d0 = s * p.slab, d1 = min(d0 + p.slab, a.n + a.vocab);
-  ptx::wait_dependencies();
-  if (tid < 32) {
-    int64_t v0, v1;
-    merge_search(a.keys, a.n, a.vocab, d0, d1, v0, v1);
-    if (tid == 0) {
-      split[0] = v0;
-      split[1] = v1;
+  zero_unnamed<true>(a, [&](int64_t r) {
+    for (int c = tid & 31; c < cols; c += 32) {
+      const int64_t at = r * a.grad_ld + c0 + c;
+      if constexpr (kOutBf16) static_cast<uint16_t*>(a.grad)[at] = 0;
+      else static_cast<float*>(a.grad)[at] = 0.f;
     }
-  }
-  __syncthreads();
+  });
   ptx::launch_dependents();
-  const int64_t v0 = split[0], v1 = split[1], i0 = d0 - v0, i1 = d1 - v1;
-  const bool cut = v0 < a.vocab && i0 > 0 && a.keys[i0 - 1] == v0;      // row v0 starts in an earlier slab
-  if (tid < 32 && blockIdx.y == 0 && cut && v1 > v0) {
-    // a row cut at the start ends here: it begins in the slab of its first position
-    int64_t lo = 0, hi = i0;
-    while (lo < hi) {
-      const int64_t step = (hi - lo + 31) / 32, i = lo + tid * step;
-      const int cnt = __popc(__ballot_sync(0xffffffffu, i < hi && a.keys[i] < v0));
-      if (cnt == 0) {
-        hi = lo;
-      } else {
-        hi = min(hi, lo + cnt * step);
-        lo = lo + (cnt - 1) * step + 1;
-      }
-    }
-    if (tid == 0) p.cut[atomicAdd(p.n_cut, 1)] = {(int32_t)v0, (int32_t)((lo + v0) / p.slab), (int32_t)s};
-  }
+  const Slab sl = slab_of(p, s);
+  if (tid < 32 && blockIdx.y == 0) note_cut(p, sl, s);
 
   float acc[kCols] = {};
-  int64_t v = v0;
-  bool named = false;                                  // row v has a position in this slab
-  float* const part0 = p.parts + 2 * s * p.part_ld + c0;
-  // Row v is complete in this slab.
-  auto finish = [&]() {
-    if (v == v0 && cut) {
-      store8<false, kVec>(part0, 0, tid, threads, cols, acc);
-    } else if (named || !a.accumulate) {
-      const int64_t at = v * a.grad_ld + c0;
-#pragma unroll
-      for (int k = 0; k < kCols; ++k) acc[k] *= a.scale;
-      if (a.accumulate) {
-        Row8<kOutBf16, kVec> old;
-        float x[8];
-        old.load(a.grad, at, tid, threads, cols);
-        old.get(x);
-#pragma unroll
-        for (int k = 0; k < kCols; ++k) acc[k] += x[k];
-      }
-      store8<kOutBf16, kVec>(a.grad, at, tid, threads, cols, acc);
-    }
-    ++v;
-    named = false;
-#pragma unroll
-    for (int k = 0; k < kCols; ++k) acc[k] = 0.f;
-  };
-
-  for (int64_t base = i0; base < i1; base += kStage) {
-    const int cnt = (int)min((int64_t)kStage, i1 - base);
+  int64_t v = -1;
+  bool first = true;                                   // row v is the slab's first
+  for (int64_t base = sl.i0; base < sl.i1; base += kStage) {
+    const int cnt = (int)min((int64_t)kStage, sl.i1 - base);
     __syncthreads();
     for (int j = tid; j < cnt; j += threads) {
       keys[j] = a.keys[base + j];
       order[j] = a.order[base + j];
     }
     __syncthreads();
-    for (int j0 = 0; j0 < cnt; j0 += kBatch) {
-      Row8<kInBf16, kVec> row[kBatch];
+    for (int j0 = 0; j0 < cnt; j0 += kAhead) {
+      Row8<kInBf16, false> row[kAhead];
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b)
+      for (int b = 0; b < kAhead; ++b)
         if (j0 + b < cnt && keys[j0 + b] < a.vocab)
           row[b].load(a.dout, (int64_t)order[j0 + b] * a.dout_ld + c0, tid, threads, cols);
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
+      for (int b = 0; b < kAhead; ++b) {
         if (j0 + b >= cnt) break;
         const int key = keys[j0 + b];
         if (key >= a.vocab) break;                     // masked: after every row
-        while (v < key) finish();
+        if (key != v) {
+          if (v >= 0) {
+            put_row<kOutBf16, false>(p, sl, s, c0, v, first, false, tid, threads, cols, acc);
+            first = false;
+          }
+          v = key;
+#pragma unroll
+          for (int k = 0; k < kCols; ++k) acc[k] = 0.f;
+        }
         float x[8];
         row[b].get(x);
 #pragma unroll
-        for (int k = 0; k < kCols; ++k) acc[k] += x[k];
-        named = true;
+        for (int k = 0; k < kCols; ++k) acc[k] = fmaf(a.scale, x[k], acc[k]);
       }
     }
   }
-  while (v < v1) finish();
-  // Row v1 goes on in the next slab.
-  if (v1 < a.vocab && (named || (v1 == v0 && cut)))
-    store8<false, kVec>(v1 == v0 && cut ? part0 : part0 + p.part_ld, 0, tid, threads, cols, acc);
+  // (a masked key that goes on is no row: v is the last row before it)
+  if (v >= 0) put_row<kOutBf16, false>(p, sl, s, c0, v, first, a.keys[sl.i1 - 1] == v, tid, threads, cols, acc);
+}
+
+// The same over rows on vector boundaries.  Warp 0 copies the slab's rows of
+// dout into the stages of a ring, a batch at a time (a lane each), and hands
+// on their keys; the other warps add the rows up, 8 columns a thread.
+constexpr int kMaxBatch = 32;              // a lane each
+constexpr int kMaxStages = 8;
+constexpr int kBatchBytes = 32768;         // a batch's rows, about
+constexpr int kRingBytes = 98304;          // of the CTAs an SM holds: two, or more with less each
+constexpr uint64_t kWaitNs = 2000000000ull;   // a stage is due within microseconds: longer is an error
+
+template <bool kInBf16, bool kOutBf16>
+__global__ void __launch_bounds__(32 + kMaxThreads) embed_rows_kernel(const __grid_constant__ GradKernelArgs p) {
+  extern __shared__ __align__(128) uint8_t smem[];     // a zero row, then the ring
+  __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages];
+  __shared__ int32_t keys[kMaxStages][kMaxBatch];
+  __shared__ int32_t count[kMaxStages];                // positions of the batch; the last one: ~positions
+  const EmbedGradArgs& a = p.a;
+  const int threads = blockDim.x - 32, lane = threadIdx.x & 31;
+  const int64_t c0 = (int64_t)blockIdx.y * threads * kCols;
+  const int cols = (int)min((int64_t)threads * kCols, a.dim - c0);
+  const uint32_t row_bytes = (uint32_t)cols * (kInBf16 ? 2 : 4), out_bytes = (uint32_t)cols * (kOutBf16 ? 2 : 4);
+  const int64_t s = blockIdx.x;
+  uint8_t* const ring = smem + p.zero_bytes;
+  for (int i = threadIdx.x; i < p.zero_bytes / 16; i += blockDim.x)
+    reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
+  if (threadIdx.x == 0) {
+    for (int k = 0; k < p.stages; ++k) {
+      ptx::mbar_init(ptx::smem_u32(&full[k]), 1);
+      ptx::mbar_init(ptx::smem_u32(&empty[k]), (uint32_t)threads / 32);
+    }
+    ptx::fence_barrier_init();
+  }
+  ptx::fence_proxy_async_smem();
+  __syncthreads();
+  uint8_t* const out = static_cast<uint8_t*>(a.grad) + c0 * (kOutBf16 ? 2 : 4);
+  const uint32_t zeros = ptx::smem_u32(smem);
+  zero_unnamed<false>(a, [&](int64_t r) { ptx::bulk_store(out + r * a.grad_ld * (kOutBf16 ? 2 : 4), zeros, out_bytes); });
+  ptx::bulk_commit();
+  ptx::launch_dependents();
+  const Slab sl = slab_of(p, s);
+
+  if (threadIdx.x < 32) {
+    const int64_t in_stride = a.dout_ld * (kInBf16 ? 2 : 4);
+    const uint8_t* in = static_cast<const uint8_t*>(a.dout) + c0 * (kInBf16 ? 2 : 4);
+    int stage = 0, use = 0;
+    bool more = true;
+    int64_t base = sl.i0;
+    int key = 0, from = 0;
+    if (lane < p.batch && base + lane < sl.i1) {
+      key = a.keys[base + lane];
+      from = a.order[base + lane];
+    }
+    while (more) {
+      const bool in_row = lane < p.batch && base + lane < sl.i1 && key < a.vocab;
+      const int cnt = __popc(__ballot_sync(0xffffffffu, in_row));      // a prefix of the lanes: masked keys are last
+      const int64_t next = base + p.batch;
+      more = cnt == p.batch && next < sl.i1;
+      const int this_key = key, this_from = from;
+      if (more && lane < p.batch && next + lane < sl.i1) {             // in flight while this batch is queued
+        key = a.keys[next + lane];
+        from = a.order[next + lane];
+      }
+      if (!__all_sync(0xffffffffu, ptx::mbar_wait(ptx::smem_u32(&empty[stage]), (use & 1) ^ 1, kWaitNs))) {
+        if (lane == 0) atomicCAS(p.status, 0, 1);
+        break;
+      }
+      if (in_row) keys[stage][lane] = this_key;
+      if (lane == 0) {
+        count[stage] = more ? cnt : ~cnt;
+        ptx::mbar_arrive_expect_tx(ptx::smem_u32(&full[stage]), (uint32_t)cnt * row_bytes);
+      }
+      __syncwarp();
+      if (in_row)
+        ptx::bulk_load(ptx::smem_u32(ring) + (uint32_t)(stage * p.batch + lane) * p.row_slot, in + this_from * in_stride,
+                       row_bytes, ptx::smem_u32(&full[stage]));
+      if (++stage == p.stages) { stage = 0; ++use; }
+      base = next;
+    }
+    if (blockIdx.y == 0) note_cut(p, sl, s);
+  } else {
+    const int tid = threadIdx.x - 32;
+    float acc[kCols] = {};
+    int64_t v = -1;
+    bool first = true;                                 // row v is the slab's first
+    int stage = 0, use = 0;
+    bool more = true, ok = true;
+    while (more) {
+      ok = __all_sync(0xffffffffu, ptx::mbar_wait(ptx::smem_u32(&full[stage]), use & 1, kWaitNs));
+      if (!ok) {
+        if (lane == 0) atomicCAS(p.status, 0, 2);
+        break;
+      }
+      const int c = count[stage];
+      more = c >= 0;
+      const int cnt = more ? c : ~c;
+      const uint8_t* rows = ring + (size_t)stage * p.batch * p.row_slot;
+      constexpr int kAhead = 4;
+      for (int b0 = 0; b0 < cnt; b0 += kAhead) {
+        Row8<kInBf16, true> row[kAhead];
+#pragma unroll
+        for (int b = 0; b < kAhead; ++b)
+          if (b0 + b < cnt) row[b].load_shared(rows + (size_t)(b0 + b) * p.row_slot, tid, cols);
+#pragma unroll
+        for (int b = 0; b < kAhead; ++b) {
+          if (b0 + b >= cnt) break;
+          const int key = keys[stage][b0 + b];
+          if (key != v) {
+            if (v >= 0) {
+              put_row<kOutBf16, true>(p, sl, s, c0, v, first, false, tid, threads, cols, acc);
+              first = false;
+            }
+            v = key;
+#pragma unroll
+            for (int k = 0; k < kCols; ++k) acc[k] = 0.f;
+          }
+          float x[8];
+          row[b].get(x);
+#pragma unroll
+          for (int k = 0; k < kCols; ++k) acc[k] = fmaf(a.scale, x[k], acc[k]);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&empty[stage]));
+      if (++stage == p.stages) { stage = 0; ++use; }
+    }
+    // (a masked key that goes on is no row: v is the last row before it)
+    if (ok && v >= 0)
+      put_row<kOutBf16, true>(p, sl, s, c0, v, first, a.keys[sl.i1 - 1] == v, tid, threads, cols, acc);
+  }
+  ptx::bulk_wait_all();                                // the zero row is shared memory of this CTA
 }
 
 // Adds the partial rows of the rows cut by slab ends: slab `first` holds a
-// row's start (second row of its pair), the following slabs up to `last` the rest.
-// A CTA takes 128 columns of one row at a time, each warp an eighth of the
-// slabs (a token that fills the batch has one partial row in every slab).
+// row's start (second row of its pair), the following slabs up to `last` the
+// rest.  An item is 128 columns of one row.  Most rows are cut once: a warp
+// adds those by itself.  A frequent token's row goes through many slabs (one that
+// fills the batch, through all): the warps of a CTA take an eighth of them each.
+constexpr int kShortCut = 16;
+
+__device__ __forceinline__ void add_parts(const GradKernelArgs& p, const CutRow& cut, int lo, int hi, int64_t c,
+                                          float4& acc) {
+#pragma unroll 8
+  for (int s = lo; s < hi; ++s) {
+    const float4 x = *reinterpret_cast<const float4*>(p.parts + (2 * (int64_t)s + (s == cut.first)) * p.part_ld + c);
+    acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
+  }
+}
+
+template <bool kOutBf16>
+__device__ __forceinline__ void store_fix(const EmbedGradArgs& a, int64_t row, int64_t c, const float4& acc) {
+  const float v[4] = {acc.x, acc.y, acc.z, acc.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (c + k >= a.dim) break;
+    const int64_t at = row * a.grad_ld + c + k;
+    float x = v[k];
+    if constexpr (kOutBf16) {
+      __nv_bfloat16* g = static_cast<__nv_bfloat16*>(a.grad) + at;
+      if (a.accumulate) x += __bfloat162float(*g);
+      *g = __float2bfloat16_rn(x);
+    } else {
+      float* g = static_cast<float*>(a.grad) + at;
+      if (a.accumulate) x += *g;
+      *g = x;
+    }
+  }
+}
+
 template <bool kOutBf16>
 __global__ void __launch_bounds__(32 * kFixParts) embed_fix_kernel(const __grid_constant__ GradKernelArgs p) {
   __shared__ float4 sum[kFixParts][32];
@@ -323,21 +563,23 @@ __global__ void __launch_bounds__(32 * kFixParts) embed_fix_kernel(const __grid_
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int blocks = (int)((a.dim + kFixCols - 1) / kFixCols);
   ptx::wait_dependencies();
-  const int items = *p.n_cut * blocks;
-  for (int it = blockIdx.x; it < items; it += gridDim.x) {
+  const int64_t items = (int64_t)*p.n_cut * blocks;
+  for (int64_t it = (int64_t)warp * gridDim.x + blockIdx.x; it < items; it += (int64_t)kFixParts * gridDim.x) {
     const CutRow cut = p.cut[it / blocks];
-    const int64_t c = (int64_t)(it % blocks) * kFixCols + 4 * lane;
-    const int slabs = cut.last - cut.first + 1;
-    const int lo = cut.first + (int)((int64_t)slabs * warp / kFixParts);
-    const int hi = cut.first + (int)((int64_t)slabs * (warp + 1) / kFixParts);
+    if (cut.last - cut.first >= kShortCut) continue;
+    const int64_t c = it % blocks * kFixCols + 4 * lane;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (c < p.part_ld) {
-#pragma unroll 8
-      for (int s = lo; s < hi; ++s) {
-        const float4 x = *reinterpret_cast<const float4*>(p.parts + (2 * (int64_t)s + (s == cut.first)) * p.part_ld + c);
-        acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
-      }
-    }
+    if (c < p.part_ld) add_parts(p, cut, cut.first, cut.last + 1, c, acc);
+    store_fix<kOutBf16>(a, cut.row, c, acc);
+  }
+  for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+    const CutRow cut = p.cut[it / blocks];
+    if (cut.last - cut.first < kShortCut) continue;
+    const int64_t c = it % blocks * kFixCols + 4 * lane;
+    const int64_t slabs = cut.last - cut.first + 1;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (c < p.part_ld)
+      add_parts(p, cut, cut.first + (int)(slabs * warp / kFixParts), cut.first + (int)(slabs * (warp + 1) / kFixParts), c, acc);
     __syncthreads();
     sum[warp][lane] = acc;
     __syncthreads();
@@ -347,29 +589,10 @@ __global__ void __launch_bounds__(32 * kFixParts) embed_fix_kernel(const __grid_
       const float4 x = sum[w][lane];
       acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
     }
-    const float v[4] = {acc.x, acc.y, acc.z, acc.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (c + k >= a.dim) break;
-      const int64_t at = cut.row * a.grad_ld + c + k;
-      float x = v[k] * a.scale;
-      if constexpr (kOutBf16) {
-        __nv_bfloat16* g = static_cast<__nv_bfloat16*>(a.grad) + at;
-        if (a.accumulate) x += __bfloat162float(*g);
-        *g = __float2bfloat16_rn(x);
-      } else {
-        float* g = static_cast<float*>(a.grad) + at;
-        if (a.accumulate) x += *g;
-        *g = x;
-      }
-    }
+    store_fix<kOutBf16>(a, cut.row, c, acc);
   }
 }
 
-// Threads that cover `dim` columns, 8 each, in whole warps.
-int threads_for(int64_t dim) {
-  return (int)std::min<int64_t>(kMaxThreads, (dim + 32 * kCols - 1) / (32 * kCols) * 32);
-}
 // Rows of a tensor start on the vector's boundary: 16 bytes of bf16, 32 of fp32.
 bool vec_rows(const void* p, int64_t ld, int64_t dim, int32_t bf16) {
   return ld % kCols == 0 && dim % kCols == 0 && aligned(p, bf16 ? 16 : 32);
@@ -379,9 +602,33 @@ template <bool kA, bool kB, bool kVec>
 void lookup_launch(const LookupArgs& a, dim3 grid, dim3 block, cudaStream_t s) {
   lookup_kernel<kA, kB, kVec><<<grid, block, 0, s>>>(a);
 }
-template <bool kA, bool kB, bool kVec>
-cudaError_t grad_launch(const GradKernelArgs& p, dim3 grid, int threads, cudaStream_t s) {
-  return launch_overlapped(embed_grad_kernel<kA, kB, kVec>, grid, dim3((unsigned)threads), s, p);
+template <bool kIn, bool kOut>
+cudaError_t grad_launch(GradKernelArgs& p, int64_t ctas, bool vec, cudaStream_t s) {
+  const EmbedGradArgs& a = p.a;
+  const int threads = threads_for(a.dim);
+  const dim3 grid((unsigned)ctas, (unsigned)((a.dim + threads * kCols - 1) / (threads * kCols)));
+  // The kernel writes before its wait, so what it may overlap has to be the sort:
+  // without ids there is none.
+  const bool after_sort = a.n > 0;
+  if (!vec) return launch_overlapped(embed_grad_kernel<kIn, kOut>, grid, dim3((unsigned)threads), 0, s, after_sort, p);
+  const int cols = (int)std::min<int64_t>(a.dim, (int64_t)threads * kCols);
+  p.row_slot = (uint32_t)round_up((size_t)cols * (kIn ? 2 : 4), 128);
+  p.zero_bytes = (int32_t)round_up((size_t)cols * (kOut ? 2 : 4), 128);
+  const int ring = 2 * kRingBytes / ctas_per_sm(a.dim);
+  p.batch = (int32_t)std::max<int64_t>(4, std::min<int64_t>({kMaxBatch, kBatchBytes / p.row_slot, ring / (2 * p.row_slot)}));
+  p.stages = (int32_t)std::max<int64_t>(2, std::min<int64_t>(kMaxStages, ring / (p.batch * p.row_slot)));
+  const size_t smem = p.zero_bytes + (size_t)p.stages * p.batch * p.row_slot;
+  static std::atomic<bool> ready[kMaxDevices];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  if (!ready[dev].load()) {
+    e = cudaFuncSetAttribute(embed_rows_kernel<kIn, kOut>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes + 16384);
+    if (e != cudaSuccess) return e;
+    ready[dev].store(true);
+  }
+  return launch_overlapped(embed_rows_kernel<kIn, kOut>, grid, dim3((unsigned)(32 + threads)), smem, s, after_sort, p);
 }
 
 }  // namespace
@@ -401,32 +648,29 @@ cudaError_t launch_lookup(const LookupArgs& a, cudaStream_t s) {
 }
 
 size_t embed_grad_partial_bytes(int64_t n, int64_t vocab, int64_t dim) {
-  const SlabPlan sp = plan_slabs(n, vocab);
-  return 256 + round_up(sp.slabs * sizeof(CutRow), 256) + (size_t)sp.slabs * 2 * round_up((size_t)dim, 8) * sizeof(float);
+  const SlabPlan sp = plan_slabs(n, vocab, dim);
+  return round_up(sp.slabs * sizeof(CutRow), 256) + (size_t)sp.slabs * 2 * round_up((size_t)dim, 8) * sizeof(float);
 }
 
 cudaError_t launch_embed_grad(const EmbedGradArgs& a, cudaStream_t s) {
-  const SlabPlan sp = plan_slabs(a.n, a.vocab);
+  const SlabPlan sp = plan_slabs(a.n, a.vocab, a.dim);
   GradKernelArgs p;
   p.a = a;
   p.slab = sp.slab;
   p.part_ld = (int64_t)round_up((size_t)a.dim, 8);
   uint8_t* at = reinterpret_cast<uint8_t*>(a.partials);
-  p.n_cut = a.partials_count();
-  p.cut = reinterpret_cast<CutRow*>(at + 256);
-  p.parts = reinterpret_cast<float*>(at + 256 + round_up(sp.slabs * sizeof(CutRow), 256));
+  p.status = a.header;
+  p.n_cut = a.header + 1;
+  p.cut = reinterpret_cast<CutRow*>(at);
+  p.parts = reinterpret_cast<float*>(at + round_up(sp.slabs * sizeof(CutRow), 256));
   const bool vec = vec_rows(a.dout, a.dout_ld, a.dim, a.dout_bf16) && vec_rows(a.grad, a.grad_ld, a.dim, a.grad_bf16);
-  const int threads = threads_for(a.dim);
-  const dim3 grid((unsigned)sp.slabs, (unsigned)((a.dim + threads * kCols - 1) / (threads * kCols)));
-  const auto go = vec ? (a.dout_bf16 ? (a.grad_bf16 ? grad_launch<true, true, true> : grad_launch<true, false, true>)
-                                     : (a.grad_bf16 ? grad_launch<false, true, true> : grad_launch<false, false, true>))
-                      : (a.dout_bf16 ? (a.grad_bf16 ? grad_launch<true, true, false> : grad_launch<true, false, false>)
-                                     : (a.grad_bf16 ? grad_launch<false, true, false> : grad_launch<false, false, false>));
-  const cudaError_t e = go(p, grid, threads, s);
+  const cudaError_t e = a.dout_bf16 ? (a.grad_bf16 ? grad_launch<true, true>(p, sp.ctas, vec, s) : grad_launch<true, false>(p, sp.ctas, vec, s))
+                                    : (a.grad_bf16 ? grad_launch<false, true>(p, sp.ctas, vec, s) : grad_launch<false, false>(p, sp.ctas, vec, s));
   if (e != cudaSuccess || a.n == 0) return e;
   const int64_t items = sp.slabs * ((a.dim + kFixCols - 1) / kFixCols);      // at most
   const dim3 fix((unsigned)std::min<int64_t>(items, 4 * std::max(1, sm_count())));
-  return launch_overlapped(a.grad_bf16 ? embed_fix_kernel<true> : embed_fix_kernel<false>, fix, dim3(32 * kFixParts), s, p);
+  return launch_overlapped(a.grad_bf16 ? embed_fix_kernel<true> : embed_fix_kernel<false>, fix, dim3(32 * kFixParts),
+                           0, s, true, p);
 }
 
 }  // namespace ops

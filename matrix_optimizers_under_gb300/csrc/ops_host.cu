@@ -204,12 +204,12 @@ struct EmbedLayout {
 };
 EmbedLayout embed_layout(int64_t n, int64_t vocab, int64_t dim) {
   EmbedLayout l;
-  size_t off = 0;
+  size_t off = 256;                                         // the status word and a counter
   l.keys = off; off += round_up((size_t)n * 4, 256);
   l.order = off; off += round_up((size_t)n * 4, 256);
   l.sort = off; off += round_up(sort_scratch_bytes(n, vocab), 256);
   l.partials = off; off += round_up(embed_grad_partial_bytes(n, vocab, dim), 256);
-  l.bytes = std::max<size_t>(off, 256);
+  l.bytes = off;
   return l;
 }
 
@@ -385,6 +385,8 @@ extern "C" int mfsdp_embedding_grad(const void* dout, int32_t dout_dtype, int64_
   EmbedGradArgs a{};
   a.dout = dout;
   a.grad = grad;
+  a.ids = ids;
+  a.ids64 = s.ids64;
   a.keys = s.keys_out;
   a.order = s.order_out;
   a.partials = reinterpret_cast<float*>(ws + l.partials);
@@ -397,9 +399,9 @@ extern "C" int mfsdp_embedding_grad(const void* dout, int32_t dout_dtype, int64_
   a.grad_bf16 = grad_dtype == MFSDP_DTYPE_BF16;
   a.accumulate = accumulate;
   a.scale = (float)scale;
-  s.zero = a.partials_count();
+  a.header = s.zero = reinterpret_cast<int32_t*>(ws);
   const OpRange range("mfsdp embedding gradient");
-  cudaError_t e = launch_sort(s, stream);
+  cudaError_t e = n > 0 ? launch_sort(s, stream) : cudaMemsetAsync(ws, 0, 8, stream);
   if (e == cudaSuccess) e = launch_embed_grad(a, stream);
   return cuda_status(e);
 }
@@ -418,7 +420,7 @@ extern "C" size_t mfsdp_expert_workspace_bytes(int32_t n_experts, int64_t n_rows
   return bytes;
 }
 
-extern "C" int mfsdp_expert_device_status(const void* workspace, void* stream, int32_t* detail) {
+extern "C" int mfsdp_op_device_status(const void* workspace, void* stream, int32_t* detail) {
   return mfsdp_muon_device_status(workspace, stream, detail);
 }
 

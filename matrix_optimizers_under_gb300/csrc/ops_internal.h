@@ -28,19 +28,22 @@ inline size_t dtype_size(int32_t dt) { return dt == MFSDP_DTYPE_BF16 ? 2 : 4; }
 inline size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 inline int cuda_status(cudaError_t e) { return e == cudaSuccess ? MFSDP_OK : MFSDP_ERR_CUDA; }
 
-// Launch whose prologue may overlap the end of the kernel before it in the
-// stream; it calls ptx::wait_dependencies() before it reads that one's results.
+// Launch that may overlap the kernel before it in the stream from where that
+// one allows it (ptx::launch_dependents), or in plain order.  The kernel calls
+// ptx::wait_dependencies() before it reads that one's results.
 template <typename... P, typename... A>
-cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, dim3 block, cudaStream_t s, A&&... args) {
+cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, bool overlap,
+                              A&&... args) {
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = overlap ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<A&&>(args)...);
 }
 
@@ -84,7 +87,7 @@ struct SortArgs {
   int32_t* keys_out;     // sorted keys [n]
   int32_t* order_out;    // the position each came from [n]
   void* scratch;         // sort_scratch_bytes(n, n_keys)
-  int32_t* zero;         // a counter the sort sets to 0 (may be null)
+  int32_t* zero;         // two words the sort sets to 0 (may be null)
 };
 size_t sort_scratch_bytes(int64_t n, int64_t n_keys);
 cudaError_t launch_sort(const SortArgs& a, cudaStream_t s);
@@ -104,17 +107,15 @@ cudaError_t launch_lookup(const LookupArgs& a, cudaStream_t s);
 struct EmbedGradArgs {
   const void* dout;
   void* grad;
+  const void* ids;
   const int32_t* keys;   // sorted
   const int32_t* order;
   float* partials;       // embed_grad_partial_bytes(n, vocab, dim)
+  int32_t* header;       // two words, zeroed before: status, a counter
   int64_t n, vocab, dim, dout_ld, grad_ld;
-  int32_t dout_bf16, grad_bf16, accumulate;
+  int32_t dout_bf16, grad_bf16, accumulate, ids64;
   float scale;
-  // Counter at the head of `partials`: the sort that runs before the gradient zeroes it.
-  int32_t* partials_count() const { return reinterpret_cast<int32_t*>(partials); }
 };
-// Slabs the embedding gradient's work is cut into, about (8 CTAs an SM).
-constexpr int kSlabTarget = 1216;
 size_t embed_grad_partial_bytes(int64_t n, int64_t vocab, int64_t dim);
 cudaError_t launch_embed_grad(const EmbedGradArgs& a, cudaStream_t s);
 

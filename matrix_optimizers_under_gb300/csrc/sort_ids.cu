@@ -7,7 +7,7 @@
 // lane) order.  A pass counts every tile's digits, adds up the counts that
 // come before a tile's -- all smaller digits of every tile, and its own digit
 // in earlier tiles -- and moves the pairs.  A pair's place among its warp's
-// equal digits comes from a warp match, so the sort is stable and its result
+// equal digits comes from ballots, so the sort is stable and its result
 // does not depend on timing.  An id outside [0, n_keys) sorts as n_keys, after
 // all valid ones.
 //
@@ -29,13 +29,27 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kDigits = 256;
 
+// Lanes of the warp that hold the same 8-bit digit, among the lanes of `live`:
+// one ballot a bit.  (A match instruction takes ~250 cycles of its scheduler: the
+// counting loop of 32768 ids took 8200 cycles a pass with it, and 36 % of the sort.)
+__device__ __forceinline__ unsigned same_digit(int digit, unsigned live) {
+  unsigned same = live;
+#pragma unroll
+  for (int b = 0; b < 8; ++b) {
+    const unsigned v = __ballot_sync(0xffffffffu, (digit >> b) & 1);
+    same &= (digit >> b) & 1 ? v : ~v;
+  }
+  return same;
+}
+
 // ------------------------------------------------------------- one cluster
 constexpr int kClusterThreads = 1024;
 constexpr int kClusterWarps = kClusterThreads / 32;
 constexpr int kClusterSteps = 8;                                // pairs of a thread
 constexpr int kClusterTile = kClusterThreads * kClusterSteps;   // pairs of a CTA
 constexpr int kMaxCluster = 8;
-constexpr size_t kClusterSmem = (size_t)kClusterTile * 8 + (size_t)kClusterWarps * kDigits * 4;
+constexpr int kQuarters = kClusterThreads / kDigits;             // threads that add up one digit's warps
+constexpr size_t kClusterSmem = (size_t)kClusterTile * 16 + (size_t)kClusterWarps * kDigits * 4;
 
 struct ClusterArgs {
   const void* ids;
@@ -50,14 +64,17 @@ struct ClusterArgs {
 __global__ void __launch_bounds__(kClusterThreads, 1) sort_cluster_kernel(const __grid_constant__ ClusterArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   uint64_t* pairs = reinterpret_cast<uint64_t*>(smem);                       // (position << 32) | key
-  int (*cnt)[kDigits] = reinterpret_cast<int (*)[kDigits]>(smem + (size_t)kClusterTile * 8);
+  uint64_t* local = pairs + kClusterTile;                                    // this CTA's pairs by digit
+  int (*cnt)[kDigits] = reinterpret_cast<int (*)[kDigits]>(smem + (size_t)kClusterTile * 16);
   __shared__ int hist[kDigits];                                              // this CTA's digits
-  __shared__ int scan[kDigits / 32];
+  __shared__ int quarter[kQuarters][kDigits];
+  __shared__ int start[kDigits], shift_to[kDigits];                          // of a digit in `local`; from there to its place
+  __shared__ int scan[2][kDigits / 32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = blockIdx.x, ctas = gridDim.x;                             // the grid is one cluster
   const int tile = a.steps * kClusterThreads;
   ptx::launch_dependents();
-  if (rank == 0 && threadIdx.x == 0 && a.zero) *a.zero = 0;
+  if (rank == 0 && threadIdx.x < 2 && a.zero) a.zero[threadIdx.x] = 0;
   const int local0 = warp * a.steps * 32 + lane;                             // this thread's first pair in the tile
   uint64_t pr[kClusterSteps];
 #pragma unroll
@@ -82,61 +99,96 @@ __global__ void __launch_bounds__(kClusterThreads, 1) sort_cluster_kernel(const 
     for (int k = 0; k < kClusterSteps; ++k) {
       if (k >= a.steps) break;
       const bool in = rank * tile + local0 + 32 * k < a.n;
-      const int digit = in ? (int)((uint32_t)pr[k] >> shift) & (kDigits - 1) : kDigits;
-      const unsigned same = __match_any_sync(0xffffffffu, digit);
+      const int digit = in ? (int)((uint32_t)pr[k] >> shift) & (kDigits - 1) : 0;
+      const unsigned same = same_digit(digit, __ballot_sync(0xffffffffu, in));
       if (in) place[k] = cnt[warp][digit] + __popc(same & ((1u << lane) - 1));
       __syncwarp();
       if (in && (same >> lane) == 1u) cnt[warp][digit] = place[k] + 1;
       __syncwarp();
     }
     __syncthreads();
-    const int d = threadIdx.x;
-    if (d < kDigits) {
-      int s = 0;
+    // counts of a digit over the warps before each: four threads a digit
+    const int d = threadIdx.x & (kDigits - 1), q = threadIdx.x / kDigits;
+    constexpr int kPer = kClusterWarps / kQuarters;
+    int own[kPer], sum = 0;
 #pragma unroll
-      for (int w = 0; w < kClusterWarps; ++w) {
-        const int c = cnt[w][d];
-        cnt[w][d] = s;
-        s += c;
-      }
-      hist[d] = s;
+    for (int w = 0; w < kPer; ++w) own[w] = cnt[q * kPer + w][d];
+#pragma unroll
+    for (int w = 0; w < kPer; ++w) {
+      const int c = own[w];
+      own[w] = sum;
+      sum += c;
     }
+    quarter[q][d] = sum;
+    __syncthreads();
+    int ahead = 0, mine = 0;
+#pragma unroll
+    for (int k = 0; k < kQuarters; ++k) {
+      if (k < q) ahead += quarter[k][d];
+      mine += quarter[k][d];
+    }
+#pragma unroll
+    for (int w = 0; w < kPer; ++w) cnt[q * kPer + w][d] = own[w] + ahead;
+    if (q == 0) hist[d] = mine;
     ptx::cluster_sync();                 // every CTA's counts stand, and its pairs are in registers
-    int total = 0, before = 0, run = 0;
-    if (d < kDigits) {
-      const uint32_t mine = ptx::smem_u32(&hist[d]);
-      for (int c = 0; c < ctas; ++c) {
-        const int h = ptx::ld_shared_cluster_s32(ptx::mapa_shared(mine, (uint32_t)c));
-        total += h;
-        if (c < rank) before += h;
+    int total = 0, before = 0, run = mine, all = 0;
+    if (q == 0) {
+      const uint32_t at = ptx::smem_u32(&hist[d]);
+      int h[kMaxCluster];                // all in flight together: a remote read takes ~0.5 us
+#pragma unroll
+      for (int c = 0; c < kMaxCluster; ++c)
+        h[c] = c < ctas ? ptx::ld_shared_cluster_s32(ptx::mapa_shared(at, (uint32_t)c)) : 0;
+#pragma unroll
+      for (int c = 0; c < kMaxCluster; ++c) {
+        total += h[c];
+        if (c < rank) before += h[c];
       }
-      run = total;                       // inclusive scan over the digits
+      all = total;                       // inclusive scans over the digits: here, and in the cluster
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, run, o);
-        if (lane >= o) run += v;
+        const int v = __shfl_up_sync(0xffffffffu, run, o), u = __shfl_up_sync(0xffffffffu, all, o);
+        if (lane >= o) {
+          run += v;
+          all += u;
+        }
       }
-      if (lane == 31) scan[warp] = run;
+      if (lane == 31) {
+        scan[0][warp] = run;
+        scan[1][warp] = all;
+      }
     }
     __syncthreads();
-    if (d < kDigits) {
-      int at = run - total + before;
-      for (int w = 0; w < warp; ++w) at += scan[w];
-#pragma unroll 8
-      for (int w = 0; w < kClusterWarps; ++w) cnt[w][d] += at;
+    if (q == 0) {
+      for (int w = 0; w < warp; ++w) {
+        run += scan[0][w];
+        all += scan[1][w];
+      }
+      start[d] = run - mine;
+      shift_to[d] = all - total + before - (run - mine);
     }
     __syncthreads();
-    const bool last = pass == a.passes - 1;
+    // By digit in this CTA first, so that neighbours then move to neighbouring places.
 #pragma unroll
     for (int k = 0; k < kClusterSteps; ++k) {
       if (k >= a.steps || rank * tile + local0 + 32 * k >= a.n) break;
-      const int to = cnt[warp][((uint32_t)pr[k] >> shift) & (kDigits - 1)] + place[k];
+      const int digit = ((uint32_t)pr[k] >> shift) & (kDigits - 1);
+      local[start[digit] + cnt[warp][digit] + place[k]] = pr[k];
+    }
+    __syncthreads();
+    const bool last = pass == a.passes - 1;
+    const int held = min(tile, a.n - rank * tile);
+#pragma unroll
+    for (int k = 0; k < kClusterSteps; ++k) {
+      const int j = k * kClusterThreads + threadIdx.x;
+      if (j >= held) break;
+      const uint64_t v = local[j];
+      const int to = j + shift_to[((uint32_t)v >> shift) & (kDigits - 1)];
       if (last) {
-        a.keys_out[to] = (int32_t)(uint32_t)pr[k];
-        a.order_out[to] = (int32_t)(pr[k] >> 32);
+        a.keys_out[to] = (int32_t)(uint32_t)v;
+        a.order_out[to] = (int32_t)(v >> 32);
       } else {
         const int c = to / tile;
-        ptx::st_shared_cluster_u64(ptx::mapa_shared(ptx::smem_u32(&pairs[to - c * tile]), (uint32_t)c), pr[k]);
+        ptx::st_shared_cluster_u64(ptx::mapa_shared(ptx::smem_u32(&pairs[to - c * tile]), (uint32_t)c), v);
       }
     }
     if (!last) ptx::cluster_sync();      // every pair has arrived, and no CTA still reads these counts
@@ -241,7 +293,7 @@ __device__ __forceinline__ void count_digits(const PassArgs& a, int (*cnt)[kDigi
 
 __global__ void __launch_bounds__(kThreads) sort_count_kernel(const __grid_constant__ PassArgs a) {
   __shared__ int cnt[kWarps][kDigits];
-  if (a.zero && blockIdx.x == 0 && threadIdx.x == 0) *a.zero = 0;
+  if (a.zero && blockIdx.x == 0 && threadIdx.x < 2) a.zero[threadIdx.x] = 0;
   count_digits(a, cnt);
   int s = 0;
 #pragma unroll
@@ -282,10 +334,10 @@ __global__ void __launch_bounds__(kThreads) sort_move_kernel(const __grid_consta
     const int64_t i = base + k * 32 + lane;
     const bool in = i < a.n;
     const unsigned live = __ballot_sync(0xffffffffu, in);
+    const int2 p = in ? load_pair(a, i) : make_int2(0, 0);
+    const int digit = (p.x >> a.shift) & (kDigits - 1);
+    const unsigned same = same_digit(digit, live);
     if (in) {
-      const int2 p = load_pair(a, i);
-      const int digit = (p.x >> a.shift) & (kDigits - 1);
-      const unsigned same = __match_any_sync(live, digit);
       const int place = cnt[warp][digit] + __popc(same & ((1u << lane) - 1));
       __syncwarp(live);
       if ((same >> lane) == 1u) cnt[warp][digit] = place + 1;     // the last of them moves the next place on
