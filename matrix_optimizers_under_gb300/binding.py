@@ -143,6 +143,16 @@ def version() -> str:
     return _lib.mfsdp_version().decode()
 
 
+def _current_stream() -> int:
+    """The current CUDA stream's handle.  Making a torch.cuda.Stream object for it takes 3 us of a call
+    that may take 5; torch hands out the plain handle too."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is None or not torch.cuda.is_initialized():
+        return int(torch.cuda.current_stream().cuda_stream)
+    return raw(torch._C._cuda_getDevice())
+
+
 def _check(status: int, what: str) -> None:
     if status != OK:
         raise MfsdpError(status, what)
@@ -311,8 +321,7 @@ def _dtype_code(t) -> int:
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
-        return int(torch.cuda.current_stream().cuda_stream)
+        return _current_stream()
     return int(stream) if isinstance(stream, int) else int(stream.cuda_stream)
 
 

@@ -422,9 +422,10 @@ __global__ void __launch_bounds__(32 + kMaxThreads) embed_rows_kernel(const __gr
   }
   ptx::fence_proxy_async_smem();
   __syncthreads();
+  const uint64_t first_out = ptx::policy_evict_first();   // (90 us with it, 93 without)
   uint8_t* const out = static_cast<uint8_t*>(a.grad) + c0 * (kOutBf16 ? 2 : 4);
   const uint32_t zeros = ptx::smem_u32(smem);
-  zero_unnamed<false>(a, [&](int64_t r) { ptx::bulk_store(out + r * a.grad_ld * (kOutBf16 ? 2 : 4), zeros, out_bytes); });
+  zero_unnamed<false>(a, [&](int64_t r) { ptx::bulk_store(out + r * a.grad_ld * (kOutBf16 ? 2 : 4), zeros, out_bytes, first_out); });
   ptx::bulk_commit();
   ptx::launch_dependents();
   const Slab sl = slab_of(p, s);
