@@ -52,11 +52,14 @@ bool rows_fit(int64_t n, int64_t ld, int64_t width) {
 constexpr int64_t kMaxChunks = (int64_t)1 << 30;
 constexpr int kMaxClipBlocks = 2048;     // CTAs (and partial sums) of one launch
 
+// Chunks of a tensor: its 16-byte vectors from the first boundary on, 32 KB a
+// chunk (the elements before and after them go with the first and last one).
 int64_t chunks_of(const mfsdp_grad_tensor& t) {
   if (t.numel == 0) return 0;
   const size_t es = dtype_size(t.src_dtype);
   const int64_t head = (int64_t)(((16 - (reinterpret_cast<uintptr_t>(t.src) & 15)) & 15) / es);
-  return t.numel <= head ? 1 : (t.numel - head + kClipChunk - 1) / kClipChunk;
+  const int64_t vecs = t.numel <= head ? 0 : (t.numel - head) / (int64_t)(16 / es);
+  return std::max<int64_t>(1, (vecs + kClipChunkBytes / 16 - 1) / (kClipChunkBytes / 16));
 }
 
 // The checks shared by the norm and the clipping; `clip`: the destinations too.
@@ -146,12 +149,10 @@ int run_clip(const mfsdp_grad_tensor* t, int32_t n, double max_norm, double eps,
   const int sms = sm_count();
   if (sms <= 0) return MFSDP_ERR_CUDA;
   const OpRange range(clip ? "mfsdp grad clip" : "mfsdp grad norm");
-  // Launches of at most kClipTable tensors: all sums first, then the scaling.
-  std::vector<ClipBatch> batches;
-  int partials = 0;
-  for (int i = 0; i < n || batches.empty();) {
-    batches.emplace_back();
-    ClipBatch& b = batches.back();
+  // Launches of at most kClipTable tensors: all sums first, then the scaling,
+  // whose launches add up all partial sums.
+  cudaStream_t s = stream;
+  const auto fill = [&](ClipBatch<kClipTable>& b, int& i) {
     b.n = 0;
     int64_t chunks = 0;
     for (; i < n && b.n < kClipTable; ++i) {
@@ -166,22 +167,38 @@ int run_clip(const mfsdp_grad_tensor* t, int32_t n, double max_norm, double eps,
       chunks += chunks_of(t[i]);
     }
     b.chunks = (int32_t)chunks;
-    b.first_partial = partials;
-    partials += clip_blocks(chunks, sms);
-  }
+  };
+  ClipBatch<kClipTable> b;
+  b.partials = static_cast<double*>(ws);
+  b.out = out;
+  b.max_norm = max_norm;
+  b.eps = eps;
+  b.first_partial = b.n_partials = 0;
   cudaError_t e = cudaSuccess;
-  for (ClipBatch& b : batches) {
-    b.n_partials = partials;
-    b.partials = static_cast<double*>(ws);
-    b.out = out;
-    b.max_norm = max_norm;
-    b.eps = eps;
-    if (b.chunks > 0 && e == cudaSuccess) e = launch_clip_norm(b, clip_blocks(b.chunks, sms), stream);
+  int launches = 0;
+  for (int i = 0; i < n || launches == 0; ++launches) {
+    fill(b, i);
+    if (b.chunks == 0) continue;
+    const int blocks = clip_blocks(b.chunks, sms);
+    e = launch_clip_norm(b, blocks, s);
+    if (e != cudaSuccess) return cuda_status(e);
+    b.first_partial += blocks;
   }
-  if (!clip || partials == 0) return cuda_status(e == cudaSuccess ? launch_clip_finish(batches[0], stream) : e);
-  for (const ClipBatch& b : batches)
-    if (b.chunks > 0 && e == cudaSuccess) e = launch_clip_scale(b, clip_blocks(b.chunks, sms), stream);
-  return cuda_status(e);
+  b.n_partials = b.first_partial;
+  if (!clip || b.n_partials == 0) return cuda_status(launch_clip_finish(b, s));
+  b.first_partial = 0;
+  bool first = true;
+  for (int i = 0; i < n;) {
+    if (launches > 1) fill(b, i);
+    else i = n;                                                  // still filled
+    if (b.chunks == 0) continue;
+    const int blocks = clip_blocks(b.chunks, sms);
+    e = launch_clip_scale(b, blocks, first, s);
+    if (e != cudaSuccess) return cuda_status(e);
+    first = false;
+    b.first_partial += blocks;
+  }
+  return MFSDP_OK;
 }
 
 // ------------------------------------------------------------ sort, embedding

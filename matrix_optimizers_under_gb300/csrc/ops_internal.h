@@ -61,9 +61,10 @@ struct ClipTensor {
   int32_t chunk0;        // its first chunk of the launch
   int16_t src_bf16, dst_bf16;
 };
-constexpr int kClipChunk = 16384;       // elements of one chunk
+constexpr int kClipChunkBytes = 32768;  // source bytes of one chunk
 constexpr int kClipTable = 512;         // tensors per launch
-struct ClipBatch {
+constexpr int kClipShort = 16;          // tensors of a short table (a launch copies its table)
+struct ClipHead {
   int32_t n;
   int32_t chunks;        // chunks of this launch
   int32_t first_partial; // this launch's first slot in `partials`
@@ -71,12 +72,15 @@ struct ClipBatch {
   double* partials;      // one sum of squares per CTA of the norm launches
   float* out;            // {norm, coefficient}
   double max_norm, eps;
-  ClipTensor t[kClipTable];
 };
-static_assert(sizeof(ClipBatch) < 32000, "kernel parameter limit");
-cudaError_t launch_clip_norm(const ClipBatch& b, int blocks, cudaStream_t s);
-cudaError_t launch_clip_finish(const ClipBatch& b, cudaStream_t s);
-cudaError_t launch_clip_scale(const ClipBatch& b, int blocks, cudaStream_t s);
+template <int kN>
+struct ClipBatch : ClipHead {
+  ClipTensor t[kN];
+};
+static_assert(sizeof(ClipBatch<kClipTable>) < 32000, "kernel parameter limit");
+cudaError_t launch_clip_norm(const ClipBatch<kClipTable>& b, int blocks, cudaStream_t s);
+cudaError_t launch_clip_finish(const ClipHead& b, cudaStream_t s);
+cudaError_t launch_clip_scale(const ClipBatch<kClipTable>& b, int blocks, bool overlap, cudaStream_t s);
 
 // ------------------------------------------------------------------- id sort
 struct SortArgs {
