@@ -147,6 +147,20 @@ __device__ __forceinline__ Tile decode(const ExpertArgs& p, const Shape& sh, con
   return r;
 }
 
+// A value that all lanes hold, as the compiler can see.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
+__device__ __forceinline__ Tile uniform(const Tile& t) {
+  Tile r;
+  r.e = __shfl_sync(0xffffffffu, t.e, 0);
+  r.group = __shfl_sync(0xffffffffu, t.group, 0);
+  r.m0 = __shfl_sync(0xffffffffu, t.m0, 0);
+  r.n0 = __shfl_sync(0xffffffffu, t.n0, 0);
+  r.n = __shfl_sync(0xffffffffu, t.n, 0);
+  r.n_mma = __shfl_sync(0xffffffffu, t.n_mma, 0);
+  r.k_len = __shfl_sync(0xffffffffu, t.k_len, 0);
+  return r;
+}
+
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
@@ -291,41 +305,49 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
   const int stages = min(kMaxStages, kSmemStages / (int)stage_bytes);
 
   if (warp == 0) {
-    if (lane == 0) {
-      // ------------------------------------------------------------ producer
-      if (n_rows > 0) {
-        ptx::prefetch_tensormap(&maps.a);
-        ptx::prefetch_tensormap(&maps.b);
-      }
-      uint32_t s = 0, use = 0;
-      bool ok = true;
-      for (int t = pair0; t < n_tiles && ok; t += pairs) {
-        const Tile tl = decode<kMode>(p, sh, start, first, t);
-        const int blocks = ceil_div(tl.k_len, kBlockK);
-        const int nh = tl.n_mma >> 1;                         // this CTA's columns of B
-        const int mc = tl.m0 + (int)rank * kCtaM;
-        // rows wholly past the matrix are not loaded (their output is not stored)
-        const bool a_in = mc < sh.m;
-        const int copies_b = kWgrad ? ceil_div(nh, 64) : (nh > 96 ? 1 : ceil_div(nh, 32));
-        const uint32_t bytes_b = kWgrad ? copies_b * kMnBlock : (nh > 96 ? 128u : 32u * copies_b) * 128u;
-        const uint32_t own_bytes = (a_in ? kBytesA : 0) + bytes_b;
-        const uint32_t pair_bytes = (tl.m0 + kCtaM < sh.m ? 2u : 1u) * kBytesA + 2u * bytes_b;
-        const bool ragged = kWgrad && (tl.k_len & 15) != 0;   // the last block needs its end zeroed
-        for (int kb = 0; kb < blocks; ++kb) {
-          ok = wait_bar<false>(ptx::smem_u32(&empty_bar[s]), (use & 1) ^ 1, ab, kRoleStage);
-          if (!ok) break;
-          const uint32_t full = ptx::smem_u32(&full_bar[s]);
-          uint32_t bar = ptx::mapa_shared(full, 0);
-          if (ragged && kb == blocks - 1) {
+    // -------------------------------------------------------------- producer
+    // The whole warp runs the loop on warp-uniform values and one elected lane
+    // issues: with the loop inside one lane, every copy took 100-170 cycles to
+    // issue and the issue bound the kernel.
+    const uint32_t rank_u = uniform(rank), base_u = uniform(smem_base);
+    const uint32_t full0 = uniform(ptx::smem_u32(&full_bar[0])), empty0 = uniform(ptx::smem_u32(&empty_bar[0]));
+    const uint32_t pair_full0 = uniform(ptx::mapa_shared(full0, 0));
+    const uint32_t tail0 = uniform(ptx::smem_u32(&tail_bar[0])), own_tail0 = uniform(ptx::mapa_shared(tail0, rank_u));
+    if (n_rows > 0 && ptx::elect_one()) {
+      ptx::prefetch_tensormap(&maps.a);
+      ptx::prefetch_tensormap(&maps.b);
+    }
+    __syncwarp();
+    uint32_t s = 0, use = 0;
+    bool ok = true;
+    for (int t = pair0; t < n_tiles && ok; t += pairs) {
+      const Tile tl = uniform(decode<kMode>(p, sh, start, first, t));
+      const int blocks = ceil_div(tl.k_len, kBlockK);
+      const int nh = tl.n_mma >> 1;                         // this CTA's columns of B
+      const int mc = tl.m0 + (int)rank_u * kCtaM;
+      // rows wholly past the matrix are not loaded (their output is not stored)
+      const bool a_in = mc < sh.m;
+      const int copies_b = kWgrad ? ceil_div(nh, 64) : (nh > 96 ? 1 : ceil_div(nh, 32));
+      const uint32_t bytes_b = kWgrad ? copies_b * kMnBlock : (nh > 96 ? 128u : 32u * copies_b) * 128u;
+      const uint32_t own_bytes = (a_in ? kBytesA : 0) + bytes_b;
+      const uint32_t pair_bytes = (tl.m0 + kCtaM < sh.m ? 2u : 1u) * kBytesA + 2u * bytes_b;
+      const bool ragged = kWgrad && (tl.k_len & 15) != 0;   // the last block needs its end zeroed
+      const int nc = tl.n0 + (int)rank_u * nh;
+      for (int kb = 0; kb < blocks; ++kb) {
+        ok = __all_sync(0xffffffffu, wait_bar<false>(empty0 + 8 * s, (use & 1) ^ 1, ab, kRoleStage));
+        if (!ok) break;
+        const bool tail = ragged && kb == blocks - 1;
+        const uint32_t bar = tail ? own_tail0 + 8 * s : pair_full0 + 8 * s;
+        const uint32_t sa = base_u + s * stage_bytes, sb = sa + kBytesA;
+        const int k0 = kb * kBlockK;
+        if (ptx::elect_one()) {
+          if (tail) {
             // lands on this CTA's own barrier, for its zeroing warp
-            bar = ptx::mapa_shared(ptx::smem_u32(&tail_bar[s]), rank);
-            ptx::mbar_arrive_expect_tx(ptx::smem_u32(&tail_bar[s]), own_bytes);
-            if (rank == 0) ptx::mbar_arrive(full);
-          } else if (rank == 0) {
-            ptx::mbar_arrive_expect_tx(full, pair_bytes);
+            ptx::mbar_arrive_expect_tx(tail0 + 8 * s, own_bytes);
+            if (rank_u == 0) ptx::mbar_arrive(full0 + 8 * s);
+          } else if (rank_u == 0) {
+            ptx::mbar_arrive_expect_tx(full0 + 8 * s, pair_bytes);
           }
-          const uint32_t sa = smem_base + s * stage_bytes, sb = sa + kBytesA;
-          const int k0 = kb * kBlockK;
           if (a_in) {
             if (!kAmn) {
               ptx::tma_load_3d_pair(sa, &maps.a, k0, mc, tl.e, bar);
@@ -335,79 +357,86 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
               ptx::tma_load_3d_pair(sa + kMnBlock, &maps.a, mc + 64, y, z, bar);
             }
           }
-          const int nc = tl.n0 + (int)rank * nh;
           if (kWgrad) {
-            for (int j = 0; j < copies_b; ++j)
-              ptx::tma_load_3d_pair(sb + j * kMnBlock, &maps.b, nc + 64 * j, tl.group + k0, 0, bar);
+            ptx::tma_load_3d_pair(sb, &maps.b, nc, tl.group + k0, 0, bar);
+            if (copies_b > 1) ptx::tma_load_3d_pair(sb + kMnBlock, &maps.b, nc + 64, tl.group + k0, 0, bar);
           } else if (nh > 96) {
             ptx::tma_load_3d_pair(sb, &maps.b128, k0, tl.group + nc, 0, bar);
           } else {
-            for (int j = 0; j < copies_b; ++j)
-              ptx::tma_load_3d_pair(sb + j * 4096, &maps.b, k0, tl.group + nc + 32 * j, 0, bar);
+            ptx::tma_load_3d_pair(sb, &maps.b, k0, tl.group + nc, 0, bar);
+            if (copies_b > 1) ptx::tma_load_3d_pair(sb + 4096, &maps.b, k0, tl.group + nc + 32, 0, bar);
+            if (copies_b > 2) ptx::tma_load_3d_pair(sb + 8192, &maps.b, k0, tl.group + nc + 64, 0, bar);
           }
-          if (++s == (uint32_t)stages) { s = 0; ++use; }
         }
-      }
-      // Drain: every stage this CTA filled has been read, so no copy into its
-      // shared memory is in flight (bounded).
-      for (int i = 0; i < stages; ++i) {
-        if (use > 0 || s > 0) {
-          const uint32_t last = s == 0 ? stages - 1 : s - 1, luse = s == 0 ? use - 1 : use;
-          if (!ptx::mbar_wait(ptx::smem_u32(&empty_bar[last]), luse & 1, kDrainNs)) break;
-          s = last;
-          use = luse;
-        }
+        __syncwarp();
+        if (++s == (uint32_t)stages) { s = 0; ++use; }
       }
     }
-    __syncwarp();
+    // Drain: every stage this CTA filled has been read, so no copy into its
+    // shared memory is in flight (bounded).
+    for (int i = 0; i < stages; ++i) {
+      if (use > 0 || s > 0) {
+        const uint32_t last = s == 0 ? stages - 1 : s - 1, luse = s == 0 ? use - 1 : use;
+        if (!__all_sync(0xffffffffu, ptx::mbar_wait(empty0 + 8 * last, luse & 1, kDrainNs))) break;
+        s = last;
+        use = luse;
+      }
+    }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
-      // --------------------------------------------------------- MMA issuer
+    if (rank == 0) {
+      // ----------------------------------------------------------- MMA issuer
+      const uint32_t base_u = uniform(smem_base), tmem_u = uniform(tmem_base);
+      const uint32_t full0 = uniform(ptx::smem_u32(&full_bar[0])), empty0 = uniform(ptx::smem_u32(&empty_bar[0]));
+      const uint32_t fixed0 = uniform(ptx::smem_u32(&fixed_bar[0]));
+      const uint32_t tfull0 = uniform(ptx::smem_u32(&tfull_bar[0])), tempty0 = uniform(ptx::smem_u32(&tempty_bar[0]));
       uint32_t s = 0, use = 0, acc_it = 0, fix_use = 0;
       bool ok = true;
       for (int t = pair0; t < n_tiles && ok; t += pairs) {
-        const Tile tl = decode<kMode>(p, sh, start, first, t);
+        const Tile tl = uniform(decode<kMode>(p, sh, start, first, t));
         const int blocks = ceil_div(tl.k_len, kBlockK);
         if (blocks == 0) continue;
         const bool ragged = kWgrad && (tl.k_len & 15) != 0;
         const uint32_t a = acc_it & 1;
-        ok = wait_bar<true>(ptx::smem_u32(&tempty_bar[a]), ((acc_it >> 1) & 1) ^ 1, ab, kRoleAccFree);
+        ok = __all_sync(0xffffffffu, wait_bar<true>(tempty0 + 8 * a, ((acc_it >> 1) & 1) ^ 1, ab, kRoleAccFree));
         if (!ok) break;
         ptx::tc_fence_after();
-        const uint32_t d_tmem = tmem_base + a * kAccCols;
+        const uint32_t d_tmem = tmem_u + a * kAccCols;
         const uint32_t idesc = ptx::idesc_bf16_f32(kPairM, (uint32_t)tl.n_mma, kWgrad ? 1u : 0u, kAmn ? 1u : 0u);
         for (int kb = 0; kb < blocks; ++kb) {
-          ok = wait_bar<true>(ptx::smem_u32(&full_bar[s]), use & 1, ab, kRoleOperands);
+          ok = __all_sync(0xffffffffu, wait_bar<true>(full0 + 8 * s, use & 1, ab, kRoleOperands));
           if (ok && ragged && kb == blocks - 1) {
-            ok = wait_bar<true>(ptx::smem_u32(&fixed_bar[s]), (fix_use >> s) & 1, ab, kRoleTail);
+            ok = __all_sync(0xffffffffu, wait_bar<true>(fixed0 + 8 * s, (fix_use >> s) & 1, ab, kRoleTail));
             fix_use ^= 1u << s;
           }
           if (!ok) break;
           ptx::tc_fence_after();
-          const uint32_t sa = smem_base + s * stage_bytes, sb = sa + kBytesA;
+          const uint32_t sa = base_u + s * stage_bytes, sb = sa + kBytesA;
+          // K-major: 16 elements (32 bytes) along the swizzle row, 8-row groups
+          // 1 KB apart.  MN-major: 16 K rows (2 KB), 64-element blocks 8 KB
+          // apart (leading offset), 8-row K groups 1 KB apart (stride offset).
+          const uint64_t adesc = ptx::smem_desc_sw128(sa, kAmn ? kMnBlock : 16, 1024);
+          const uint64_t bdesc = ptx::smem_desc_sw128(sb, kWgrad ? kMnBlock : 16, 1024);
           const int steps = min(kBlockK / 16, ceil_div(tl.k_len - kb * kBlockK, 16));
-          for (int k = 0; k < steps; ++k) {
-            // K-major: 16 elements (32 bytes) along the swizzle row, 8-row groups
-            // 1 KB apart.  MN-major: 16 K rows (2 KB), 64-element blocks 8 KB
-            // apart (leading offset), 8-row K groups 1 KB apart (stride offset).
-            const uint64_t adesc = kAmn ? ptx::smem_desc_sw128(sa + k * 2048, kMnBlock, 1024)
-                                        : ptx::smem_desc_sw128(sa + k * 32, 16, 1024);
-            const uint64_t bdesc = kWgrad ? ptx::smem_desc_sw128(sb + k * 2048, kMnBlock, 1024)
-                                          : ptx::smem_desc_sw128(sb + k * 32, 16, 1024);
-            ptx::umma_bf16_pair(d_tmem, adesc, bdesc, idesc, kb > 0 || k > 0 ? 1u : 0u);
+          if (ptx::elect_one()) {
+#pragma unroll
+            for (int k = 0; k < kBlockK / 16; ++k)
+              if (k < steps)
+                ptx::umma_bf16_pair(d_tmem, adesc + k * (kAmn ? 2048 >> 4 : 32 >> 4),
+                                    bdesc + k * (kWgrad ? 2048 >> 4 : 32 >> 4), idesc, kb > 0 || k > 0 ? 1u : 0u);
+            ptx::umma_commit_pair_multicast(empty0 + 8 * s, 0x3);
+            if (kb == blocks - 1) ptx::umma_commit_pair_multicast(tfull0 + 8 * a, 0x3);
           }
-          ptx::umma_commit_pair_multicast(ptx::smem_u32(&empty_bar[s]), 0x3);
+          __syncwarp();
           if (++s == (uint32_t)stages) { s = 0; ++use; }
         }
         if (!ok) break;
-        ptx::umma_commit_pair_multicast(ptx::smem_u32(&tfull_bar[a]), 0x3);
         ++acc_it;
       }
       // every MMA issued has completed before TMEM is released
-      ptx::umma_commit_pair_multicast(ptx::smem_u32(&drain_bar), 0x1);
+      if (ptx::elect_one()) ptx::umma_commit_pair_multicast(ptx::smem_u32(&drain_bar), 0x1);
+      __syncwarp();
       ptx::mbar_wait(ptx::smem_u32(&drain_bar), 0, kDrainNs);
     }
-    __syncwarp();
   } else if (warp == 2) {
     // ---------------------------------------------- zeroing of group ends
     // The last block of a group whose length is no multiple of 16 holds, after

@@ -22,6 +22,13 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const void* tmap,
       : "memory");
 }
 
+// One lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // Value of a shared-memory variable of any CTA of the cluster (a
 // shared::cluster address).
 __device__ __forceinline__ int32_t ld_shared_cluster_s32(uint32_t addr) {
