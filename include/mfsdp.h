@@ -671,8 +671,8 @@ int mfsdp_expert_weight_grad(const void* dy, int64_t dy_ld, const void* x, int64
  * workspace (synchronises `stream`): MFSDP_OK, or MFSDP_ERR_DEVICE_TIMEOUT if
  * one of its bounded waits gave up (its outputs are then undefined); *detail (may
  * be NULL) receives the role that waited.  Products: 1 a pipeline stage, 2 its
- * operands, 3 a drained and 4 a finished accumulator, 5 a group's zeroed end; a
- * wait gives up after 2 s plus 64 ns for each element of the contraction.
+ * operands, 3 a drained and 4 a finished accumulator; a wait gives up after 2 s
+ * plus 64 ns for each element of the contraction.
  * Embedding gradient: 1 a pipeline stage, 2 its rows; 2 s.  Every call that
  * launches clears the word. */
 int mfsdp_op_device_status(const void* workspace, void* stream, int32_t* detail);

@@ -17,17 +17,19 @@
 // No operand is transposed or copied first.  A matrix edge needs no code: the
 // maps are bounded by the matrix (three dimensions, the expert the last) and
 // fill with zeros.  A group's edge does: on the N side the extra tokens are
-// computed and not stored; on the K side (weight gradient) the MMAs stop at
-// the last 16 tokens, and the rows of those past the group's end, which hold
-// the next group's tokens, are zeroed in shared memory in both operands.
+// computed and not stored; on the K side (weight gradient) a group's last
+// tokens past a multiple of 16, the MMA's K, come from a copy padded to 16 rows with
+// zeros, which a small kernel makes first: 16 rows of both operands an expert.
+// (Zeroing the next group's rows in shared memory instead, in both CTAs of the pair,
+// cost the issuer 1800-1950 cycles a tile of 5300; zeroing one operand
+// would let a NaN of the other through.)
 //
 // CTA pairs (one CTA per SM, cta_group::2) take tiles of 256 x up to 256
 // round-robin from a list that every CTA works out from `starts`, expert by
 // expert, so a wave's tiles share their operands in L2.  A CTA loads its 128
 // rows of A and its half of B, 32 KB per 64 of K: 64 bytes a clock at the full
 // MMA rate, where a CTA alone on 128 x 256 would need 96.  Warp roles: 0
-// producer, 1 MMA issuer (even CTA), 2 zeroes group ends (weight gradient),
-// 4-11 epilogue; two accumulators in TMEM let the epilogue overlap the next
+// producer, 1 MMA issuer (even CTA), 4-11 epilogue; two accumulators in TMEM let the epilogue overlap the next
 // tile.  The pipeline has as many stages as shared memory holds at the
 // launch's widest tile: 6 of 32 KB for 256 tokens, 9 of 20 KB for a few tokens,
 // where the product is bound by reading W and bytes in flight count.
@@ -50,7 +52,10 @@ constexpr int kStepN = 32;                // N granularity of the pair MMA
 constexpr int kBlockK = 64;               // K of a stage: one 128-byte swizzle row of bf16
 constexpr int kBytesA = kCtaM * kBlockK * 2;          // 16 KB
 constexpr int kMnBlock = 64 * kBlockK * 2;            // 8 KB: 64 MN elements x 64 K rows (MN-major)
+constexpr int kEnd = 16;                              // K of one MMA: rows of a group's padded end
+constexpr int kEndBlock = 64 * kEnd * 2;
 constexpr int kSmemStages = 6 * 32768;
+constexpr int kEpiStage = 2048;                       // staging of an epilogue warp
 constexpr int kMaxStages = 9;               // of 20 KB
 constexpr int kEpiWarps = 8;
 constexpr int kFirstEpiWarp = 4;
@@ -62,7 +67,8 @@ constexpr uint64_t kDrainNs = 2000000000ull;          // limit of the waits that
 struct Maps {
   CUtensorMap a;      // box 64 x 128 (K-major A) or 64 x 64
   CUtensorMap b;      // box 64 x 32 (K-major B) or 64 x 64
-  CUtensorMap b128;   // box 64 x 128 (K-major B of a full tile)
+  CUtensorMap c;      // box 64 x 128 (K-major B of a full tile); weight gradient: the padded ends of A, box 64 x 16
+  CUtensorMap d;      // weight gradient: the padded ends of B, box 64 x 16
 };
 
 // First failing wait of a launch: (role << 0); the wait's limit.
@@ -71,7 +77,7 @@ struct Abort {
   int32_t* status;
   uint64_t limit_ns;
 };
-enum Role : int32_t { kRoleStage = 1, kRoleOperands = 2, kRoleAccFree = 3, kRoleAccFull = 4, kRoleTail = 5 };
+enum Role : int32_t { kRoleStage = 1, kRoleOperands = 2, kRoleAccFree = 3, kRoleAccFull = 4 };
 
 template <bool kCluster>
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const Abort& ab, int32_t role) {
@@ -109,6 +115,12 @@ struct Shape {
 };
 
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+// Stages of a contraction of length k: whole blocks of 64 (the last one may be
+// short), and in the weight gradient the padded end of a length that is no multiple of 16.
+template <bool kWgrad>
+__device__ __forceinline__ int blocks_of(int k) {
+  return kWgrad ? ceil_div(k & ~(kEnd - 1), kBlockK) + ((k & (kEnd - 1)) != 0) : ceil_div(k, kBlockK);
+}
 // n split over `parts` tiles, each a multiple of 32 wide.
 __device__ __forceinline__ int even_width(int n, int parts) {
   return (ceil_div(n, parts) + kStepN - 1) / kStepN * kStepN;
@@ -149,67 +161,156 @@ __device__ __forceinline__ Tile decode(const ExpertArgs& p, const Shape& sh, con
 
 // A value that all lanes hold, as the compiler can see.
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
-__device__ __forceinline__ Tile uniform(const Tile& t) {
-  Tile r;
-  r.e = __shfl_sync(0xffffffffu, t.e, 0);
-  r.group = __shfl_sync(0xffffffffu, t.group, 0);
-  r.m0 = __shfl_sync(0xffffffffu, t.m0, 0);
-  r.n0 = __shfl_sync(0xffffffffu, t.n0, 0);
-  r.n = __shfl_sync(0xffffffffu, t.n, 0);
-  r.n_mma = __shfl_sync(0xffffffffu, t.n_mma, 0);
-  r.k_len = __shfl_sync(0xffffffffu, t.k_len, 0);
-  return r;
-}
+
+// The tiles a pair takes: pair0, pair0 + pairs, ...  Finding a tile's place
+// takes divisions and a search, ~1000 cycles, of the ~3000 a small tile takes
+// in all; so a warp finds 32 tiles at a time, one a lane, and hands them out.
+template <int kMode>
+struct TileWalk {
+  const ExpertArgs& p;
+  const Shape& sh;
+  const int32_t* start;
+  const int32_t* first;
+  int t, pairs, n_tiles;
+  int held;               // tiles left in `mine`
+  Tile mine;
+
+  __device__ __forceinline__ TileWalk(const ExpertArgs& p_, const Shape& sh_, const int32_t* start_,
+                                      const int32_t* first_, int pair0, int pairs_, int n_tiles_)
+      : p(p_), sh(sh_), start(start_), first(first_), t(pair0), pairs(pairs_), n_tiles(n_tiles_), held(0) {}
+  // The next tile, the same in all lanes; false after the last.
+  __device__ __forceinline__ bool next(Tile& r) {
+    if (t >= n_tiles) return false;
+    if (held == 0) {
+      const int64_t ahead = t + (int64_t)(threadIdx.x & 31) * pairs;
+      if (ahead < n_tiles) mine = decode<kMode>(p, sh, start, first, (int)ahead);
+      held = 32;
+      __syncwarp();
+    }
+    const int lane = 32 - held;
+    r.e = __shfl_sync(0xffffffffu, mine.e, lane);
+    r.group = __shfl_sync(0xffffffffu, mine.group, lane);
+    r.m0 = __shfl_sync(0xffffffffu, mine.m0, lane);
+    r.n0 = __shfl_sync(0xffffffffu, mine.n0, lane);
+    r.n = __shfl_sync(0xffffffffu, mine.n, lane);
+    r.n_mma = __shfl_sync(0xffffffffu, mine.n_mma, lane);
+    r.k_len = __shfl_sync(0xffffffffu, mine.k_len, lane);
+    --held;
+    t += pairs;
+    return true;
+  }
+};
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// 32 consecutive columns of one row of a weight gradient.
-__device__ __forceinline__ void store_row(const ExpertArgs& p, int64_t at, int n, const float (&v)[32]) {
-  if (p.out_vec && n == 32) {
-    if (p.out_bf16) {
-      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + at;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t w[8], old[8];
-        if (p.accumulate) ptx::ld_v8(o + 16 * h, old);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          float a = v[16 * h + 2 * k], b = v[16 * h + 2 * k + 1];
-          if (p.accumulate) { a += bf16_lo(old[k]); b += bf16_hi(old[k]); }
-          const __nv_bfloat162 q = __floats2bfloat162_rn(a, b);
-          w[k] = *reinterpret_cast<const uint32_t*>(&q);
-        }
-        ptx::st_v8(o + 16 * h, w);
-      }
-    } else {
-      float* o = static_cast<float*>(p.out) + at;
-#pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        uint32_t w[8], old[8];
-        if (p.accumulate) ptx::ld_v8(o + 8 * h, old);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          w[k] = __float_as_uint(p.accumulate ? v[8 * h + k] + __uint_as_float(old[k]) : v[8 * h + k]);
-        ptx::st_v8(o + 8 * h, w);
-      }
-    }
-    return;
-  }
+// `n` (at most 32) consecutive columns of one row of a weight gradient, element
+// by element: rows that do not start on 16-byte boundaries, and edges.
+template <bool kBf16, bool kAccumulate>
+__device__ __forceinline__ void store_row(const ExpertArgs& p, int64_t at, int n, const uint32_t (&v)[32]) {
 #pragma unroll
   for (int k = 0; k < 32; ++k) {
     if (k >= n) continue;
-    if (p.out_bf16) {
+    const float x = __uint_as_float(v[k]);
+    if constexpr (kBf16) {
       __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + at + k;
-      *o = __float2bfloat16_rn(p.accumulate ? v[k] + __bfloat162float(*o) : v[k]);
+      *o = __float2bfloat16_rn(kAccumulate ? x + __bfloat162float(*o) : x);
     } else {
       float* o = static_cast<float*>(p.out) + at + k;
-      *o = p.accumulate ? v[k] + *o : v[k];
+      *o = kAccumulate ? x + *o : x;
     }
   }
 }
 
-template <int kMode>
+// 128 bytes of each of a warp's 32 rows (64 bf16 or 32 fp32 columns), lane l
+// holding row l's in `w`.  A lane's own 16- or 32-byte stores to its row would
+// touch 32 lines an instruction (that took the epilogue 5000 cycles a tile,
+// twice the MMAs'); through the warp's 2 KB of shared memory, 16 rows at a
+// time, an instruction moves 4 whole lines.  Chunk c of row r sits at c ^ (r & 7).
+// Rows from `rows` on and 16-byte chunks from `chunks` on are left alone.
+__device__ __forceinline__ void put_rows(uint8_t* stage, const uint32_t (&w)[32], uint8_t* out, int64_t pitch,
+                                         int rows, int chunks) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if ((lane >> 4) == h) {
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        *reinterpret_cast<uint4*>(stage + (lane & 15) * 128 + ((c ^ (lane & 7)) << 4)) =
+            make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int r = 4 * k + (lane >> 3), c = lane & 7;
+      const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + ((c ^ (r & 7)) << 4));
+      if (16 * h + r < rows && c < chunks) __stcs(reinterpret_cast<uint4*>(out + (16 * h + r) * pitch + 16 * c), v);
+    }
+    __syncwarp();
+  }
+}
+// The way back: each lane receives its row's 128 bytes.
+__device__ __forceinline__ void get_rows(uint8_t* stage, uint32_t (&w)[32], const uint8_t* in, int64_t pitch, int rows,
+                                         int chunks) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int r = 4 * k + (lane >> 3), c = lane & 7;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (16 * h + r < rows && c < chunks) v = *reinterpret_cast<const uint4*>(in + (16 * h + r) * pitch + 16 * c);
+      *reinterpret_cast<uint4*>(stage + r * 128 + ((c ^ (r & 7)) << 4)) = v;
+    }
+    __syncwarp();
+    if ((lane >> 4) == h) {
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const uint4 v = *reinterpret_cast<const uint4*>(stage + (lane & 15) * 128 + ((c ^ (lane & 7)) << 4));
+        w[4 * c] = v.x; w[4 * c + 1] = v.y; w[4 * c + 2] = v.z; w[4 * c + 3] = v.w;
+      }
+    }
+    __syncwarp();
+  }
+}
+
+// One chunk of a weight gradient's rows from the accumulator at `taddr`: 64
+// columns to bf16, or 32 to fp32.  `last`: then hands the accumulator back.
+template <bool kBf16, bool kAccumulate, typename Release>
+__device__ __forceinline__ void put_chunk(const ExpertArgs& p, uint8_t* stage, uint32_t taddr, int64_t at, int rows,
+                                          int cols, bool last, Release release) {
+  constexpr int kEsz = kBf16 ? 2 : 4;
+  uint8_t* out = static_cast<uint8_t*>(p.out) + at * kEsz;
+  const int64_t pitch = p.out_ld * kEsz;
+  const int chunks = min(8, cols * kEsz / 16);
+  uint32_t w[32], acc[32];
+  if constexpr (kAccumulate) get_rows(stage, w, out, pitch, rows, chunks);
+#pragma unroll
+  for (int h = 0; h < (kBf16 ? 2 : 1); ++h) {
+    ptx::tmem_ld_32x32b_x32(taddr + 32 * h, acc);
+    ptx::tmem_ld_wait();
+    if (last && h == (kBf16 ? 1 : 0)) release();
+#pragma unroll
+    for (int k = 0; k < (kBf16 ? 16 : 32); ++k) {
+      if constexpr (kBf16) {
+        float a = __uint_as_float(acc[2 * k]), b = __uint_as_float(acc[2 * k + 1]);
+        if constexpr (kAccumulate) {
+          a += bf16_lo(w[16 * h + k]);
+          b += bf16_hi(w[16 * h + k]);
+        }
+        const __nv_bfloat162 q = __floats2bfloat162_rn(a, b);
+        w[16 * h + k] = *reinterpret_cast<const uint32_t*>(&q);
+      } else {
+        w[k] = kAccumulate ? __float_as_uint(__uint_as_float(acc[k]) + __uint_as_float(w[k])) : acc[k];
+      }
+    }
+  }
+  put_rows(stage, w, out, pitch, rows, chunks);
+}
+
+// kBf16: the output's type.  Weight gradient: kAccumulate, and kVec: the rows
+// of dW start on 16-byte boundaries.
+template <int kMode, bool kBf16, bool kAccumulate, bool kVec>
 __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_constant__ ExpertArgs p,
                                                              const __grid_constant__ Maps maps) {
   constexpr bool kWgrad = kMode == kExpertWeightGrad;
@@ -220,8 +321,6 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
   __shared__ int32_t widest;                            // columns of the launch's widest tile
   __shared__ __align__(8) uint64_t full_bar[kMaxStages];    // even CTA: both CTAs' operands have landed
   __shared__ __align__(8) uint64_t empty_bar[kMaxStages];
-  __shared__ __align__(8) uint64_t tail_bar[kMaxStages];    // this CTA's operands of a group's ragged end
-  __shared__ __align__(8) uint64_t fixed_bar[kMaxStages];   // even CTA: both CTAs have zeroed past the end
   __shared__ __align__(8) uint64_t tfull_bar[2], tempty_bar[2], drain_bar;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
@@ -250,8 +349,6 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
     for (int s = 0; s < kMaxStages; ++s) {
       ptx::mbar_init(ptx::smem_u32(&full_bar[s]), 1);
       ptx::mbar_init(ptx::smem_u32(&empty_bar[s]), 1);
-      ptx::mbar_init(ptx::smem_u32(&tail_bar[s]), 1);
-      ptx::mbar_init(ptx::smem_u32(&fixed_bar[s]), 2);
     }
     for (int a = 0; a < 2; ++a) {
       ptx::mbar_init(ptx::smem_u32(&tfull_bar[a]), 1);
@@ -296,8 +393,12 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
   ptx::tc_fence_after();
   const uint32_t tmem_base = tmem_slot;
   const Abort ab{&abort_flag, p.status, p.wait_limit_ns};
+  // packed operands and padded ends come from the kernels before this one
+  ptx::wait_dependencies();
+  ptx::fence_proxy_async_global();
   const int n_tiles = kWgrad ? p.n_experts * sh.tiles_m * sh.tiles_n : first[p.n_experts];
-  const int pair0 = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  TileWalk<kMode> walk(p, sh, start, first, blockIdx.x >> 1, gridDim.x >> 1, n_tiles);
+  Tile tl;
   // Shared memory of a stage: A, then this CTA's half of B.
   const int wide = kWgrad ? sh.width_n : widest;
   const int bytes_b_max = kWgrad ? ceil_div(wide / 2, 64) * kMnBlock : (wide / 2 > 96 ? 128 : ceil_div(wide / 2, 32) * 32) * 128;
@@ -312,60 +413,63 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
     const uint32_t rank_u = uniform(rank), base_u = uniform(smem_base);
     const uint32_t full0 = uniform(ptx::smem_u32(&full_bar[0])), empty0 = uniform(ptx::smem_u32(&empty_bar[0]));
     const uint32_t pair_full0 = uniform(ptx::mapa_shared(full0, 0));
-    const uint32_t tail0 = uniform(ptx::smem_u32(&tail_bar[0])), own_tail0 = uniform(ptx::mapa_shared(tail0, rank_u));
     if (n_rows > 0 && ptx::elect_one()) {
       ptx::prefetch_tensormap(&maps.a);
       ptx::prefetch_tensormap(&maps.b);
+      ptx::prefetch_tensormap(&maps.c);
     }
     __syncwarp();
     uint32_t s = 0, use = 0;
     bool ok = true;
-    for (int t = pair0; t < n_tiles && ok; t += pairs) {
-      const Tile tl = uniform(decode<kMode>(p, sh, start, first, t));
-      const int blocks = ceil_div(tl.k_len, kBlockK);
+    while (ok && walk.next(tl)) {
+      const int blocks = blocks_of<kWgrad>(tl.k_len);
       const int nh = tl.n_mma >> 1;                         // this CTA's columns of B
       const int mc = tl.m0 + (int)rank_u * kCtaM;
       // rows wholly past the matrix are not loaded (their output is not stored)
       const bool a_in = mc < sh.m;
       const int copies_b = kWgrad ? ceil_div(nh, 64) : (nh > 96 ? 1 : ceil_div(nh, 32));
       const uint32_t bytes_b = kWgrad ? copies_b * kMnBlock : (nh > 96 ? 128u : 32u * copies_b) * 128u;
-      const uint32_t own_bytes = (a_in ? kBytesA : 0) + bytes_b;
       const uint32_t pair_bytes = (tl.m0 + kCtaM < sh.m ? 2u : 1u) * kBytesA + 2u * bytes_b;
-      const bool ragged = kWgrad && (tl.k_len & 15) != 0;   // the last block needs its end zeroed
+      const bool ragged = kWgrad && (tl.k_len & (kEnd - 1)) != 0;
       const int nc = tl.n0 + (int)rank_u * nh;
       for (int kb = 0; kb < blocks; ++kb) {
         ok = __all_sync(0xffffffffu, wait_bar<false>(empty0 + 8 * s, (use & 1) ^ 1, ab, kRoleStage));
         if (!ok) break;
-        const bool tail = ragged && kb == blocks - 1;
-        const uint32_t bar = tail ? own_tail0 + 8 * s : pair_full0 + 8 * s;
+        const uint32_t bar = pair_full0 + 8 * s;
         const uint32_t sa = base_u + s * stage_bytes, sb = sa + kBytesA;
         const int k0 = kb * kBlockK;
         if (ptx::elect_one()) {
-          if (tail) {
-            // lands on this CTA's own barrier, for its zeroing warp
-            ptx::mbar_arrive_expect_tx(tail0 + 8 * s, own_bytes);
-            if (rank_u == 0) ptx::mbar_arrive(full0 + 8 * s);
-          } else if (rank_u == 0) {
-            ptx::mbar_arrive_expect_tx(full0 + 8 * s, pair_bytes);
-          }
-          if (a_in) {
-            if (!kAmn) {
-              ptx::tma_load_3d_pair(sa, &maps.a, k0, mc, tl.e, bar);
-            } else {
-              const int y = kWgrad ? tl.group + k0 : k0, z = kWgrad ? 0 : tl.e;
-              ptx::tma_load_3d_pair(sa, &maps.a, mc, y, z, bar);
-              ptx::tma_load_3d_pair(sa + kMnBlock, &maps.a, mc + 64, y, z, bar);
+          if (ragged && kb == blocks - 1) {
+            // 16 rows: a quarter of the bytes
+            if (rank_u == 0) ptx::mbar_arrive_expect_tx(full0 + 8 * s, pair_bytes * kEnd / kBlockK);
+            const int y = tl.e * kEnd;
+            if (a_in) {
+              ptx::tma_load_3d_pair(sa, &maps.c, mc, y, 0, bar);
+              ptx::tma_load_3d_pair(sa + kMnBlock, &maps.c, mc + 64, y, 0, bar);
             }
-          }
-          if (kWgrad) {
-            ptx::tma_load_3d_pair(sb, &maps.b, nc, tl.group + k0, 0, bar);
-            if (copies_b > 1) ptx::tma_load_3d_pair(sb + kMnBlock, &maps.b, nc + 64, tl.group + k0, 0, bar);
-          } else if (nh > 96) {
-            ptx::tma_load_3d_pair(sb, &maps.b128, k0, tl.group + nc, 0, bar);
+            ptx::tma_load_3d_pair(sb, &maps.d, nc, y, 0, bar);
+            if (copies_b > 1) ptx::tma_load_3d_pair(sb + kMnBlock, &maps.d, nc + 64, y, 0, bar);
           } else {
-            ptx::tma_load_3d_pair(sb, &maps.b, k0, tl.group + nc, 0, bar);
-            if (copies_b > 1) ptx::tma_load_3d_pair(sb + 4096, &maps.b, k0, tl.group + nc + 32, 0, bar);
-            if (copies_b > 2) ptx::tma_load_3d_pair(sb + 8192, &maps.b, k0, tl.group + nc + 64, 0, bar);
+            if (rank_u == 0) ptx::mbar_arrive_expect_tx(full0 + 8 * s, pair_bytes);
+            if (a_in) {
+              if (!kAmn) {
+                ptx::tma_load_3d_pair(sa, &maps.a, k0, mc, tl.e, bar);
+              } else {
+                const int y = kWgrad ? tl.group + k0 : k0, z = kWgrad ? 0 : tl.e;
+                ptx::tma_load_3d_pair(sa, &maps.a, mc, y, z, bar);
+                ptx::tma_load_3d_pair(sa + kMnBlock, &maps.a, mc + 64, y, z, bar);
+              }
+            }
+            if (kWgrad) {
+              ptx::tma_load_3d_pair(sb, &maps.b, nc, tl.group + k0, 0, bar);
+              if (copies_b > 1) ptx::tma_load_3d_pair(sb + kMnBlock, &maps.b, nc + 64, tl.group + k0, 0, bar);
+            } else if (nh > 96) {
+              ptx::tma_load_3d_pair(sb, &maps.c, k0, tl.group + nc, 0, bar);
+            } else {
+              ptx::tma_load_3d_pair(sb, &maps.b, k0, tl.group + nc, 0, bar);
+              if (copies_b > 1) ptx::tma_load_3d_pair(sb + 4096, &maps.b, k0, tl.group + nc + 32, 0, bar);
+              if (copies_b > 2) ptx::tma_load_3d_pair(sb + 8192, &maps.b, k0, tl.group + nc + 64, 0, bar);
+            }
           }
         }
         __syncwarp();
@@ -387,15 +491,13 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
       // ----------------------------------------------------------- MMA issuer
       const uint32_t base_u = uniform(smem_base), tmem_u = uniform(tmem_base);
       const uint32_t full0 = uniform(ptx::smem_u32(&full_bar[0])), empty0 = uniform(ptx::smem_u32(&empty_bar[0]));
-      const uint32_t fixed0 = uniform(ptx::smem_u32(&fixed_bar[0]));
       const uint32_t tfull0 = uniform(ptx::smem_u32(&tfull_bar[0])), tempty0 = uniform(ptx::smem_u32(&tempty_bar[0]));
-      uint32_t s = 0, use = 0, acc_it = 0, fix_use = 0;
+      uint32_t s = 0, use = 0, acc_it = 0;
       bool ok = true;
-      for (int t = pair0; t < n_tiles && ok; t += pairs) {
-        const Tile tl = uniform(decode<kMode>(p, sh, start, first, t));
-        const int blocks = ceil_div(tl.k_len, kBlockK);
+      while (ok && walk.next(tl)) {
+        const int blocks = blocks_of<kWgrad>(tl.k_len);
         if (blocks == 0) continue;
-        const bool ragged = kWgrad && (tl.k_len & 15) != 0;
+        const bool ragged = kWgrad && (tl.k_len & (kEnd - 1)) != 0;
         const uint32_t a = acc_it & 1;
         ok = __all_sync(0xffffffffu, wait_bar<true>(tempty0 + 8 * a, ((acc_it >> 1) & 1) ^ 1, ab, kRoleAccFree));
         if (!ok) break;
@@ -404,10 +506,6 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
         const uint32_t idesc = ptx::idesc_bf16_f32(kPairM, (uint32_t)tl.n_mma, kWgrad ? 1u : 0u, kAmn ? 1u : 0u);
         for (int kb = 0; kb < blocks; ++kb) {
           ok = __all_sync(0xffffffffu, wait_bar<true>(full0 + 8 * s, use & 1, ab, kRoleOperands));
-          if (ok && ragged && kb == blocks - 1) {
-            ok = __all_sync(0xffffffffu, wait_bar<true>(fixed0 + 8 * s, (fix_use >> s) & 1, ab, kRoleTail));
-            fix_use ^= 1u << s;
-          }
           if (!ok) break;
           ptx::tc_fence_after();
           const uint32_t sa = base_u + s * stage_bytes, sb = sa + kBytesA;
@@ -416,7 +514,9 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
           // apart (leading offset), 8-row K groups 1 KB apart (stride offset).
           const uint64_t adesc = ptx::smem_desc_sw128(sa, kAmn ? kMnBlock : 16, 1024);
           const uint64_t bdesc = ptx::smem_desc_sw128(sb, kWgrad ? kMnBlock : 16, 1024);
-          const int steps = min(kBlockK / 16, ceil_div(tl.k_len - kb * kBlockK, 16));
+          // K-major operands past the contraction's end are zeros of the copy's fill
+          const int left = tl.k_len - kb * kBlockK;
+          const int steps = ragged && kb == blocks - 1 ? 1 : min(kBlockK / 16, kWgrad ? left / 16 : ceil_div(left, 16));
           if (ptx::elect_one()) {
 #pragma unroll
             for (int k = 0; k < kBlockK / 16; ++k)
@@ -437,54 +537,29 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
       __syncwarp();
       ptx::mbar_wait(ptx::smem_u32(&drain_bar), 0, kDrainNs);
     }
-  } else if (warp == 2) {
-    // ---------------------------------------------- zeroing of group ends
-    // The last block of a group whose length is no multiple of 16 holds, after
-    // its own tokens, the next group's: the MMA stops at the next multiple of
-    // 16, and the rows up to there are zeroed in both operands (not in one: a
-    // NaN of the other would survive a product with zero).
-    if (kWgrad) {
-      uint32_t s = 0, tail_use = 0;
-      bool ok = true;
-      for (int t = pair0; t < n_tiles && ok; t += pairs) {
-        const Tile tl = decode<kMode>(p, sh, start, first, t);
-        const int blocks = ceil_div(tl.k_len, kBlockK);
-        if (blocks == 0) continue;
-        const uint32_t st = (s + blocks - 1) % stages;
-        s = (s + blocks) % stages;
-        if ((tl.k_len & 15) == 0) continue;
-        ok = __all_sync(0xffffffffu, wait_bar<false>(ptx::smem_u32(&tail_bar[st]), (tail_use >> st) & 1, ab, kRoleTail));
-        if (!ok) break;
-        tail_use ^= 1u << st;
-        const int valid = tl.k_len - (blocks - 1) * kBlockK, pad = (16 - (valid & 15)) & 15;
-        uint8_t* base = smem_raw + (smem_base - ptx::smem_u32(smem_raw)) + (size_t)st * stage_bytes;
-        const int mn_blocks = 2 + ceil_div(tl.n_mma >> 1, 64);     // A's two, then B's
-        for (int i = lane; i < mn_blocks * pad * 8; i += 32) {
-          const int blk = i / (pad * 8), r = i - blk * pad * 8;
-          *reinterpret_cast<uint4*>(base + (size_t)blk * kMnBlock + (valid + (r >> 3)) * 128 + (r & 7) * 16) =
-              make_uint4(0, 0, 0, 0);
-        }
-        ptx::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_u32(&fixed_bar[st]), 0));
-      }
-    }
   } else if (warp >= kFirstEpiWarp) {
     // -------------------------------------------------------------- epilogue
     // Warp w reads TMEM lane quadrant w % 4; the two warps of a quadrant take
     // alternate chunks of 32 columns.
     const int quad = warp & 3, half = (warp - kFirstEpiWarp) >> 2;
+    uint8_t* const stage = smem_raw + (smem_base - ptx::smem_u32(smem_raw)) + kSmemStages + (warp - kFirstEpiWarp) * kEpiStage;
+    constexpr int kEsz = kBf16 ? 2 : 4;
+    constexpr int kWidth = kWgrad && kVec ? 128 / kEsz : 32;     // columns of a chunk
     uint32_t acc_it = 0;
-    for (int t = pair0; t < n_tiles; t += pairs) {
-      const Tile tl = decode<kMode>(p, sh, start, first, t);
-      const int m = tl.m0 + (int)rank * kCtaM + quad * 32 + lane;
+    while (walk.next(tl)) {
+      const int row0 = tl.m0 + (int)rank * kCtaM + quad * 32, m = row0 + lane;
+      const int64_t at0 = kWgrad ? tl.e * p.out_stride + row0 * p.out_ld + tl.n0 : 0;      // the warp's first row
       if (kWgrad && tl.k_len == 0) {
-        if (!p.accumulate && m < sh.m) {
-          float z[32];
+        if (kAccumulate) continue;
+        uint32_t z[32];
 #pragma unroll
-          for (int j = 0; j < 32; ++j) z[j] = 0.f;
-          for (int c = 32 * half; c < tl.n; c += 64)
-            store_row(p, tl.e * p.out_stride + m * p.out_ld + tl.n0 + c, min(32, tl.n - c), z);
+        for (int j = 0; j < 32; ++j) z[j] = 0;
+        for (int c = kWidth * half; c < tl.n; c += 2 * kWidth) {
+          if (kVec)
+            put_rows(stage, z, static_cast<uint8_t*>(p.out) + (at0 + c) * kEsz, p.out_ld * kEsz, sh.m - row0,
+                     min(8, (tl.n - c) * kEsz / 16));
+          else if (m < sh.m)
+            store_row<kBf16, false>(p, at0 + lane * p.out_ld + c, min(32, tl.n - c), z);
         }
         continue;
       }
@@ -493,45 +568,40 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
         break;
       ptx::tc_fence_after();
       const uint32_t t_row = tmem_base + a * kAccCols + ((uint32_t)(quad * 32) << 16);
-      for (int c = 32 * half; c < tl.n_mma; c += 64) {
-        uint32_t r[32];
-        __syncwarp();
-        ptx::tmem_ld_32x32b_x32(t_row + (uint32_t)c, r);
-        ptx::tmem_ld_wait();
-        if (c + 64 >= tl.n_mma) {
-          // this warp's last read of the accumulator: hand it back
-          ptx::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive_signal(ptx::mapa_shared(ptx::smem_u32(&tempty_bar[a]), 0));
-        }
-        if (m >= sh.m) continue;                  // the warp meets again at the next chunk
-        const int cnt = min(32, tl.n - c);
-        if (kWgrad) {
-          float v[32];
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
-          store_row(p, tl.e * p.out_stride + m * p.out_ld + tl.n0 + c, cnt, v);
-        } else {
-          // lanes are neighbours in memory: 64 (bf16) or 128 bytes a token
-          const int64_t at = (int64_t)(tl.group + tl.n0 + c) * p.out_ld + m;
-          if (p.out_bf16) {
-            __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + at;
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (j < cnt) o[j * p.out_ld] = __float2bfloat16_rn(__uint_as_float(r[j]));
-          } else {
-            float* o = static_cast<float*>(p.out) + at;
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (j < cnt) o[j * p.out_ld] = __uint_as_float(r[j]);
-          }
-        }
-      }
-      if (32 * half >= tl.n_mma) {
-        // no chunk for this warp
+      // this warp's reads of the accumulator are done: hand it back
+      auto release = [&]() {
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive_signal(ptx::mapa_shared(ptx::smem_u32(&tempty_bar[a]), 0));
+      };
+      if (kWidth * half >= tl.n_mma) release();           // no chunk for this warp
+      for (int c = kWidth * half; c < tl.n_mma; c += 2 * kWidth) {
+        const bool last = c + 2 * kWidth >= tl.n_mma;
+        __syncwarp();
+        if constexpr (kWgrad && kVec) {
+          put_chunk<kBf16, kAccumulate>(p, stage, t_row + c, at0 + c, sh.m - row0, tl.n - c, last, release);
+          continue;
+        }
+        uint32_t r[32];
+        ptx::tmem_ld_32x32b_x32(t_row + (uint32_t)c, r);
+        ptx::tmem_ld_wait();
+        if (last) release();
+        if (m >= sh.m) continue;                         // the warp meets again at the next chunk
+        const int cnt = min(32, tl.n - c);
+        if constexpr (kWgrad) {
+          store_row<kBf16, kAccumulate>(p, at0 + lane * p.out_ld + c, cnt, r);
+        } else {
+          // lanes are neighbours in memory: 64 (bf16) or 128 bytes a token
+          const int64_t at = (int64_t)(tl.group + tl.n0 + c) * p.out_ld + m;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            if (j >= cnt) continue;
+            if constexpr (kBf16)
+              static_cast<__nv_bfloat16*>(p.out)[at + j * p.out_ld] = __float2bfloat16_rn(__uint_as_float(r[j]));
+            else
+              static_cast<float*>(p.out)[at + j * p.out_ld] = __uint_as_float(r[j]);
+          }
+        }
       }
       ++acc_it;
     }
@@ -542,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
       for (int64_t i = (int64_t)blockIdx.x * (32 * kEpiWarps) + threadIdx.x - 32 * kFirstEpiWarp;
            i < (n_rows - lo) * width; i += step) {
         const int64_t at = (lo + i / width) * p.out_ld + i % width;
-        if (p.out_bf16) static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(0.f);
+        if constexpr (kBf16) static_cast<uint16_t*>(p.out)[at] = 0;
         else static_cast<float*>(p.out)[at] = 0.f;
       }
     }
@@ -564,6 +634,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
 // `starts`, matrix e (its `rows` rows) is copied only if its group has a token.
 __global__ void __launch_bounds__(256) pack_kernel(const uint16_t* src, int64_t stride, int64_t ld, uint16_t* dst,
                                                    int64_t rows, int width, int width8, const int32_t* starts) {
+  ptx::launch_dependents();
   if (starts && starts[blockIdx.y + 1] <= (blockIdx.y ? starts[blockIdx.y] : 0)) return;
   const int per = width8 >> 3;
   src += blockIdx.y * stride;
@@ -580,6 +651,47 @@ __global__ void __launch_bounds__(256) pack_kernel(const uint16_t* src, int64_t 
       w[k] = lo | (hi << 16);
     }
     *reinterpret_cast<uint4*>(dst + r * width8 + c) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// The padded ends of the groups: the last len % 16 rows of each group of x
+// (width wide, ld apart), then zeros, as rows 16 e .. 16 e + 15 of dst (width8 wide).  One
+// CTA an expert and operand; a length that is a multiple of 16 needs none.
+struct EndArgs {
+  const uint16_t* x[2];
+  int64_t ld[2];
+  uint16_t* dst[2];
+  int32_t width[2], width8[2];
+  const int32_t* starts;
+  int64_t n_rows;
+};
+__global__ void __launch_bounds__(256) group_end_kernel(const __grid_constant__ EndArgs a) {
+  ptx::launch_dependents();
+  const int e = blockIdx.x, o = blockIdx.y;
+  const int n = (int)a.n_rows;
+  const int lo = e == 0 ? 0 : min(max(a.starts[e], 0), n), hi = min(max(a.starts[e + 1], 0), n);
+  const int rest = max(0, hi - lo) & (kEnd - 1);
+  if (rest == 0) return;
+  const int per = a.width8[o] >> 3;
+  const bool vec = a.ld[o] % 8 == 0 && a.width[o] % 8 == 0;
+  for (int i = threadIdx.x; i < kEnd * per; i += 256) {
+    const int r = i / per, c = (i - r * per) * 8;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (r < rest) {
+      const uint16_t* s = a.x[o] + (int64_t)(hi - rest + r) * a.ld[o] + c;
+      if (vec) {
+        v = *reinterpret_cast<const uint4*>(s);
+      } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t x = c + 2 * k < a.width[o] ? s[2 * k] : 0, y = c + 2 * k + 1 < a.width[o] ? s[2 * k + 1] : 0;
+          w[k] = x | (y << 16);
+        }
+        v = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+    *reinterpret_cast<uint4*>(a.dst[o] + ((int64_t)e * kEnd + r) * a.width8[o] + c) = v;
   }
 }
 
@@ -614,45 +726,61 @@ bool encode(CUtensorMap* map, const void* base, int64_t width, int64_t height, i
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-constexpr size_t kSmemBytes = kSmemStages + 1024;
+constexpr size_t kSmemBytes = kSmemStages + kEpiWarps * kEpiStage + 1024;
 
-template <int kMode>
-cudaError_t launch_mode(const ExpertArgs& a, const Maps& maps, int64_t max_tiles, cudaStream_t s) {
+template <int kMode, bool kBf16, bool kAccumulate, bool kVec>
+cudaError_t launch_kernel(const ExpertArgs& a, const Maps& maps, int64_t max_tiles, cudaStream_t s) {
   static std::mutex mu;
   static int resident[kMaxDevices] = {};      // CTA pairs on the device at once
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = 2;
-  attr.val.clusterDim.y = 1;
-  attr.val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = kSmemBytes;
-  cfg.attrs = &attr;
+  cfg.attrs = attr;
   cfg.numAttrs = 1;
   int pairs = 0;
   {
     std::lock_guard<std::mutex> lock(mu);
     if (resident[dev] == 0) {
-      e = cudaFuncSetAttribute(expert_kernel<kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+      e = cudaFuncSetAttribute(expert_kernel<kMode, kBf16, kAccumulate, kVec>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
       if (e != cudaSuccess) return e;
       cfg.gridDim = dim3((unsigned)(2 * (sm_count() / 2)), 1, 1);
       int n = 0;
-      e = cudaOccupancyMaxActiveClusters(&n, expert_kernel<kMode>, &cfg);
+      e = cudaOccupancyMaxActiveClusters(&n, expert_kernel<kMode, kBf16, kAccumulate, kVec>, &cfg);
       if (e != cudaSuccess) return e;
       if (n < 1) return cudaErrorInvalidConfiguration;
       resident[dev] = n;
     }
     pairs = resident[dev];
   }
+  cfg.numAttrs = a.prepared ? 2 : 1;      // may start beside the kernels that prepare its operands
   cfg.stream = s;
   cfg.gridDim = dim3((unsigned)(2 * std::max<int64_t>(1, std::min<int64_t>(pairs, max_tiles))), 1, 1);
-  e = cudaLaunchKernelEx(&cfg, expert_kernel<kMode>, a, maps);
+  e = cudaLaunchKernelEx(&cfg, expert_kernel<kMode, kBf16, kAccumulate, kVec>, a, maps);
   return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+template <int kMode>
+cudaError_t launch_mode(const ExpertArgs& a, const Maps& maps, int64_t max_tiles, cudaStream_t s) {
+  if constexpr (kMode == kExpertWeightGrad) {
+    const auto go = a.out_vec ? (a.out_bf16 ? (a.accumulate ? launch_kernel<kMode, true, true, true> : launch_kernel<kMode, true, false, true>)
+                                            : (a.accumulate ? launch_kernel<kMode, false, true, true> : launch_kernel<kMode, false, false, true>))
+                              : (a.out_bf16 ? (a.accumulate ? launch_kernel<kMode, true, true, false> : launch_kernel<kMode, true, false, false>)
+                                            : (a.accumulate ? launch_kernel<kMode, false, true, false> : launch_kernel<kMode, false, false, false>));
+    return go(a, maps, max_tiles, s);
+  }
+  return a.out_bf16 ? launch_kernel<kMode, true, false, false>(a, maps, max_tiles, s)
+                    : launch_kernel<kMode, false, false, false>(a, maps, max_tiles, s);
 }
 
 int64_t up8(int64_t x) { return (x + 7) / 8 * 8; }
@@ -704,12 +832,33 @@ cudaError_t launch_expert(const ExpertArgs& in, cudaStream_t s) {
       ok = encode(&maps.a, a.a, a.rows, n, a.a_ld, 1, n * a.a_ld, 64) &&
            encode(&maps.b, a.b, a.cols, n, a.b_ld, 1, n * a.b_ld, 64);
       if (!ok) return cudaErrorInvalidValue;
-      maps.b128 = maps.b;
+      EndArgs ends;
+      ends.x[0] = static_cast<const uint16_t*>(in.a);
+      ends.x[1] = static_cast<const uint16_t*>(in.b);
+      ends.ld[0] = in.a_ld;
+      ends.ld[1] = in.b_ld;
+      const int64_t width[2] = {a.rows, a.cols};
+      for (int o = 0; o < 2; ++o) {
+        ends.dst[o] = reinterpret_cast<uint16_t*>(at);
+        ends.width[o] = (int32_t)width[o];
+        ends.width8[o] = (int32_t)up8(width[o]);
+        at += packed_bytes((int64_t)a.n_experts * kEnd, width[o]);
+      }
+      ends.starts = a.starts;
+      ends.n_rows = n;
+      group_end_kernel<<<dim3((unsigned)a.n_experts, 2), 256, 0, s>>>(ends);
+      e = cudaGetLastError();
+      if (e != cudaSuccess) return e;
+      a.prepared = 1;
+      const int64_t m = (int64_t)a.n_experts * kEnd;
+      ok = encode(&maps.c, ends.dst[0], a.rows, m, ends.width8[0], 1, m * ends.width8[0], kEnd) &&
+           encode(&maps.d, ends.dst[1], a.cols, m, ends.width8[1], 1, m * ends.width8[1], kEnd);
+      if (!ok) return cudaErrorInvalidValue;
     } else {
       maps = Maps{};       // no tile has a contraction: no copy is issued
     }
     const int64_t esz = a.out_bf16 ? 2 : 4;
-    a.out_vec = aligned(a.out, 32) && a.cols * esz % 32 == 0 && a.out_stride * esz % 32 == 0;
+    a.out_vec = a.cols * esz % 16 == 0 && (a.n_experts == 1 || a.out_stride * esz % 16 == 0);
     const int64_t nt = (a.cols + kMaxN - 1) / kMaxN;
     return launch_mode<kExpertWeightGrad>(a, maps, a.n_experts * mt * nt, s);
   }
@@ -727,8 +876,10 @@ cudaError_t launch_expert(const ExpertArgs& in, cudaStream_t s) {
   const int64_t w_stride = a.n_experts > 1 ? a.b_stride : a.rows * a.b_ld;
   ok = encode(&maps.a, a.b, a.cols, a.rows, a.b_ld, a.n_experts, w_stride, a.mode == kExpertForward ? 128 : 64) &&
        encode(&maps.b, a.a, k, n, a.a_ld, 1, n * a.a_ld, 32) &&
-       encode(&maps.b128, a.a, k, n, a.a_ld, 1, n * a.a_ld, 128);
+       encode(&maps.c, a.a, k, n, a.a_ld, 1, n * a.a_ld, 128);
   if (!ok) return cudaErrorInvalidValue;
+  maps.d = maps.c;
+  a.prepared = at != in.packs;
   const int64_t tiles = mt * (n / kMaxN + std::min<int64_t>(a.n_experts, n));
   return a.mode == kExpertForward ? launch_mode<kExpertForward>(a, maps, tiles, s)
                                   : launch_mode<kExpertInputGrad>(a, maps, tiles, s);

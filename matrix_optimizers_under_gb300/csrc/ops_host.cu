@@ -434,6 +434,8 @@ extern "C" size_t mfsdp_expert_workspace_bytes(int32_t n_experts, int64_t n_rows
   if (cols % 8 != 0 || (n_experts > 1 && w_stride % 8 != 0)) bytes += packed_bytes(n_experts * rows, cols);
   if (n_rows > 1 && rows_ld % 8 != 0) bytes += packed_bytes(n_rows, rows);
   if (n_rows > 1 && cols_ld % 8 != 0) bytes += packed_bytes(n_rows, cols);
+  // weight gradient: the last rows of each group, padded to 16, of both operands
+  if (n_rows > 0) bytes += packed_bytes(16 * (int64_t)n_experts, rows) + packed_bytes(16 * (int64_t)n_experts, cols);
   return bytes;
 }
 

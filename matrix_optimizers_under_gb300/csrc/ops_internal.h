@@ -141,10 +141,11 @@ struct ExpertArgs {
   int64_t b_stride;       // forward, input gradient: elements between experts' matrices
   int64_t out_ld, out_stride;
   int32_t out_bf16, accumulate;
-  int32_t out_vec;        // weight gradient: every 32 columns of its rows start 32-byte aligned
+  int32_t out_vec;        // weight gradient: its rows start on 16-byte boundaries
   int32_t* status;        // first wait that gave up (0: none)
   uint8_t* packs;         // workspace for operands whose rows are not 16-byte aligned
   uint64_t wait_limit_ns;
+  int32_t prepared;       // kernels of this call that prepare operands run right before
 };
 // Bytes of a copy of n rows of `width` bf16 elements, each padded to 16 bytes.
 inline size_t packed_bytes(int64_t n, int64_t width) {
