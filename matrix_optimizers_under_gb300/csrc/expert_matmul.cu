@@ -30,9 +30,9 @@
 // rows of A and its half of B, 32 KB per 64 of K: 64 bytes a clock at the full
 // MMA rate, where a CTA alone on 128 x 256 would need 96.  Warp roles: 0
 // producer, 1 MMA issuer (even CTA), 4-11 epilogue; two accumulators in TMEM let the epilogue overlap the next
-// tile.  The pipeline has as many stages as shared memory holds at the
-// launch's widest tile: 6 of 32 KB for 256 tokens, 9 of 20 KB for a few tokens,
-// where the product is bound by reading W and bytes in flight count.
+// tile.  A stage holds K = 128 of both; the pipeline has as many stages as shared
+// memory holds at the launch's widest tile: 3 of 64 KB for 256 tokens, 5 of 40 KB
+// for a few tokens, where the product is bound by reading W.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -54,9 +54,11 @@ constexpr int kBytesA = kCtaM * kBlockK * 2;          // 16 KB
 constexpr int kMnBlock = 64 * kBlockK * 2;            // 8 KB: 64 MN elements x 64 K rows (MN-major)
 constexpr int kEnd = 16;                              // K of one MMA: rows of a group's padded end
 constexpr int kEndBlock = 64 * kEnd * 2;
-constexpr int kSmemStages = 6 * 32768;
-constexpr int kEpiStage = 2048;                       // staging of an epilogue warp
-constexpr int kMaxStages = 9;               // of 20 KB
+constexpr int kSub = 2;                               // blocks of a stage: handing a stage on costs ~460 cycles
+constexpr int kEpiStage = 2048;                       // weight gradient: staging of an epilogue warp
+constexpr int kMaxStages = 5;                         // of 40 KB
+// Shared memory of the stages: three of 64 KB; or, in the forward products, five of 40 KB.
+constexpr int smem_stages(int mode) { return mode == kExpertWeightGrad ? 3 * 65536 : 5 * 40960; }
 constexpr int kEpiWarps = 8;
 constexpr int kFirstEpiWarp = 4;
 constexpr int kThreads = 32 * (kFirstEpiWarp + kEpiWarps);
@@ -402,8 +404,8 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
   // Shared memory of a stage: A, then this CTA's half of B.
   const int wide = kWgrad ? sh.width_n : widest;
   const int bytes_b_max = kWgrad ? ceil_div(wide / 2, 64) * kMnBlock : (wide / 2 > 96 ? 128 : ceil_div(wide / 2, 32) * 32) * 128;
-  const uint32_t stage_bytes = kBytesA + bytes_b_max;
-  const int stages = min(kMaxStages, kSmemStages / (int)stage_bytes);
+  const uint32_t sub_bytes = kBytesA + bytes_b_max, stage_bytes = kSub * sub_bytes;
+  const int stages = min(kMaxStages, smem_stages(kMode) / (int)stage_bytes);
 
   if (warp == 0) {
     // -------------------------------------------------------------- producer
@@ -432,37 +434,37 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
       const uint32_t pair_bytes = (tl.m0 + kCtaM < sh.m ? 2u : 1u) * kBytesA + 2u * bytes_b;
       const bool ragged = kWgrad && (tl.k_len & (kEnd - 1)) != 0;
       const int nc = tl.n0 + (int)rank_u * nh;
-      for (int kb = 0; kb < blocks; ++kb) {
+      for (int kb = 0; kb < blocks; kb += kSub) {
         ok = __all_sync(0xffffffffu, wait_bar<false>(empty0 + 8 * s, (use & 1) ^ 1, ab, kRoleStage));
         if (!ok) break;
         const uint32_t bar = pair_full0 + 8 * s;
-        const uint32_t sa = base_u + s * stage_bytes, sb = sa + kBytesA;
-        const int k0 = kb * kBlockK;
+        const int subs = min(kSub, blocks - kb);
+        const bool end = ragged && kb + subs == blocks;         // its last block has 16 rows: a quarter of the bytes
         if (ptx::elect_one()) {
-          if (ragged && kb == blocks - 1) {
-            // 16 rows: a quarter of the bytes
-            if (rank_u == 0) ptx::mbar_arrive_expect_tx(full0 + 8 * s, pair_bytes * kEnd / kBlockK);
-            const int y = tl.e * kEnd;
-            if (a_in) {
-              ptx::tma_load_3d_pair(sa, &maps.c, mc, y, 0, bar);
-              ptx::tma_load_3d_pair(sa + kMnBlock, &maps.c, mc + 64, y, 0, bar);
-            }
-            ptx::tma_load_3d_pair(sb, &maps.d, nc, y, 0, bar);
-            if (copies_b > 1) ptx::tma_load_3d_pair(sb + kMnBlock, &maps.d, nc + 64, y, 0, bar);
-          } else {
-            if (rank_u == 0) ptx::mbar_arrive_expect_tx(full0 + 8 * s, pair_bytes);
+          if (rank_u == 0)
+            ptx::mbar_arrive_expect_tx(full0 + 8 * s, end ? (subs - 1) * pair_bytes + pair_bytes * kEnd / kBlockK
+                                                          : subs * pair_bytes);
+#pragma unroll
+          for (int h = 0; h < kSub; ++h) {
+            if (h >= subs) break;
+            const uint32_t sa = base_u + s * stage_bytes + h * sub_bytes, sb = sa + kBytesA;
+            const int k0 = (kb + h) * kBlockK;
+            const bool last = end && h == subs - 1;
             if (a_in) {
               if (!kAmn) {
                 ptx::tma_load_3d_pair(sa, &maps.a, k0, mc, tl.e, bar);
               } else {
-                const int y = kWgrad ? tl.group + k0 : k0, z = kWgrad ? 0 : tl.e;
-                ptx::tma_load_3d_pair(sa, &maps.a, mc, y, z, bar);
-                ptx::tma_load_3d_pair(sa + kMnBlock, &maps.a, mc + 64, y, z, bar);
+                const CUtensorMap* map = last ? &maps.c : &maps.a;
+                const int y = last ? tl.e * kEnd : (kWgrad ? tl.group + k0 : k0), z = kWgrad ? 0 : tl.e;
+                ptx::tma_load_3d_pair(sa, map, mc, y, z, bar);
+                ptx::tma_load_3d_pair(sa + kMnBlock, map, mc + 64, y, z, bar);
               }
             }
             if (kWgrad) {
-              ptx::tma_load_3d_pair(sb, &maps.b, nc, tl.group + k0, 0, bar);
-              if (copies_b > 1) ptx::tma_load_3d_pair(sb + kMnBlock, &maps.b, nc + 64, tl.group + k0, 0, bar);
+              const CUtensorMap* map = last ? &maps.d : &maps.b;
+              const int y = last ? tl.e * kEnd : tl.group + k0;
+              ptx::tma_load_3d_pair(sb, map, nc, y, 0, bar);
+              if (copies_b > 1) ptx::tma_load_3d_pair(sb + kMnBlock, map, nc + 64, y, 0, bar);
             } else if (nh > 96) {
               ptx::tma_load_3d_pair(sb, &maps.c, k0, tl.group + nc, 0, bar);
             } else {
@@ -504,27 +506,34 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
         ptx::tc_fence_after();
         const uint32_t d_tmem = tmem_u + a * kAccCols;
         const uint32_t idesc = ptx::idesc_bf16_f32(kPairM, (uint32_t)tl.n_mma, kWgrad ? 1u : 0u, kAmn ? 1u : 0u);
-        for (int kb = 0; kb < blocks; ++kb) {
+        for (int kb = 0; kb < blocks; kb += kSub) {
           ok = __all_sync(0xffffffffu, wait_bar<true>(full0 + 8 * s, use & 1, ab, kRoleOperands));
           if (!ok) break;
           ptx::tc_fence_after();
-          const uint32_t sa = base_u + s * stage_bytes, sb = sa + kBytesA;
           // K-major: 16 elements (32 bytes) along the swizzle row, 8-row groups
           // 1 KB apart.  MN-major: 16 K rows (2 KB), 64-element blocks 8 KB
           // apart (leading offset), 8-row K groups 1 KB apart (stride offset).
+          const uint32_t sa = base_u + s * stage_bytes;
           const uint64_t adesc = ptx::smem_desc_sw128(sa, kAmn ? kMnBlock : 16, 1024);
-          const uint64_t bdesc = ptx::smem_desc_sw128(sb, kWgrad ? kMnBlock : 16, 1024);
-          // K-major operands past the contraction's end are zeros of the copy's fill
-          const int left = tl.k_len - kb * kBlockK;
-          const int steps = ragged && kb == blocks - 1 ? 1 : min(kBlockK / 16, kWgrad ? left / 16 : ceil_div(left, 16));
+          const uint64_t bdesc = ptx::smem_desc_sw128(sa + kBytesA, kWgrad ? kMnBlock : 16, 1024);
+          const int subs = min(kSub, blocks - kb);
           if (ptx::elect_one()) {
 #pragma unroll
-            for (int k = 0; k < kBlockK / 16; ++k)
-              if (k < steps)
-                ptx::umma_bf16_pair(d_tmem, adesc + k * (kAmn ? 2048 >> 4 : 32 >> 4),
-                                    bdesc + k * (kWgrad ? 2048 >> 4 : 32 >> 4), idesc, kb > 0 || k > 0 ? 1u : 0u);
+            for (int h = 0; h < kSub; ++h) {
+              if (h >= subs) break;
+              // K-major operands past the contraction's end are zeros of the copy's fill
+              const int left = tl.k_len - (kb + h) * kBlockK;
+              const int steps = ragged && kb + h == blocks - 1 ? 1 : min(kBlockK / 16, kWgrad ? left / 16 : ceil_div(left, 16));
+              const uint32_t off = h * (sub_bytes >> 4);
+#pragma unroll
+              for (int k = 0; k < kBlockK / 16; ++k)
+                if (k < steps)
+                  ptx::umma_bf16_pair(d_tmem, adesc + off + k * (kAmn ? 2048 >> 4 : 32 >> 4),
+                                      bdesc + off + k * (kWgrad ? 2048 >> 4 : 32 >> 4), idesc,
+                                      kb + h > 0 || k > 0 ? 1u : 0u);
+            }
             ptx::umma_commit_pair_multicast(empty0 + 8 * s, 0x3);
-            if (kb == blocks - 1) ptx::umma_commit_pair_multicast(tfull0 + 8 * a, 0x3);
+            if (kb + kSub >= blocks) ptx::umma_commit_pair_multicast(tfull0 + 8 * a, 0x3);
           }
           __syncwarp();
           if (++s == (uint32_t)stages) { s = 0; ++use; }
@@ -542,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
     // Warp w reads TMEM lane quadrant w % 4; the two warps of a quadrant take
     // alternate chunks of 32 columns.
     const int quad = warp & 3, half = (warp - kFirstEpiWarp) >> 2;
-    uint8_t* const stage = smem_raw + (smem_base - ptx::smem_u32(smem_raw)) + kSmemStages + (warp - kFirstEpiWarp) * kEpiStage;
+    uint8_t* const stage = smem_raw + (smem_base - ptx::smem_u32(smem_raw)) + smem_stages(kMode) + (warp - kFirstEpiWarp) * kEpiStage;
     constexpr int kEsz = kBf16 ? 2 : 4;
     constexpr int kWidth = kWgrad && kVec ? 128 / kEsz : 32;     // columns of a chunk
     uint32_t acc_it = 0;
@@ -726,10 +735,10 @@ bool encode(CUtensorMap* map, const void* base, int64_t width, int64_t height, i
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-constexpr size_t kSmemBytes = kSmemStages + kEpiWarps * kEpiStage + 1024;
 
 template <int kMode, bool kBf16, bool kAccumulate, bool kVec>
 cudaError_t launch_kernel(const ExpertArgs& a, const Maps& maps, int64_t max_tiles, cudaStream_t s) {
+  constexpr size_t kSmemBytes = smem_stages(kMode) + (kMode == kExpertWeightGrad ? kEpiWarps * kEpiStage : 0) + 1024;
   static std::mutex mu;
   static int resident[kMaxDevices] = {};      // CTA pairs on the device at once
   int dev = 0;
