@@ -30,9 +30,9 @@
 // rows of A and its half of B, 32 KB per 64 of K: 64 bytes a clock at the full
 // MMA rate, where a CTA alone on 128 x 256 would need 96.  Warp roles: 0
 // producer, 1 MMA issuer (even CTA), 4-11 epilogue; two accumulators in TMEM let the epilogue overlap the next
-// tile.  A stage holds K = 128 of both; the pipeline has as many stages as shared
-// memory holds at the launch's widest tile: 3 of 64 KB for 256 tokens, 5 of 40 KB
-// for a few tokens, where the product is bound by reading W.
+// tile.  The pipeline has as many stages of K = 64 as shared memory holds at the
+// launch's widest tile: 6 of 32 KB for 256 tokens, 10 of 20 KB for a few tokens,
+// where the product is bound by reading W.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -53,12 +53,14 @@ constexpr int kBlockK = 64;               // K of a stage: one 128-byte swizzle 
 constexpr int kBytesA = kCtaM * kBlockK * 2;          // 16 KB
 constexpr int kMnBlock = 64 * kBlockK * 2;            // 8 KB: 64 MN elements x 64 K rows (MN-major)
 constexpr int kEnd = 16;                              // K of one MMA: rows of a group's padded end
-constexpr int kEndBlock = 64 * kEnd * 2;
-constexpr int kSub = 2;                               // blocks of a stage: handing a stage on costs ~460 cycles
-constexpr int kEpiStage = 2048;                       // weight gradient: staging of an epilogue warp
-constexpr int kMaxStages = 5;                         // of 40 KB
-// Shared memory of the stages: three of 64 KB; or, in the forward products, five of 40 KB.
-constexpr int smem_stages(int mode) { return mode == kExpertWeightGrad ? 3 * 65536 : 5 * 40960; }
+constexpr int kEpiPart = 2048;                        // 16 rows of 128 bytes
+constexpr int kEpiStage = 2 * kEpiPart;               // weight gradient: staging of an epilogue warp
+constexpr int kMaxStages = 10;
+// The producer and the issuer take two stages at a time: a turn of their loops
+// (waits, election, counters) costs ~400 cycles, and a stage's MMAs take 512.
+constexpr int kTurn = 2;
+// Shared memory of the stages: six of 32 KB, or ten of 20 KB (the weight gradient has none so small).
+constexpr int smem_stages(int mode) { return mode == kExpertWeightGrad ? 6 * 32768 : 10 * 20480; }
 constexpr int kEpiWarps = 8;
 constexpr int kFirstEpiWarp = 4;
 constexpr int kThreads = 32 * (kFirstEpiWarp + kEpiWarps);
@@ -71,6 +73,7 @@ struct Maps {
   CUtensorMap b;      // box 64 x 32 (K-major B) or 64 x 64
   CUtensorMap c;      // box 64 x 128 (K-major B of a full tile); weight gradient: the padded ends of A, box 64 x 16
   CUtensorMap d;      // weight gradient: the padded ends of B, box 64 x 16
+  CUtensorMap out;    // weight gradient: dW, box 128 bytes x 16
 };
 
 // First failing wait of a launch: (role << 0); the wait's limit.
@@ -99,6 +102,15 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const Ab
   }
 }
 
+// The same for a stage, and if `two` for the next one too.
+template <bool kCluster>
+__device__ __forceinline__ bool wait_bars(uint32_t bar0, uint32_t parity0, bool two, uint32_t bar1, uint32_t parity1,
+                                          const Abort& ab, int32_t role) {
+  bool ok = wait_bar<kCluster>(bar0, parity0, ab, role);
+  if (ok && two) ok = wait_bar<kCluster>(bar1, parity1, ab, role);
+  return __all_sync(0xffffffffu, ok);
+}
+
 // One tile: `rows` [m0, m0 + 256) of the M side, columns [n0, n0 + n) of the N
 // side (n_mma of them in the MMA), k_len of contraction.
 struct Tile {
@@ -123,9 +135,14 @@ template <bool kWgrad>
 __device__ __forceinline__ int blocks_of(int k) {
   return kWgrad ? ceil_div(k & ~(kEnd - 1), kBlockK) + ((k & (kEnd - 1)) != 0) : ceil_div(k, kBlockK);
 }
-// n split over `parts` tiles, each a multiple of 32 wide.
-__device__ __forceinline__ int even_width(int n, int parts) {
-  return (ceil_div(n, parts) + kStepN - 1) / kStepN * kStepN;
+// n split over `parts` tiles, each a multiple of `step` wide.
+__device__ __forceinline__ int even_width(int n, int parts, int step = kStepN) {
+  return (ceil_div(n, parts) + step - 1) / step * step;
+}
+
+// First token of expert e's group, kept inside the rows there are.
+__device__ __forceinline__ int start_of(const ExpertArgs& p, int e) {
+  return e == 0 ? 0 : min(max(p.starts[e], 0), (int)p.n_rows);
 }
 
 template <int kMode>
@@ -139,8 +156,8 @@ __device__ __forceinline__ Tile decode(const ExpertArgs& p, const Shape& sh, con
     r.m0 = (i - j * sh.tiles_m) * kPairM;
     r.n0 = j * sh.width_n;
     r.n = min(sh.width_n, sh.n - r.n0);
-    r.group = start[r.e];
-    r.k_len = max(0, start[r.e + 1] - start[r.e]);
+    r.group = start_of(p, r.e);
+    r.k_len = max(0, start_of(p, r.e + 1) - r.group);
   } else {
     int lo = 0, hi = p.n_experts - 1;
     while (lo < hi) {
@@ -180,7 +197,8 @@ struct TileWalk {
   __device__ __forceinline__ TileWalk(const ExpertArgs& p_, const Shape& sh_, const int32_t* start_,
                                       const int32_t* first_, int pair0, int pairs_, int n_tiles_)
       : p(p_), sh(sh_), start(start_), first(first_), t(pair0), pairs(pairs_), n_tiles(n_tiles_), held(0) {}
-  // The next tile, the same in all lanes; false after the last.
+  // The next tile, the same in all lanes (kShape: only its n_mma and k_len); false after the last.
+  template <bool kShape = false>
   __device__ __forceinline__ bool next(Tile& r) {
     if (t >= n_tiles) return false;
     if (held == 0) {
@@ -190,11 +208,13 @@ struct TileWalk {
       __syncwarp();
     }
     const int lane = 32 - held;
-    r.e = __shfl_sync(0xffffffffu, mine.e, lane);
-    r.group = __shfl_sync(0xffffffffu, mine.group, lane);
-    r.m0 = __shfl_sync(0xffffffffu, mine.m0, lane);
-    r.n0 = __shfl_sync(0xffffffffu, mine.n0, lane);
-    r.n = __shfl_sync(0xffffffffu, mine.n, lane);
+    if (!kShape) {
+      r.e = __shfl_sync(0xffffffffu, mine.e, lane);
+      r.group = __shfl_sync(0xffffffffu, mine.group, lane);
+      r.m0 = __shfl_sync(0xffffffffu, mine.m0, lane);
+      r.n0 = __shfl_sync(0xffffffffu, mine.n0, lane);
+      r.n = __shfl_sync(0xffffffffu, mine.n, lane);
+    }
     r.n_mma = __shfl_sync(0xffffffffu, mine.n_mma, lane);
     r.k_len = __shfl_sync(0xffffffffu, mine.k_len, lane);
     --held;
@@ -224,37 +244,42 @@ __device__ __forceinline__ void store_row(const ExpertArgs& p, int64_t at, int n
   }
 }
 
-// 128 bytes of each of a warp's 32 rows (64 bf16 or 32 fp32 columns), lane l
-// holding row l's in `w`.  A lane's own 16- or 32-byte stores to its row would
-// touch 32 lines an instruction (that took the epilogue 5000 cycles a tile,
-// twice the MMAs'); through the warp's 2 KB of shared memory, 16 rows at a
-// time, an instruction moves 4 whole lines.  Chunk c of row r sits at c ^ (r & 7).
-// Rows from `rows` on and 16-byte chunks from `chunks` on are left alone.
-__device__ __forceinline__ void put_rows(uint8_t* stage, const uint32_t (&w)[32], uint8_t* out, int64_t pitch,
-                                         int rows, int chunks) {
+// 128 bytes of each of a warp's 32 rows (64 bf16 or 32 fp32 columns, `x` on,
+// of rows `y` on of matrix `z`), lane l holding row l's in `w`.  The rows go, 16 at a
+// time, through the warp's two 2 KB of shared memory, out by tensor copies, which
+// leave out what lies past the matrix (`rows` rows are left in it) and take the
+// writes off the warp: with its own stores, of whole lines, the epilogue took
+// 3800 cycles a tile of 2300 cycles of MMAs; with each lane's to its own row
+// 5000.  Chunk c of row r sits at c ^ (r & 7), the copy's swizzle.
+__device__ __forceinline__ void put_rows(uint8_t* stage, const uint32_t (&w)[32], const CUtensorMap* map, int x, int y,
+                                         int z, int rows, uint32_t& parts) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
+    if (16 * h >= rows) break;
+    uint8_t* const part = stage + (parts++ & 1) * kEpiPart;
+    if (lane == 0) ptx::bulk_wait_read<1>();           // the copy before the last has left this part
+    __syncwarp();
     if ((lane >> 4) == h) {
 #pragma unroll
       for (int c = 0; c < 8; ++c)
-        *reinterpret_cast<uint4*>(stage + (lane & 15) * 128 + ((c ^ (lane & 7)) << 4)) =
+        *reinterpret_cast<uint4*>(part + (lane & 15) * 128 + ((c ^ (lane & 7)) << 4)) =
             make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+      ptx::fence_proxy_async_smem();
     }
     __syncwarp();
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int r = 4 * k + (lane >> 3), c = lane & 7;
-      const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + ((c ^ (r & 7)) << 4));
-      if (16 * h + r < rows && c < chunks) __stcs(reinterpret_cast<uint4*>(out + (16 * h + r) * pitch + 16 * c), v);
+    if (lane == 0) {
+      ptx::tma_store_3d(map, ptx::smem_u32(part), x, y + 16 * h, z);
+      ptx::bulk_commit();
     }
-    __syncwarp();
   }
 }
 // The way back: each lane receives its row's 128 bytes.
 __device__ __forceinline__ void get_rows(uint8_t* stage, uint32_t (&w)[32], const uint8_t* in, int64_t pitch, int rows,
                                          int chunks) {
   const int lane = threadIdx.x & 31;
+  if (lane == 0) ptx::bulk_wait_read<0>();
+  __syncwarp();
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
 #pragma unroll
@@ -279,14 +304,14 @@ __device__ __forceinline__ void get_rows(uint8_t* stage, uint32_t (&w)[32], cons
 // One chunk of a weight gradient's rows from the accumulator at `taddr`: 64
 // columns to bf16, or 32 to fp32.  `last`: then hands the accumulator back.
 template <bool kBf16, bool kAccumulate, typename Release>
-__device__ __forceinline__ void put_chunk(const ExpertArgs& p, uint8_t* stage, uint32_t taddr, int64_t at, int rows,
-                                          int cols, bool last, Release release) {
+__device__ __forceinline__ void put_chunk(const ExpertArgs& p, const CUtensorMap* map, uint8_t* stage, uint32_t taddr,
+                                          int x, int y, int z, int rows, int cols, uint32_t& parts, bool last,
+                                          Release release) {
   constexpr int kEsz = kBf16 ? 2 : 4;
-  uint8_t* out = static_cast<uint8_t*>(p.out) + at * kEsz;
-  const int64_t pitch = p.out_ld * kEsz;
-  const int chunks = min(8, cols * kEsz / 16);
   uint32_t w[32], acc[32];
-  if constexpr (kAccumulate) get_rows(stage, w, out, pitch, rows, chunks);
+  if constexpr (kAccumulate)
+    get_rows(stage, w, static_cast<const uint8_t*>(p.out) + (z * p.out_stride + y * p.out_ld + x) * kEsz,
+             p.out_ld * kEsz, rows, min(8, cols * kEsz / 16));
 #pragma unroll
   for (int h = 0; h < (kBf16 ? 2 : 1); ++h) {
     ptx::tmem_ld_32x32b_x32(taddr + 32 * h, acc);
@@ -307,7 +332,7 @@ __device__ __forceinline__ void put_chunk(const ExpertArgs& p, uint8_t* stage, u
       }
     }
   }
-  put_rows(stage, w, out, pitch, rows, chunks);
+  put_rows(stage, w, map, x, y, z, rows, parts);
 }
 
 // kBf16: the output's type.  Weight gradient: kAccumulate, and kVec: the rows
@@ -318,8 +343,8 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
   constexpr bool kWgrad = kMode == kExpertWeightGrad;
   constexpr bool kAmn = kMode != kExpertForward;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ int32_t start[MFSDP_MAX_EXPERTS + 1];      // first token of each group, clamped
-  __shared__ int32_t first[MFSDP_MAX_EXPERTS + 1];      // first tile of each expert (forward products)
+  // forward products: first token (clamped) and first tile of each expert
+  __shared__ int32_t start[kWgrad ? 1 : MFSDP_MAX_EXPERTS + 1], first[kWgrad ? 1 : MFSDP_MAX_EXPERTS + 1];
   __shared__ int32_t widest;                            // columns of the launch's widest tile
   __shared__ __align__(8) uint64_t full_bar[kMaxStages];    // even CTA: both CTAs' operands have landed
   __shared__ __align__(8) uint64_t empty_bar[kMaxStages];
@@ -337,12 +362,10 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
   sh.tiles_m = ceil_div(sh.m, kPairM);
   sh.n = (int)p.cols;
   sh.tiles_n = ceil_div(sh.n, kMaxN);
-  sh.width_n = even_width(sh.n, sh.tiles_n);
+  sh.width_n = even_width(sh.n, sh.tiles_n, 64);       // whole chunks of the epilogue, which writes them whole
 
-  for (int i = threadIdx.x; i <= p.n_experts; i += kThreads) {
-    const int s = i == 0 ? 0 : p.starts[i];
-    start[i] = min(max(s, 0), n_rows);
-  }
+  if (!kWgrad)
+    for (int i = threadIdx.x; i <= p.n_experts; i += kThreads) start[i] = start_of(p, i);
   if (warp == 1) {
     ptx::tmem_alloc_pair(ptx::smem_u32(&tmem_slot), kTmemCols);
     ptx::tmem_relinquish_pair();
@@ -404,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
   // Shared memory of a stage: A, then this CTA's half of B.
   const int wide = kWgrad ? sh.width_n : widest;
   const int bytes_b_max = kWgrad ? ceil_div(wide / 2, 64) * kMnBlock : (wide / 2 > 96 ? 128 : ceil_div(wide / 2, 32) * 32) * 128;
-  const uint32_t sub_bytes = kBytesA + bytes_b_max, stage_bytes = kSub * sub_bytes;
+  const uint32_t stage_bytes = kBytesA + bytes_b_max;
   const int stages = min(kMaxStages, smem_stages(kMode) / (int)stage_bytes);
 
   if (warp == 0) {
@@ -434,22 +457,21 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
       const uint32_t pair_bytes = (tl.m0 + kCtaM < sh.m ? 2u : 1u) * kBytesA + 2u * bytes_b;
       const bool ragged = kWgrad && (tl.k_len & (kEnd - 1)) != 0;
       const int nc = tl.n0 + (int)rank_u * nh;
-      for (int kb = 0; kb < blocks; kb += kSub) {
-        ok = __all_sync(0xffffffffu, wait_bar<false>(empty0 + 8 * s, (use & 1) ^ 1, ab, kRoleStage));
+      for (int kb = 0; kb < blocks; kb += kTurn) {
+        const int turn = min(kTurn, blocks - kb);
+        const uint32_t s1 = s + 1 == (uint32_t)stages ? 0 : s + 1, use1 = s1 == 0 ? use + 1 : use;
+        ok = wait_bars<false>(empty0 + 8 * s, (use & 1) ^ 1, turn > 1, empty0 + 8 * s1, (use1 & 1) ^ 1, ab, kRoleStage);
         if (!ok) break;
-        const uint32_t bar = pair_full0 + 8 * s;
-        const int subs = min(kSub, blocks - kb);
-        const bool end = ragged && kb + subs == blocks;         // its last block has 16 rows: a quarter of the bytes
         if (ptx::elect_one()) {
-          if (rank_u == 0)
-            ptx::mbar_arrive_expect_tx(full0 + 8 * s, end ? (subs - 1) * pair_bytes + pair_bytes * kEnd / kBlockK
-                                                          : subs * pair_bytes);
 #pragma unroll
-          for (int h = 0; h < kSub; ++h) {
-            if (h >= subs) break;
-            const uint32_t sa = base_u + s * stage_bytes + h * sub_bytes, sb = sa + kBytesA;
+          for (int h = 0; h < kTurn; ++h) {
+            if (h >= turn) break;
+            const uint32_t slot = h == 0 ? s : s1;
+            const uint32_t sa = base_u + slot * stage_bytes, sb = sa + kBytesA, bar = pair_full0 + 8 * slot;
             const int k0 = (kb + h) * kBlockK;
-            const bool last = end && h == subs - 1;
+            const bool last = ragged && kb + h == blocks - 1;       // 16 rows: a quarter of the bytes
+            if (rank_u == 0)
+              ptx::mbar_arrive_expect_tx(full0 + 8 * slot, last ? pair_bytes * kEnd / kBlockK : pair_bytes);
             if (a_in) {
               if (!kAmn) {
                 ptx::tma_load_3d_pair(sa, &maps.a, k0, mc, tl.e, bar);
@@ -474,10 +496,11 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
             }
           }
         }
-        __syncwarp();
+        if (turn > 1) { s = s1; use = use1; }
         if (++s == (uint32_t)stages) { s = 0; ++use; }
       }
     }
+    __syncwarp();
     // Drain: every stage this CTA filled has been read, so no copy into its
     // shared memory is in flight (bounded).
     for (int i = 0; i < stages; ++i) {
@@ -496,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
       const uint32_t tfull0 = uniform(ptx::smem_u32(&tfull_bar[0])), tempty0 = uniform(ptx::smem_u32(&tempty_bar[0]));
       uint32_t s = 0, use = 0, acc_it = 0;
       bool ok = true;
-      while (ok && walk.next(tl)) {
+      while (ok && walk.template next<true>(tl)) {
         const int blocks = blocks_of<kWgrad>(tl.k_len);
         if (blocks == 0) continue;
         const bool ragged = kWgrad && (tl.k_len & (kEnd - 1)) != 0;
@@ -506,42 +529,43 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
         ptx::tc_fence_after();
         const uint32_t d_tmem = tmem_u + a * kAccCols;
         const uint32_t idesc = ptx::idesc_bf16_f32(kPairM, (uint32_t)tl.n_mma, kWgrad ? 1u : 0u, kAmn ? 1u : 0u);
-        for (int kb = 0; kb < blocks; kb += kSub) {
-          ok = __all_sync(0xffffffffu, wait_bar<true>(full0 + 8 * s, use & 1, ab, kRoleOperands));
+        for (int kb = 0; kb < blocks; kb += kTurn) {
+          const int turn = min(kTurn, blocks - kb);
+          const uint32_t s1 = s + 1 == (uint32_t)stages ? 0 : s + 1, use1 = s1 == 0 ? use + 1 : use;
+          ok = wait_bars<true>(full0 + 8 * s, use & 1, turn > 1, full0 + 8 * s1, use1 & 1, ab, kRoleOperands);
           if (!ok) break;
           ptx::tc_fence_after();
-          // K-major: 16 elements (32 bytes) along the swizzle row, 8-row groups
-          // 1 KB apart.  MN-major: 16 K rows (2 KB), 64-element blocks 8 KB
-          // apart (leading offset), 8-row K groups 1 KB apart (stride offset).
-          const uint32_t sa = base_u + s * stage_bytes;
-          const uint64_t adesc = ptx::smem_desc_sw128(sa, kAmn ? kMnBlock : 16, 1024);
-          const uint64_t bdesc = ptx::smem_desc_sw128(sa + kBytesA, kWgrad ? kMnBlock : 16, 1024);
-          const int subs = min(kSub, blocks - kb);
           if (ptx::elect_one()) {
 #pragma unroll
-            for (int h = 0; h < kSub; ++h) {
-              if (h >= subs) break;
+            for (int h = 0; h < kTurn; ++h) {
+              if (h >= turn) break;
+              // K-major: 16 elements (32 bytes) along the swizzle row, 8-row groups
+              // 1 KB apart.  MN-major: 16 K rows (2 KB), 64-element blocks 8 KB
+              // apart (leading offset), 8-row K groups 1 KB apart (stride offset).
+              const uint32_t slot = h == 0 ? s : s1, sa = base_u + slot * stage_bytes;
+              const uint64_t adesc = ptx::smem_desc_sw128(sa, kAmn ? kMnBlock : 16, 1024);
+              const uint64_t bdesc = ptx::smem_desc_sw128(sa + kBytesA, kWgrad ? kMnBlock : 16, 1024);
               // K-major operands past the contraction's end are zeros of the copy's fill
               const int left = tl.k_len - (kb + h) * kBlockK;
               const int steps = ragged && kb + h == blocks - 1 ? 1 : min(kBlockK / 16, kWgrad ? left / 16 : ceil_div(left, 16));
-              const uint32_t off = h * (sub_bytes >> 4);
 #pragma unroll
               for (int k = 0; k < kBlockK / 16; ++k)
                 if (k < steps)
-                  ptx::umma_bf16_pair(d_tmem, adesc + off + k * (kAmn ? 2048 >> 4 : 32 >> 4),
-                                      bdesc + off + k * (kWgrad ? 2048 >> 4 : 32 >> 4), idesc,
+                  ptx::umma_bf16_pair(d_tmem, adesc + k * (kAmn ? 2048 >> 4 : 32 >> 4),
+                                      bdesc + k * (kWgrad ? 2048 >> 4 : 32 >> 4), idesc,
                                       kb + h > 0 || k > 0 ? 1u : 0u);
+              ptx::umma_commit_pair_multicast(empty0 + 8 * slot, 0x3);
             }
-            ptx::umma_commit_pair_multicast(empty0 + 8 * s, 0x3);
-            if (kb + kSub >= blocks) ptx::umma_commit_pair_multicast(tfull0 + 8 * a, 0x3);
+            if (kb + turn == blocks) ptx::umma_commit_pair_multicast(tfull0 + 8 * a, 0x3);
           }
-          __syncwarp();
+          if (turn > 1) { s = s1; use = use1; }
           if (++s == (uint32_t)stages) { s = 0; ++use; }
         }
         if (!ok) break;
         ++acc_it;
       }
       // every MMA issued has completed before TMEM is released
+      __syncwarp();
       if (ptx::elect_one()) ptx::umma_commit_pair_multicast(ptx::smem_u32(&drain_bar), 0x1);
       __syncwarp();
       ptx::mbar_wait(ptx::smem_u32(&drain_bar), 0, kDrainNs);
@@ -554,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
     uint8_t* const stage = smem_raw + (smem_base - ptx::smem_u32(smem_raw)) + smem_stages(kMode) + (warp - kFirstEpiWarp) * kEpiStage;
     constexpr int kEsz = kBf16 ? 2 : 4;
     constexpr int kWidth = kWgrad && kVec ? 128 / kEsz : 32;     // columns of a chunk
-    uint32_t acc_it = 0;
+    uint32_t acc_it = 0, parts = 0;
     while (walk.next(tl)) {
       const int row0 = tl.m0 + (int)rank * kCtaM + quad * 32, m = row0 + lane;
       const int64_t at0 = kWgrad ? tl.e * p.out_stride + row0 * p.out_ld + tl.n0 : 0;      // the warp's first row
@@ -565,8 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
         for (int j = 0; j < 32; ++j) z[j] = 0;
         for (int c = kWidth * half; c < tl.n; c += 2 * kWidth) {
           if (kVec)
-            put_rows(stage, z, static_cast<uint8_t*>(p.out) + (at0 + c) * kEsz, p.out_ld * kEsz, sh.m - row0,
-                     min(8, (tl.n - c) * kEsz / 16));
+            put_rows(stage, z, &maps.out, tl.n0 + c, row0, tl.e, sh.m - row0, parts);
           else if (m < sh.m)
             store_row<kBf16, false>(p, at0 + lane * p.out_ld + c, min(32, tl.n - c), z);
         }
@@ -588,7 +611,8 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
         const bool last = c + 2 * kWidth >= tl.n_mma;
         __syncwarp();
         if constexpr (kWgrad && kVec) {
-          put_chunk<kBf16, kAccumulate>(p, stage, t_row + c, at0 + c, sh.m - row0, tl.n - c, last, release);
+          put_chunk<kBf16, kAccumulate>(p, &maps.out, stage, t_row + c, tl.n0 + c, row0, tl.e, sh.m - row0, tl.n - c, parts,
+                                        last, release);
           continue;
         }
         uint32_t r[32];
@@ -614,6 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
       }
       ++acc_it;
     }
+    if (kWgrad && kVec && lane == 0) ptx::bulk_wait_all();
     if (!kWgrad) {
       // rows of no expert
       const int64_t lo = start[p.n_experts], width = sh.m;
@@ -721,16 +746,16 @@ EncodeTiledFn encode_fn() {
 }
 
 // A stack of n matrices (width x height, rows ld apart, matrices `stride`
-// apart) in boxes of 64 x box_rows x 1.
+// apart) in boxes of 128 bytes x box_rows x 1.
 bool encode(CUtensorMap* map, const void* base, int64_t width, int64_t height, int64_t ld, int64_t n, int64_t stride,
-            int box_rows) {
+            int box_rows, bool f32 = false) {
   const EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)height, (cuuint64_t)n};
-  const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)stride * 2};
-  const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
+  const cuuint64_t strides[2] = {(cuuint64_t)ld * (f32 ? 4 : 2), (cuuint64_t)stride * (f32 ? 4 : 2)};
+  const cuuint32_t box[3] = {f32 ? 32u : 64u, (cuuint32_t)box_rows, 1};
   const cuuint32_t one[3] = {1, 1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, one,
+  return fn(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, one,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -868,6 +893,9 @@ cudaError_t launch_expert(const ExpertArgs& in, cudaStream_t s) {
     }
     const int64_t esz = a.out_bf16 ? 2 : 4;
     a.out_vec = a.cols * esz % 16 == 0 && (a.n_experts == 1 || a.out_stride * esz % 16 == 0);
+    const int64_t stride = a.n_experts > 1 ? a.out_stride : a.rows * a.out_ld;
+    if (a.out_vec && !encode(&maps.out, a.out, a.cols, a.rows, a.out_ld, a.n_experts, stride, 16, !a.out_bf16))
+      return cudaErrorInvalidValue;
     const int64_t nt = (a.cols + kMaxN - 1) / kMaxN;
     return launch_mode<kExpertWeightGrad>(a, maps, a.n_experts * mt * nt, s);
   }
@@ -887,7 +915,7 @@ cudaError_t launch_expert(const ExpertArgs& in, cudaStream_t s) {
        encode(&maps.b, a.a, k, n, a.a_ld, 1, n * a.a_ld, 32) &&
        encode(&maps.c, a.a, k, n, a.a_ld, 1, n * a.a_ld, 128);
   if (!ok) return cudaErrorInvalidValue;
-  maps.d = maps.c;
+  maps.d = maps.out = maps.c;
   a.prepared = at != in.packs;
   const int64_t tiles = mt * (n / kMaxN + std::min<int64_t>(a.n_experts, n));
   return a.mode == kExpertForward ? launch_mode<kExpertForward>(a, maps, tiles, s)
