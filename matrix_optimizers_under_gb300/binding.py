@@ -307,16 +307,23 @@ def _ptr(t) -> Optional[int]:
         return None
     if isinstance(t, int):
         return t
-    return int(t.data_ptr())
+    return t.data_ptr()
+
+
+_dtype_codes: dict = {}   # torch dtype -> code, filled once torch is there
+_id_codes: dict = {}
+
+
+def _fill_codes() -> None:
+    import torch
+    _dtype_codes.update({torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16})
+    _id_codes.update({torch.int32: ID_I32, torch.int64: ID_I64})
 
 
 def _dtype_code(t) -> int:
-    import torch
-    if t.dtype == torch.float32:
-        return DTYPE_F32
-    if t.dtype == torch.bfloat16:
-        return DTYPE_BF16
-    return 99   # rejected by the library as UNSUPPORTED_DTYPE
+    if not _dtype_codes:
+        _fill_codes()
+    return _dtype_codes.get(t.dtype, 99)   # 99: rejected by the library as UNSUPPORTED_DTYPE
 
 
 def _stream(stream) -> Optional[int]:
@@ -585,21 +592,21 @@ def _rows_of(t, what: str) -> int:
     """Leading dimension of a 2D CUDA tensor with contiguous rows."""
     if not t.is_cuda:
         raise ValueError(f"{what} must be a CUDA tensor")
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or (shape[1] > 1 and stride[1] != 1):
         raise ValueError(f"{what} must be 2D with contiguous rows")
-    ld = t.stride(0)
-    return ld if t.shape[0] > 1 else max(ld, t.shape[1])
+    return stride[0] if shape[0] > 1 else max(stride[0], shape[1])
 
 
 def _id_code(t) -> int:
-    import torch
-    return {torch.int32: ID_I32, torch.int64: ID_I64}.get(t.dtype, 99)
+    if not _id_codes:
+        _fill_codes()
+    return _id_codes.get(t.dtype, 99)
 
 
 def _int32(t, n: int, what: str):
-    import torch
     _flat(t, what)
-    if t.dtype != torch.int32 or t.numel() != n:
+    if _id_code(t) != ID_I32 or t.numel() != n:
         raise ValueError(f"{what} must be {n} int32 elements")
     return t
 
@@ -641,9 +648,8 @@ def grad_clip_workspace_bytes(tensors: GradSet) -> int:
 
 
 def _norm_out(out):
-    import torch
     _flat(out, "out")
-    if out.dtype != torch.float32 or out.numel() < 2:
+    if _dtype_code(out) != DTYPE_F32 or out.numel() < 2:
         raise ValueError("out must be two float32 elements")
     return _ptr(out)
 
@@ -679,7 +685,7 @@ def embedding_lookup(weight, ids, out, *, scale: float = 1.0, stream=None) -> No
     """out[t, :] = scale * weight[ids[t], :]; zeros for an id outside the vocabulary."""
     w_ld, o_ld = _rows_of(weight, "weight"), _rows_of(out, "out")
     n, (vocab, dim) = int(_flat(ids, "ids").numel()), weight.shape
-    if tuple(out.shape) != (n, dim):
+    if out.shape != (n, dim):
         raise ValueError(f"out must be {n} x {dim}")
     _check(_lib.mfsdp_embedding_lookup(_ptr(weight), _dtype_code(weight), vocab, dim, w_ld, _ptr(ids), _id_code(ids),
                                        n, float(scale), _ptr(out), _dtype_code(out), o_ld, _stream(stream)),
@@ -695,7 +701,7 @@ def embedding_grad(dout, ids, grad, workspace, *, scale: float = 1.0, accumulate
     """grad[v, :] = (grad[v, :] +) scale * sum of dout[t, :] over ids[t] = v (see include/mfsdp.h)."""
     d_ld, g_ld = _rows_of(dout, "dout"), _rows_of(grad, "grad")
     n, (vocab, dim) = int(_flat(ids, "ids").numel()), grad.shape
-    if tuple(dout.shape) != (n, dim):
+    if dout.shape != (n, dim):
         raise ValueError(f"dout must be {n} x {dim}")
     _check(_lib.mfsdp_embedding_grad(_ptr(dout), _dtype_code(dout), d_ld, _ptr(ids), _id_code(ids), n, float(scale),
                                      _ptr(grad), _dtype_code(grad), vocab, dim, g_ld, int(bool(accumulate)),
@@ -715,9 +721,10 @@ def _stack(t, what: str) -> int:
     """Element stride between the matrices of a 3D CUDA tensor, each contiguous."""
     if not t.is_cuda:
         raise ValueError(f"{what} must be a CUDA tensor")
-    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1) or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or (shape[2] > 1 and stride[2] != 1) or (shape[1] > 1 and stride[1] != shape[2]):
         raise ValueError(f"{what} must be 3D with contiguous matrices")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+    return stride[0] if shape[0] > 1 else shape[1] * shape[2]
 
 
 def expert_matmul(x, w, starts, y, workspace, *, input_grad: bool = False, stream=None) -> None:
@@ -727,7 +734,7 @@ def expert_matmul(x, w, starts, y, workspace, *, input_grad: bool = False, strea
     e, rows, cols = w.shape
     n = x.shape[0]
     xw, yw = (rows, cols) if input_grad else (cols, rows)
-    if x.shape[1] != xw or tuple(y.shape) != (n, yw):
+    if x.shape[1] != xw or y.shape != (n, yw):
         raise ValueError(f"x must be n x {xw} and y n x {yw}")
     in_dtype = _dtype_code(x) if x.dtype == w.dtype else 99
     _check(_lib.mfsdp_expert_matmul(_ptr(x), x_ld, _ptr(w), w_stride, in_dtype, _ptr(_int32(starts, e + 1, "starts")),
@@ -740,7 +747,7 @@ def expert_weight_grad(dy, x, starts, dw, workspace, *, accumulate: bool = False
     dy_ld, x_ld, dw_stride = _rows_of(dy, "dy"), _rows_of(x, "x"), _stack(dw, "dw")
     e, rows, cols = dw.shape
     n = x.shape[0]
-    if tuple(dy.shape) != (n, rows) or x.shape[1] != cols:
+    if dy.shape != (n, rows) or x.shape[1] != cols:
         raise ValueError(f"dy must be n x {rows} and x n x {cols}")
     in_dtype = _dtype_code(x) if x.dtype == dy.dtype else 99
     _check(_lib.mfsdp_expert_weight_grad(_ptr(dy), dy_ld, _ptr(x), x_ld, in_dtype,

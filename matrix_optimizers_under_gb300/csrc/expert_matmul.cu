@@ -226,20 +226,36 @@ struct TileWalk {
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// `n` (at most 32) consecutive columns of one row of a weight gradient, element
-// by element: rows that do not start on 16-byte boundaries, and edges.
+// 32 columns (`cols` of them in the matrix) of each of a warp's 32 rows (`rows`
+// of them), element by element, for rows that do not start on 16-byte
+// boundaries: through shared memory, so that a store's lanes are neighbours in a row.
+// out: the first row's first element.
 template <bool kBf16, bool kAccumulate>
-__device__ __forceinline__ void store_row(const ExpertArgs& p, int64_t at, int n, const uint32_t (&v)[32]) {
+__device__ __forceinline__ void put_plain(const ExpertArgs& p, uint8_t* stage, const uint32_t (&v)[32], int64_t at,
+                                          int rows, int cols) {
+  const int lane = threadIdx.x & 31;
+  float* const part = reinterpret_cast<float*>(stage);      // 16 rows of 33 floats
 #pragma unroll
-  for (int k = 0; k < 32; ++k) {
-    if (k >= n) continue;
-    const float x = __uint_as_float(v[k]);
-    if constexpr (kBf16) {
-      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + at + k;
-      *o = __float2bfloat16_rn(kAccumulate ? x + __bfloat162float(*o) : x);
-    } else {
-      float* o = static_cast<float*>(p.out) + at + k;
-      *o = kAccumulate ? x + *o : x;
+  for (int h = 0; h < 2; ++h) {
+    __syncwarp();
+    if ((lane >> 4) == h) {
+#pragma unroll
+      for (int c = 0; c < 32; ++c) part[(lane & 15) * 33 + c] = __uint_as_float(v[c]);
+    }
+    __syncwarp();
+    if (lane >= cols) continue;
+#pragma unroll 4
+    for (int r = 0; r < 16; ++r) {
+      if (16 * h + r >= rows) break;
+      const float x = part[r * 33 + lane];
+      const int64_t i = at + (16 * h + r) * p.out_ld + lane;
+      if constexpr (kBf16) {
+        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + i;
+        *o = __float2bfloat16_rn(kAccumulate ? x + __bfloat162float(*o) : x);
+      } else {
+        float* o = static_cast<float*>(p.out) + i;
+        *o = kAccumulate ? x + *o : x;
+      }
     }
   }
 }
@@ -590,8 +606,8 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
         for (int c = kWidth * half; c < tl.n; c += 2 * kWidth) {
           if (kVec)
             put_rows(stage, z, &maps.out, tl.n0 + c, row0, tl.e, sh.m - row0, parts);
-          else if (m < sh.m)
-            store_row<kBf16, false>(p, at0 + lane * p.out_ld + c, min(32, tl.n - c), z);
+          else
+            put_plain<kBf16, false>(p, stage, z, at0 + c, sh.m - row0, tl.n - c);
         }
         continue;
       }
@@ -619,11 +635,11 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
         ptx::tmem_ld_32x32b_x32(t_row + (uint32_t)c, r);
         ptx::tmem_ld_wait();
         if (last) release();
-        if (m >= sh.m) continue;                         // the warp meets again at the next chunk
-        const int cnt = min(32, tl.n - c);
         if constexpr (kWgrad) {
-          store_row<kBf16, kAccumulate>(p, at0 + lane * p.out_ld + c, cnt, r);
+          put_plain<kBf16, kAccumulate>(p, stage, r, at0 + c, sh.m - row0, tl.n - c);
         } else {
+          if (m >= sh.m) continue;                       // the warp meets again at the next chunk
+          const int cnt = min(32, tl.n - c);
           // lanes are neighbours in memory: 64 (bf16) or 128 bytes a token
           const int64_t at = (int64_t)(tl.group + tl.n0 + c) * p.out_ld + m;
 #pragma unroll
@@ -663,69 +679,73 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
   }
 }
 
-// Rows of `width` elements, ld apart, into rows of `width8` (width rounded up
-// to 8, zero-filled): the form whose rows start on 16-byte boundaries.  With
-// `starts`, matrix e (its `rows` rows) is copied only if its group has a token.
-__global__ void __launch_bounds__(256) pack_kernel(const uint16_t* src, int64_t stride, int64_t ld, uint16_t* dst,
-                                                   int64_t rows, int width, int width8, const int32_t* starts) {
-  ptx::launch_dependents();
-  if (starts && starts[blockIdx.y + 1] <= (blockIdx.y ? starts[blockIdx.y] : 0)) return;
-  const int per = width8 >> 3;
-  src += blockIdx.y * stride;
-  dst += (int64_t)blockIdx.y * rows * width8;
-  const int64_t total = rows * per;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t r = i / per;
-    const int c = (int)(i - r * per) * 8;
-    const uint16_t* s = src + r * ld + c;
-    uint32_t w[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t lo = c + 2 * k < width ? s[2 * k] : 0, hi = c + 2 * k + 1 < width ? s[2 * k + 1] : 0;
-      w[k] = lo | (hi << 16);
-    }
-    *reinterpret_cast<uint4*>(dst + r * width8 + c) = make_uint4(w[0], w[1], w[2], w[3]);
-  }
-}
-
-// The padded ends of the groups: the last len % 16 rows of each group of x
-// (width wide, ld apart), then zeros, as rows 16 e .. 16 e + 15 of dst (width8 wide).  One
-// CTA an expert and operand; a length that is a multiple of 16 needs none.
-struct EndArgs {
-  const uint16_t* x[2];
-  int64_t ld[2];
-  uint16_t* dst[2];
-  int32_t width[2], width8[2];
+// What a call prepares for its tensor copies, in one launch: copies of operands
+// whose rows do not start on 16-byte boundaries (`rows` rows of `width` elements, ld
+// apart, of each of n matrices `stride` apart, into rows of width8 elements, zero-filled; a matrix
+// without tokens is left out), and the padded ends of the groups (rows 16 e ..
+// 16 e + 15: the last len % 16 rows of group e, then zeros; a length that is
+// a multiple of 16 needs none).
+struct PrepareJob {
+  const uint16_t* src;
+  uint16_t* dst;
+  int64_t ld, stride, rows;
+  int32_t width, width8, n;
+  int32_t ends;            // 1: the groups' ends
+  int32_t of_experts;      // 1: the n matrices are the experts'
+  int32_t block0, per;     // first block of the job, blocks of a matrix
+};
+struct PrepareArgs {
+  PrepareJob job[4];
+  int32_t jobs;
+  int32_t blocks;
   const int32_t* starts;
   int64_t n_rows;
 };
-__global__ void __launch_bounds__(256) group_end_kernel(const __grid_constant__ EndArgs a) {
-  ptx::launch_dependents();
-  const int e = blockIdx.x, o = blockIdx.y;
-  const int n = (int)a.n_rows;
-  const int lo = e == 0 ? 0 : min(max(a.starts[e], 0), n), hi = min(max(a.starts[e + 1], 0), n);
-  const int rest = max(0, hi - lo) & (kEnd - 1);
-  if (rest == 0) return;
-  const int per = a.width8[o] >> 3;
-  const bool vec = a.ld[o] % 8 == 0 && a.width[o] % 8 == 0;
-  for (int i = threadIdx.x; i < kEnd * per; i += 256) {
-    const int r = i / per, c = (i - r * per) * 8;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (r < rest) {
-      const uint16_t* s = a.x[o] + (int64_t)(hi - rest + r) * a.ld[o] + c;
-      if (vec) {
-        v = *reinterpret_cast<const uint4*>(s);
-      } else {
-        uint32_t w[4];
+constexpr int kPrepareThreads = 256;
+
+// 8 elements from column c of a row of `width`, zero past it.
+__device__ __forceinline__ uint4 load8(const uint16_t* row, int c, int width, bool vec) {
+  if (vec) return *reinterpret_cast<const uint4*>(row + c);
+  uint32_t w[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t x = c + 2 * k < a.width[o] ? s[2 * k] : 0, y = c + 2 * k + 1 < a.width[o] ? s[2 * k + 1] : 0;
-          w[k] = x | (y << 16);
-        }
-        v = make_uint4(w[0], w[1], w[2], w[3]);
-      }
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t x = c + 2 * k < width ? row[c + 2 * k] : 0, y = c + 2 * k + 1 < width ? row[c + 2 * k + 1] : 0;
+    w[k] = x | (y << 16);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(const __grid_constant__ PrepareArgs a) {
+  ptx::launch_dependents();
+  int k = 0;
+  while (k + 1 < a.jobs && (int)blockIdx.x >= a.job[k + 1].block0) ++k;
+  const PrepareJob& j = a.job[k];
+  const int e = (blockIdx.x - j.block0) / j.per, part = (blockIdx.x - j.block0) - e * j.per;
+  const int chunks = j.width8 >> 3, n = (int)a.n_rows;
+  int lo = 0, hi = 0;
+  if (j.of_experts) {
+    lo = e == 0 ? 0 : min(max(a.starts[e], 0), n);
+    hi = min(max(a.starts[e + 1], 0), n);
+  }
+  if (j.ends) {
+    const int rest = max(0, hi - lo) & (kEnd - 1);
+    if (rest == 0) return;
+    const bool vec = j.ld % 8 == 0 && j.width % 8 == 0;
+    for (int i = part * kPrepareThreads + threadIdx.x; i < kEnd * chunks; i += j.per * kPrepareThreads) {
+      const int r = i / chunks, c = (i - r * chunks) * 8;
+      const uint4 v = r < rest ? load8(j.src + (int64_t)(hi - rest + r) * j.ld, c, j.width, vec) : make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(j.dst + ((int64_t)e * kEnd + r) * j.width8 + c) = v;
     }
-    *reinterpret_cast<uint4*>(a.dst[o] + ((int64_t)e * kEnd + r) * a.width8[o] + c) = v;
+    return;
+  }
+  if (j.of_experts && hi <= lo) return;
+  const uint16_t* src = j.src + e * j.stride;
+  uint16_t* dst = j.dst + (int64_t)e * j.rows * j.width8;
+  const int64_t total = j.rows * chunks;
+  for (int64_t i = (int64_t)part * kPrepareThreads + threadIdx.x; i < total; i += (int64_t)j.per * kPrepareThreads) {
+    const int64_t r = i / chunks;
+    const int c = (int)(i - r * chunks) * 8;
+    *reinterpret_cast<uint4*>(dst + r * j.width8 + c) = load8(src + r * j.ld, c, j.width, false);
   }
 }
 
@@ -819,104 +839,93 @@ cudaError_t launch_mode(const ExpertArgs& a, const Maps& maps, int64_t max_tiles
 
 int64_t up8(int64_t x) { return (x + 7) / 8 * 8; }
 
-cudaError_t pack(const void* src, int64_t stride, int64_t ld, void* dst, int64_t rows, int64_t width, int n,
-                 const int32_t* starts, cudaStream_t s) {
-  const int64_t blocks = std::min<int64_t>((rows * (up8(width) / 8) + 255) / 256, (int64_t)sm_count() * 8);
-  pack_kernel<<<dim3((unsigned)blocks, (unsigned)n), 256, 0, s>>>(static_cast<const uint16_t*>(src), stride, ld,
-                                                                  static_cast<uint16_t*>(dst), rows, (int)width,
-                                                                  (int)up8(width), starts);
-  return cudaGetLastError();
-}
+// The jobs of one call and the workspace they fill.
+struct Prepare {
+  PrepareArgs a{};
+  uint8_t* at;
 
-// Activations n x width, ld apart, ready for the tensor copies: in place when
-// every row starts on a 16-byte boundary (a single row always does), else
-// packed at *at.
-cudaError_t aligned_rows(const void** x, int64_t* ld, int64_t n, int64_t width, uint8_t** at, cudaStream_t s) {
-  if (n <= 1) {
-    *ld = up8(width);
-    return cudaSuccess;
+  Prepare(const ExpertArgs& p) : at(p.packs) {
+    a.starts = p.starts;
+    a.n_rows = p.n_rows;
   }
-  if (*ld % 8 == 0) return cudaSuccess;
-  const cudaError_t e = pack(*x, 0, *ld, *at, n, width, 1, nullptr, s);
-  *x = *at;
-  *ld = up8(width);
-  *at += packed_bytes(n, width);
-  return e;
-}
+  const void* add(const void* src, int64_t ld, int64_t stride, int64_t rows, int64_t width, int n, bool of_experts,
+                  bool ends) {
+    PrepareJob& j = a.job[a.jobs++];
+    j.src = static_cast<const uint16_t*>(src);
+    j.dst = reinterpret_cast<uint16_t*>(at);
+    j.ld = ld;
+    j.stride = stride;
+    j.rows = rows;
+    j.width = (int32_t)width;
+    j.width8 = (int32_t)up8(width);
+    j.n = n;
+    j.of_experts = of_experts;
+    j.ends = ends;
+    j.block0 = a.blocks;
+    const int64_t share = std::max<int64_t>(1, (int64_t)sm_count() * 8 / n);       // enough blocks to fill the GPU
+    j.per = (int32_t)std::min<int64_t>(ends ? 1 : share, (rows * (up8(width) / 8) + kPrepareThreads - 1) / kPrepareThreads);
+    a.blocks += j.per * n;
+    at += packed_bytes(n * rows, width);
+    return j.dst;
+  }
+  // Activations n x width, ld apart: in place when every row starts on a 16-byte
+  // boundary (a single row always does), else packed.
+  void rows(const void** x, int64_t* ld, int64_t n, int64_t width) {
+    if (n > 1 && *ld % 8 != 0) *x = add(*x, *ld, 0, n, width, 1, false, false);
+    if (n <= 1 || *ld % 8 != 0) *ld = up8(width);
+  }
+  cudaError_t launch(cudaStream_t s) const {
+    if (a.jobs == 0) return cudaSuccess;
+    prepare_kernel<<<(unsigned)a.blocks, kPrepareThreads, 0, s>>>(a);
+    return cudaGetLastError();
+  }
+};
 
 }  // namespace
 
 cudaError_t launch_expert(const ExpertArgs& in, cudaStream_t s) {
   ExpertArgs a = in;
   const int64_t n = a.n_rows, mt = ((a.mode == kExpertInputGrad ? a.cols : a.rows) + kPairM - 1) / kPairM;
-  uint8_t* at = a.packs;
-  Maps maps;
-  cudaError_t e;
-  bool ok;
+  Prepare prep(a);
+  Maps maps{};
+  bool ok = true;
   // The longest wait is the epilogue's for a tile's whole contraction: 2 s, and
   // 64 ns for each of its K (8 clocks at the MMA's rate, at 1 GHz, 8 times over).
   const int64_t k_max = a.mode == kExpertWeightGrad ? n : (a.mode == kExpertForward ? a.cols : a.rows);
   a.wait_limit_ns = 2000000000ull + 64ull * (uint64_t)k_max;
   if (a.mode == kExpertWeightGrad) {
-    if (n > 0) {
-      e = aligned_rows(&a.a, &a.a_ld, n, a.rows, &at, s);
-      if (e != cudaSuccess) return e;
-      e = aligned_rows(&a.b, &a.b_ld, n, a.cols, &at, s);
-      if (e != cudaSuccess) return e;
+    if (n > 0) {                                   // without rows no tile has a contraction, and no copy is issued
+      prep.rows(&a.a, &a.a_ld, n, a.rows);
+      prep.rows(&a.b, &a.b_ld, n, a.cols);
+      const void* end_a = prep.add(in.a, in.a_ld, 0, kEnd, a.rows, a.n_experts, true, true);
+      const void* end_b = prep.add(in.b, in.b_ld, 0, kEnd, a.cols, a.n_experts, true, true);
+      const int64_t m = (int64_t)a.n_experts * kEnd, ea = up8(a.rows), eb = up8(a.cols);
       ok = encode(&maps.a, a.a, a.rows, n, a.a_ld, 1, n * a.a_ld, 64) &&
-           encode(&maps.b, a.b, a.cols, n, a.b_ld, 1, n * a.b_ld, 64);
-      if (!ok) return cudaErrorInvalidValue;
-      EndArgs ends;
-      ends.x[0] = static_cast<const uint16_t*>(in.a);
-      ends.x[1] = static_cast<const uint16_t*>(in.b);
-      ends.ld[0] = in.a_ld;
-      ends.ld[1] = in.b_ld;
-      const int64_t width[2] = {a.rows, a.cols};
-      for (int o = 0; o < 2; ++o) {
-        ends.dst[o] = reinterpret_cast<uint16_t*>(at);
-        ends.width[o] = (int32_t)width[o];
-        ends.width8[o] = (int32_t)up8(width[o]);
-        at += packed_bytes((int64_t)a.n_experts * kEnd, width[o]);
-      }
-      ends.starts = a.starts;
-      ends.n_rows = n;
-      group_end_kernel<<<dim3((unsigned)a.n_experts, 2), 256, 0, s>>>(ends);
-      e = cudaGetLastError();
-      if (e != cudaSuccess) return e;
-      a.prepared = 1;
-      const int64_t m = (int64_t)a.n_experts * kEnd;
-      ok = encode(&maps.c, ends.dst[0], a.rows, m, ends.width8[0], 1, m * ends.width8[0], kEnd) &&
-           encode(&maps.d, ends.dst[1], a.cols, m, ends.width8[1], 1, m * ends.width8[1], kEnd);
-      if (!ok) return cudaErrorInvalidValue;
-    } else {
-      maps = Maps{};       // no tile has a contraction: no copy is issued
+           encode(&maps.b, a.b, a.cols, n, a.b_ld, 1, n * a.b_ld, 64) &&
+           encode(&maps.c, end_a, a.rows, m, ea, 1, m * ea, kEnd) && encode(&maps.d, end_b, a.cols, m, eb, 1, m * eb, kEnd);
     }
     const int64_t esz = a.out_bf16 ? 2 : 4;
     a.out_vec = a.cols * esz % 16 == 0 && (a.n_experts == 1 || a.out_stride * esz % 16 == 0);
     const int64_t stride = a.n_experts > 1 ? a.out_stride : a.rows * a.out_ld;
-    if (a.out_vec && !encode(&maps.out, a.out, a.cols, a.rows, a.out_ld, a.n_experts, stride, 16, !a.out_bf16))
-      return cudaErrorInvalidValue;
-    const int64_t nt = (a.cols + kMaxN - 1) / kMaxN;
-    return launch_mode<kExpertWeightGrad>(a, maps, a.n_experts * mt * nt, s);
+    if (a.out_vec) ok = ok && encode(&maps.out, a.out, a.cols, a.rows, a.out_ld, a.n_experts, stride, 16, !a.out_bf16);
+  } else {
+    const int64_t k = a.mode == kExpertForward ? a.cols : a.rows;
+    if (a.cols % 8 != 0 || (a.n_experts > 1 && a.b_stride % 8 != 0)) {
+      a.b = prep.add(a.b, a.b_ld, a.b_stride, a.rows, a.cols, a.n_experts, true, false);
+      a.b_ld = up8(a.cols);
+      a.b_stride = a.rows * a.b_ld;
+    }
+    prep.rows(&a.a, &a.a_ld, n, k);
+    const int64_t w_stride = a.n_experts > 1 ? a.b_stride : a.rows * a.b_ld;
+    ok = encode(&maps.a, a.b, a.cols, a.rows, a.b_ld, a.n_experts, w_stride, a.mode == kExpertForward ? 128 : 64) &&
+         encode(&maps.b, a.a, k, n, a.a_ld, 1, n * a.a_ld, 32) && encode(&maps.c, a.a, k, n, a.a_ld, 1, n * a.a_ld, 128);
   }
-  const int64_t k = a.mode == kExpertForward ? a.cols : a.rows;
-  if (a.cols % 8 != 0 || (a.n_experts > 1 && a.b_stride % 8 != 0)) {
-    e = pack(a.b, a.b_stride, a.b_ld, at, a.rows, a.cols, a.n_experts, a.starts, s);
-    if (e != cudaSuccess) return e;
-    a.b = at;
-    a.b_ld = up8(a.cols);
-    a.b_stride = a.rows * a.b_ld;
-    at += packed_bytes(a.n_experts * a.rows, a.cols);
-  }
-  e = aligned_rows(&a.a, &a.a_ld, n, k, &at, s);
-  if (e != cudaSuccess) return e;
-  const int64_t w_stride = a.n_experts > 1 ? a.b_stride : a.rows * a.b_ld;
-  ok = encode(&maps.a, a.b, a.cols, a.rows, a.b_ld, a.n_experts, w_stride, a.mode == kExpertForward ? 128 : 64) &&
-       encode(&maps.b, a.a, k, n, a.a_ld, 1, n * a.a_ld, 32) &&
-       encode(&maps.c, a.a, k, n, a.a_ld, 1, n * a.a_ld, 128);
   if (!ok) return cudaErrorInvalidValue;
-  maps.d = maps.out = maps.c;
-  a.prepared = at != in.packs;
+  a.prepared = prep.a.jobs > 0;
+  const cudaError_t e = prep.launch(s);
+  if (e != cudaSuccess) return e;
+  if (a.mode == kExpertWeightGrad)
+    return launch_mode<kExpertWeightGrad>(a, maps, a.n_experts * mt * ((a.cols + kMaxN - 1) / kMaxN), s);
   const int64_t tiles = mt * (n / kMaxN + std::min<int64_t>(a.n_experts, n));
   return a.mode == kExpertForward ? launch_mode<kExpertForward>(a, maps, tiles, s)
                                   : launch_mode<kExpertInputGrad>(a, maps, tiles, s);
