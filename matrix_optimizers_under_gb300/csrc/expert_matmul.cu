@@ -53,14 +53,14 @@ constexpr int kBlockK = 64;               // K of a stage: one 128-byte swizzle 
 constexpr int kBytesA = kCtaM * kBlockK * 2;          // 16 KB
 constexpr int kMnBlock = 64 * kBlockK * 2;            // 8 KB: 64 MN elements x 64 K rows (MN-major)
 constexpr int kEnd = 16;                              // K of one MMA: rows of a group's padded end
-constexpr int kEpiPart = 2048;                        // 16 rows of 128 bytes
-constexpr int kEpiStage = 2 * kEpiPart;               // weight gradient: staging of an epilogue warp
 constexpr int kMaxStages = 10;
 // The producer and the issuer take two stages at a time: a turn of their loops
-// (waits, election, counters) costs ~400 cycles, and a stage's MMAs take 512.
+// (election, counters) costs ~300 cycles, and a stage's MMAs take 512.
 constexpr int kTurn = 2;
-// Shared memory of the stages: six of 32 KB, or ten of 20 KB (the weight gradient has none so small).
-constexpr int smem_stages(int mode) { return mode == kExpertWeightGrad ? 6 * 32768 : 10 * 20480; }
+// Shared memory of the stages (six of 32 KB, or ten of 20 KB), and of a part of an
+// epilogue warp's staging, which has two.
+constexpr int kRingBytes(int mode) { return mode == kExpertWeightGrad ? 6 * 32768 : 10 * 20480; }
+constexpr int kPartBytes(int mode) { return mode == kExpertWeightGrad ? 2048 : 1024; }
 constexpr int kEpiWarps = 8;
 constexpr int kFirstEpiWarp = 4;
 constexpr int kThreads = 32 * (kFirstEpiWarp + kEpiWarps);
@@ -71,9 +71,9 @@ constexpr uint64_t kDrainNs = 2000000000ull;          // limit of the waits that
 struct Maps {
   CUtensorMap a;      // box 64 x 128 (K-major A) or 64 x 64
   CUtensorMap b;      // box 64 x 32 (K-major B) or 64 x 64
-  CUtensorMap c;      // box 64 x 128 (K-major B of a full tile); weight gradient: the padded ends of A, box 64 x 16
-  CUtensorMap d;      // weight gradient: the padded ends of B, box 64 x 16
-  CUtensorMap out;    // weight gradient: dW, box 128 bytes x 16
+  CUtensorMap c;      // box 64 x 128 (K-major B); weight gradient: the padded ends of A, box 64 x 16
+  CUtensorMap d;      // box 64 x 64 (K-major B); weight gradient: the padded ends of B, box 64 x 16
+  CUtensorMap out;    // dW, box 128 bytes x 16; or Y, box 32 elements x 1 KB
 };
 
 // First failing wait of a launch: (role << 0); the wait's limit.
@@ -100,15 +100,6 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const Ab
       return false;
     }
   }
-}
-
-// The same for a stage, and if `two` for the next one too.
-template <bool kCluster>
-__device__ __forceinline__ bool wait_bars(uint32_t bar0, uint32_t parity0, bool two, uint32_t bar1, uint32_t parity1,
-                                          const Abort& ab, int32_t role) {
-  bool ok = wait_bar<kCluster>(bar0, parity0, ab, role);
-  if (ok && two) ok = wait_bar<kCluster>(bar1, parity1, ab, role);
-  return __all_sync(0xffffffffu, ok);
 }
 
 // One tile: `rows` [m0, m0 + 256) of the M side, columns [n0, n0 + n) of the N
@@ -139,6 +130,9 @@ __device__ __forceinline__ int blocks_of(int k) {
 __device__ __forceinline__ int even_width(int n, int parts, int step = kStepN) {
   return (ceil_div(n, parts) + step - 1) / step * step;
 }
+
+// Rows of shared memory that one CTA's nh columns of a K-major B take: the copies' boxes.
+__device__ __forceinline__ uint32_t rows_b(int nh) { return nh > 96 ? 128 : ceil_div(nh, 32) * 32; }
 
 // First token of expert e's group, kept inside the rows there are.
 __device__ __forceinline__ int start_of(const ExpertArgs& p, int e) {
@@ -176,6 +170,18 @@ __device__ __forceinline__ Tile decode(const ExpertArgs& p, const Shape& sh, con
   }
   r.n_mma = (r.n + kStepN - 1) / kStepN * kStepN;
   return r;
+}
+
+// `rows` (32, 64, 96 or 128) rows of K-major B, K columns k0 on, from token t on.
+__device__ __forceinline__ void load_tokens(const Maps& maps, uint32_t sb, uint32_t rows, int k0, int t, uint32_t bar) {
+  if (rows == 128) {
+    ptx::tma_load_3d_pair(sb, &maps.c, k0, t, 0, bar);
+  } else if (rows >= 64) {
+    ptx::tma_load_3d_pair(sb, &maps.d, k0, t, 0, bar);
+    if (rows > 64) ptx::tma_load_3d_pair(sb + 8192, &maps.b, k0, t + 64, 0, bar);
+  } else {
+    ptx::tma_load_3d_pair(sb, &maps.b, k0, t, 0, bar);
+  }
 }
 
 // A value that all lanes hold, as the compiler can see.
@@ -273,7 +279,7 @@ __device__ __forceinline__ void put_rows(uint8_t* stage, const uint32_t (&w)[32]
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     if (16 * h >= rows) break;
-    uint8_t* const part = stage + (parts++ & 1) * kEpiPart;
+    uint8_t* const part = stage + (parts++ & 1) * kPartBytes(kExpertWeightGrad);
     if (lane == 0) ptx::bulk_wait_read<1>();           // the copy before the last has left this part
     __syncwarp();
     if ((lane >> 4) == h) {
@@ -351,8 +357,52 @@ __device__ __forceinline__ void put_chunk(const ExpertArgs& p, const CUtensorMap
   put_rows(stage, w, map, x, y, z, rows, parts);
 }
 
-// kBf16: the output's type.  Weight gradient: kAccumulate, and kVec: the rows
-// of dW start on 16-byte boundaries.
+// 32 tokens (`cnt` of them the group's) of a warp's 32 rows of M, lane l holding
+// row l's in `r`: 64 or 128 bytes of each token's row of Y.  Whole pieces of 1 KB (16
+// tokens, or 8 in fp32) go through shared memory and out by tensor copies, off
+// the warp's path (2700 cycles a chunk with its own 2-byte stores); the last tokens
+// of a group, whose neighbours are another's, and layouts whose rows do not start
+// on 16-byte boundaries, by stores.
+template <bool kBf16, bool kVec>
+__device__ __forceinline__ void put_tokens(const ExpertArgs& p, const CUtensorMap* map, uint8_t* stage,
+                                           const uint32_t (&r)[32], int row0, int rows, int token, int cnt,
+                                           uint32_t& parts) {
+  constexpr int kPiece = kBf16 ? 16 : 8;
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int q = 0; q < 32 / kPiece; ++q) {
+    if (q * kPiece >= cnt) break;
+    if (kVec && (q + 1) * kPiece <= cnt) {
+      uint8_t* const part = stage + (parts++ & 1) * kPartBytes(kExpertForward);
+      if (lane == 0) ptx::bulk_wait_read<1>();         // the copy before the last has left this part
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < kPiece; ++j) {
+        const float x = __uint_as_float(r[q * kPiece + j]);
+        if constexpr (kBf16) reinterpret_cast<__nv_bfloat16*>(part)[32 * j + lane] = __float2bfloat16_rn(x);
+        else reinterpret_cast<float*>(part)[32 * j + lane] = x;
+      }
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        ptx::tma_store_3d(map, ptx::smem_u32(part), row0, token + q * kPiece, 0);
+        ptx::bulk_commit();
+      }
+    } else if (lane < rows) {
+      const int64_t at = (int64_t)(token + q * kPiece) * p.out_ld + row0 + lane;
+#pragma unroll
+      for (int j = 0; j < kPiece; ++j) {
+        if (q * kPiece + j >= cnt) break;
+        const float x = __uint_as_float(r[q * kPiece + j]);
+        if constexpr (kBf16) static_cast<__nv_bfloat16*>(p.out)[at + j * p.out_ld] = __float2bfloat16_rn(x);
+        else static_cast<float*>(p.out)[at + j * p.out_ld] = x;
+      }
+    }
+  }
+}
+
+// kBf16: the output's type.  kVec: its rows start on 16-byte boundaries.
+// kAccumulate: weight gradient.
 template <int kMode, bool kBf16, bool kAccumulate, bool kVec>
 __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_constant__ ExpertArgs p,
                                                              const __grid_constant__ Maps maps) {
@@ -442,9 +492,8 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
   Tile tl;
   // Shared memory of a stage: A, then this CTA's half of B.
   const int wide = kWgrad ? sh.width_n : widest;
-  const int bytes_b_max = kWgrad ? ceil_div(wide / 2, 64) * kMnBlock : (wide / 2 > 96 ? 128 : ceil_div(wide / 2, 32) * 32) * 128;
-  const uint32_t stage_bytes = kBytesA + bytes_b_max;
-  const int stages = min(kMaxStages, smem_stages(kMode) / (int)stage_bytes);
+  const uint32_t stage_bytes = kBytesA + (kWgrad ? ceil_div(wide / 2, 64) * kMnBlock : rows_b(wide / 2) * 128);
+  const int stages = min(kMaxStages, kRingBytes(kMode) / (int)stage_bytes);
 
   if (warp == 0) {
     // -------------------------------------------------------------- producer
@@ -462,27 +511,28 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
     __syncwarp();
     uint32_t s = 0, use = 0;
     bool ok = true;
-    while (ok && walk.next(tl)) {
+    while (walk.next(tl)) {
       const int blocks = blocks_of<kWgrad>(tl.k_len);
       const int nh = tl.n_mma >> 1;                         // this CTA's columns of B
       const int mc = tl.m0 + (int)rank_u * kCtaM;
       // rows wholly past the matrix are not loaded (their output is not stored)
       const bool a_in = mc < sh.m;
-      const int copies_b = kWgrad ? ceil_div(nh, 64) : (nh > 96 ? 1 : ceil_div(nh, 32));
-      const uint32_t bytes_b = kWgrad ? copies_b * kMnBlock : (nh > 96 ? 128u : 32u * copies_b) * 128u;
+      const int copies_b = ceil_div(nh, 64);                // weight gradient
+      const uint32_t rows = rows_b(nh), bytes_b = kWgrad ? copies_b * kMnBlock : rows * 128;
       const uint32_t pair_bytes = (tl.m0 + kCtaM < sh.m ? 2u : 1u) * kBytesA + 2u * bytes_b;
       const bool ragged = kWgrad && (tl.k_len & (kEnd - 1)) != 0;
       const int nc = tl.n0 + (int)rank_u * nh;
       for (int kb = 0; kb < blocks; kb += kTurn) {
         const int turn = min(kTurn, blocks - kb);
         const uint32_t s1 = s + 1 == (uint32_t)stages ? 0 : s + 1, use1 = s1 == 0 ? use + 1 : use;
-        ok = wait_bars<false>(empty0 + 8 * s, (use & 1) ^ 1, turn > 1, empty0 + 8 * s1, (use1 & 1) ^ 1, ab, kRoleStage);
-        if (!ok) break;
         if (ptx::elect_one()) {
 #pragma unroll
           for (int h = 0; h < kTurn; ++h) {
             if (h >= turn) break;
-            const uint32_t slot = h == 0 ? s : s1;
+            const uint32_t slot = h == 0 ? s : s1, slot_use = h == 0 ? use : use1;
+            // after a wait that gave up, the leader issues nothing more
+            ok = ok && wait_bar<false>(empty0 + 8 * slot, (slot_use & 1) ^ 1, ab, kRoleStage);
+            if (!ok) break;
             const uint32_t sa = base_u + slot * stage_bytes, sb = sa + kBytesA, bar = pair_full0 + 8 * slot;
             const int k0 = (kb + h) * kBlockK;
             const bool last = ragged && kb + h == blocks - 1;       // 16 rows: a quarter of the bytes
@@ -503,12 +553,8 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
               const int y = last ? tl.e * kEnd : tl.group + k0;
               ptx::tma_load_3d_pair(sb, map, nc, y, 0, bar);
               if (copies_b > 1) ptx::tma_load_3d_pair(sb + kMnBlock, map, nc + 64, y, 0, bar);
-            } else if (nh > 96) {
-              ptx::tma_load_3d_pair(sb, &maps.c, k0, tl.group + nc, 0, bar);
             } else {
-              ptx::tma_load_3d_pair(sb, &maps.b, k0, tl.group + nc, 0, bar);
-              if (copies_b > 1) ptx::tma_load_3d_pair(sb + 4096, &maps.b, k0, tl.group + nc + 32, 0, bar);
-              if (copies_b > 2) ptx::tma_load_3d_pair(sb + 8192, &maps.b, k0, tl.group + nc + 64, 0, bar);
+              load_tokens(maps, sb, rows, k0, tl.group + nc, bar);
             }
           }
         }
@@ -535,30 +581,29 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
       const uint32_t tfull0 = uniform(ptx::smem_u32(&tfull_bar[0])), tempty0 = uniform(ptx::smem_u32(&tempty_bar[0]));
       uint32_t s = 0, use = 0, acc_it = 0;
       bool ok = true;
-      while (ok && walk.template next<true>(tl)) {
+      while (walk.template next<true>(tl)) {
         const int blocks = blocks_of<kWgrad>(tl.k_len);
         if (blocks == 0) continue;
         const bool ragged = kWgrad && (tl.k_len & (kEnd - 1)) != 0;
-        const uint32_t a = acc_it & 1;
-        ok = __all_sync(0xffffffffu, wait_bar<true>(tempty0 + 8 * a, ((acc_it >> 1) & 1) ^ 1, ab, kRoleAccFree));
-        if (!ok) break;
-        ptx::tc_fence_after();
+        const uint32_t a = acc_it & 1, acc_parity = ((acc_it >> 1) & 1) ^ 1;
         const uint32_t d_tmem = tmem_u + a * kAccCols;
         const uint32_t idesc = ptx::idesc_bf16_f32(kPairM, (uint32_t)tl.n_mma, kWgrad ? 1u : 0u, kAmn ? 1u : 0u);
         for (int kb = 0; kb < blocks; kb += kTurn) {
           const int turn = min(kTurn, blocks - kb);
           const uint32_t s1 = s + 1 == (uint32_t)stages ? 0 : s + 1, use1 = s1 == 0 ? use + 1 : use;
-          ok = wait_bars<true>(full0 + 8 * s, use & 1, turn > 1, full0 + 8 * s1, use1 & 1, ab, kRoleOperands);
-          if (!ok) break;
-          ptx::tc_fence_after();
           if (ptx::elect_one()) {
+            if (kb == 0) ok = ok && wait_bar<true>(tempty0 + 8 * a, acc_parity, ab, kRoleAccFree);
 #pragma unroll
             for (int h = 0; h < kTurn; ++h) {
               if (h >= turn) break;
+              const uint32_t slot = h == 0 ? s : s1, slot_use = h == 0 ? use : use1;
+              ok = ok && wait_bar<true>(full0 + 8 * slot, slot_use & 1, ab, kRoleOperands);
+              if (!ok) break;
+              ptx::tc_fence_after();
               // K-major: 16 elements (32 bytes) along the swizzle row, 8-row groups
               // 1 KB apart.  MN-major: 16 K rows (2 KB), 64-element blocks 8 KB
               // apart (leading offset), 8-row K groups 1 KB apart (stride offset).
-              const uint32_t slot = h == 0 ? s : s1, sa = base_u + slot * stage_bytes;
+              const uint32_t sa = base_u + slot * stage_bytes;
               const uint64_t adesc = ptx::smem_desc_sw128(sa, kAmn ? kMnBlock : 16, 1024);
               const uint64_t bdesc = ptx::smem_desc_sw128(sa + kBytesA, kWgrad ? kMnBlock : 16, 1024);
               // K-major operands past the contraction's end are zeros of the copy's fill
@@ -572,12 +617,11 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
                                       kb + h > 0 || k > 0 ? 1u : 0u);
               ptx::umma_commit_pair_multicast(empty0 + 8 * slot, 0x3);
             }
-            if (kb + turn == blocks) ptx::umma_commit_pair_multicast(tfull0 + 8 * a, 0x3);
+            if (ok && kb + turn == blocks) ptx::umma_commit_pair_multicast(tfull0 + 8 * a, 0x3);
           }
           if (turn > 1) { s = s1; use = use1; }
           if (++s == (uint32_t)stages) { s = 0; ++use; }
         }
-        if (!ok) break;
         ++acc_it;
       }
       // every MMA issued has completed before TMEM is released
@@ -591,12 +635,13 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
     // Warp w reads TMEM lane quadrant w % 4; the two warps of a quadrant take
     // alternate chunks of 32 columns.
     const int quad = warp & 3, half = (warp - kFirstEpiWarp) >> 2;
-    uint8_t* const stage = smem_raw + (smem_base - ptx::smem_u32(smem_raw)) + smem_stages(kMode) + (warp - kFirstEpiWarp) * kEpiStage;
+    uint8_t* const stage = smem_raw + (smem_base - ptx::smem_u32(smem_raw)) + kRingBytes(kMode) +
+                           (warp - kFirstEpiWarp) * 2 * kPartBytes(kMode);
     constexpr int kEsz = kBf16 ? 2 : 4;
     constexpr int kWidth = kWgrad && kVec ? 128 / kEsz : 32;     // columns of a chunk
     uint32_t acc_it = 0, parts = 0;
     while (walk.next(tl)) {
-      const int row0 = tl.m0 + (int)rank * kCtaM + quad * 32, m = row0 + lane;
+      const int row0 = tl.m0 + (int)rank * kCtaM + quad * 32;
       const int64_t at0 = kWgrad ? tl.e * p.out_stride + row0 * p.out_ld + tl.n0 : 0;      // the warp's first row
       if (kWgrad && tl.k_len == 0) {
         if (kAccumulate) continue;
@@ -638,23 +683,13 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
         if constexpr (kWgrad) {
           put_plain<kBf16, kAccumulate>(p, stage, r, at0 + c, sh.m - row0, tl.n - c);
         } else {
-          if (m >= sh.m) continue;                       // the warp meets again at the next chunk
-          const int cnt = min(32, tl.n - c);
-          // lanes are neighbours in memory: 64 (bf16) or 128 bytes a token
-          const int64_t at = (int64_t)(tl.group + tl.n0 + c) * p.out_ld + m;
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            if (j >= cnt) continue;
-            if constexpr (kBf16)
-              static_cast<__nv_bfloat16*>(p.out)[at + j * p.out_ld] = __float2bfloat16_rn(__uint_as_float(r[j]));
-            else
-              static_cast<float*>(p.out)[at + j * p.out_ld] = __uint_as_float(r[j]);
-          }
+          if (row0 < sh.m)
+            put_tokens<kBf16, kVec>(p, &maps.out, stage, r, row0, sh.m - row0, tl.group + tl.n0 + c, tl.n - c, parts);
         }
       }
       ++acc_it;
     }
-    if (kWgrad && kVec && lane == 0) ptx::bulk_wait_all();
+    if (kVec && lane == 0) ptx::bulk_wait_all();
     if (!kWgrad) {
       // rows of no expert
       const int64_t lo = start[p.n_experts], width = sh.m;
@@ -766,24 +801,25 @@ EncodeTiledFn encode_fn() {
 }
 
 // A stack of n matrices (width x height, rows ld apart, matrices `stride`
-// apart) in boxes of 128 bytes x box_rows x 1.
+// apart) in boxes of box_cols x box_rows x 1, swizzled where a row is 128 bytes.
 bool encode(CUtensorMap* map, const void* base, int64_t width, int64_t height, int64_t ld, int64_t n, int64_t stride,
-            int box_rows, bool f32 = false) {
+            int box_rows, int box_cols = 64, bool f32 = false, bool swizzle = true) {
   const EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
+  const int64_t esz = f32 ? 4 : 2;
   const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)height, (cuuint64_t)n};
-  const cuuint64_t strides[2] = {(cuuint64_t)ld * (f32 ? 4 : 2), (cuuint64_t)stride * (f32 ? 4 : 2)};
-  const cuuint32_t box[3] = {f32 ? 32u : 64u, (cuuint32_t)box_rows, 1};
+  const cuuint64_t strides[2] = {(cuuint64_t)(ld * esz), (cuuint64_t)(stride * esz)};
+  const cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1};
   const cuuint32_t one[3] = {1, 1, 1};
-  return fn(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, one,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  return fn(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base),
+            dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-
 template <int kMode, bool kBf16, bool kAccumulate, bool kVec>
 cudaError_t launch_kernel(const ExpertArgs& a, const Maps& maps, int64_t max_tiles, cudaStream_t s) {
-  constexpr size_t kSmemBytes = smem_stages(kMode) + (kMode == kExpertWeightGrad ? kEpiWarps * kEpiStage : 0) + 1024;
+  constexpr size_t kSmemBytes = kRingBytes(kMode) + kEpiWarps * 2 * kPartBytes(kMode) + 1024;
   static std::mutex mu;
   static int resident[kMaxDevices] = {};      // CTA pairs on the device at once
   int dev = 0;
@@ -833,8 +869,9 @@ cudaError_t launch_mode(const ExpertArgs& a, const Maps& maps, int64_t max_tiles
                                             : (a.accumulate ? launch_kernel<kMode, false, true, false> : launch_kernel<kMode, false, false, false>));
     return go(a, maps, max_tiles, s);
   }
-  return a.out_bf16 ? launch_kernel<kMode, true, false, false>(a, maps, max_tiles, s)
-                    : launch_kernel<kMode, false, false, false>(a, maps, max_tiles, s);
+  const auto go = a.out_vec ? (a.out_bf16 ? launch_kernel<kMode, true, false, true> : launch_kernel<kMode, false, false, true>)
+                            : (a.out_bf16 ? launch_kernel<kMode, true, false, false> : launch_kernel<kMode, false, false, false>);
+  return go(a, maps, max_tiles, s);
 }
 
 int64_t up8(int64_t x) { return (x + 7) / 8 * 8; }
@@ -907,7 +944,7 @@ cudaError_t launch_expert(const ExpertArgs& in, cudaStream_t s) {
     const int64_t esz = a.out_bf16 ? 2 : 4;
     a.out_vec = a.cols * esz % 16 == 0 && (a.n_experts == 1 || a.out_stride * esz % 16 == 0);
     const int64_t stride = a.n_experts > 1 ? a.out_stride : a.rows * a.out_ld;
-    if (a.out_vec) ok = ok && encode(&maps.out, a.out, a.cols, a.rows, a.out_ld, a.n_experts, stride, 16, !a.out_bf16);
+    if (a.out_vec) ok = ok && encode(&maps.out, a.out, a.cols, a.rows, a.out_ld, a.n_experts, stride, 16, 128 / (int)esz, !a.out_bf16);
   } else {
     const int64_t k = a.mode == kExpertForward ? a.cols : a.rows;
     if (a.cols % 8 != 0 || (a.n_experts > 1 && a.b_stride % 8 != 0)) {
@@ -918,7 +955,13 @@ cudaError_t launch_expert(const ExpertArgs& in, cudaStream_t s) {
     prep.rows(&a.a, &a.a_ld, n, k);
     const int64_t w_stride = a.n_experts > 1 ? a.b_stride : a.rows * a.b_ld;
     ok = encode(&maps.a, a.b, a.cols, a.rows, a.b_ld, a.n_experts, w_stride, a.mode == kExpertForward ? 128 : 64) &&
-         encode(&maps.b, a.a, k, n, a.a_ld, 1, n * a.a_ld, 32) && encode(&maps.c, a.a, k, n, a.a_ld, 1, n * a.a_ld, 128);
+         encode(&maps.b, a.a, k, n, a.a_ld, 1, n * a.a_ld, 32) && encode(&maps.c, a.a, k, n, a.a_ld, 1, n * a.a_ld, 128) &&
+         encode(&maps.d, a.a, k, n, a.a_ld, 1, n * a.a_ld, 64);
+    // (a single row's leading dimension says nothing)
+    const int64_t width = a.mode == kExpertForward ? a.rows : a.cols, y_ld = n > 1 ? a.out_ld : up8(width);
+    a.out_vec = y_ld * (a.out_bf16 ? 2 : 4) % 16 == 0;
+    if (a.out_vec)
+      ok = ok && encode(&maps.out, a.out, width, n, y_ld, 1, n * y_ld, a.out_bf16 ? 16 : 8, 32, !a.out_bf16, false);
   }
   if (!ok) return cudaErrorInvalidValue;
   a.prepared = prep.a.jobs > 0;

@@ -141,7 +141,7 @@ struct ExpertArgs {
   int64_t b_stride;       // forward, input gradient: elements between experts' matrices
   int64_t out_ld, out_stride;
   int32_t out_bf16, accumulate;
-  int32_t out_vec;        // weight gradient: its rows start on 16-byte boundaries
+  int32_t out_vec;        // the output's rows start on 16-byte boundaries
   int32_t* status;        // first wait that gave up (0: none)
   uint8_t* packs;         // workspace for operands whose rows are not 16-byte aligned
   uint64_t wait_limit_ns;
