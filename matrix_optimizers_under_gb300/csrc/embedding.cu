@@ -103,8 +103,8 @@ __device__ __forceinline__ void store8(void* base, int64_t at, int tid, int thre
       __nv_bfloat162 h[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) h[k] = __floats2bfloat162_rn(x[2 * k], x[2 * k + 1]);
-      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(base) + at + kCols * tid) =
-          *reinterpret_cast<const uint4*>(h);
+      __stcs(reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(base) + at + kCols * tid),
+             *reinterpret_cast<const uint4*>(h));
     } else {
       uint32_t w[8];
 #pragma unroll
