@@ -156,7 +156,12 @@ __global__ void __launch_bounds__(kMaxThreads) lookup_kernel(const __grid_consta
 }
 
 // -------------------------------------------------------------------- gradient
-constexpr int kStage = 256;                // scalar rows: positions of a slab staged at a time
+constexpr int kMaxBatch = 32;              // a lane each
+constexpr int kMaxStages = 8;
+constexpr int kBatchBytes = 32768;         // a batch's rows, about
+constexpr int kScalarBytes = 47104;        // rows of dout and dW as fp32, of layouts off the vectors' boundaries
+constexpr int kRingBytes = 98304;          // of the CTAs an SM holds: two, or more with less each
+constexpr uint64_t kWaitNs = 2000000000ull;   // a stage is due within microseconds: longer is an error
 constexpr int kFixCols = 128;              // columns of a CTA that adds partial rows
 constexpr int kFixParts = 8;               // its warps: each adds an eighth of the slabs
 
@@ -165,20 +170,22 @@ int threads_for(int64_t dim) {
   return (int)std::min<int64_t>(kMaxThreads, (dim + 32 * kCols - 1) / (32 * kCols) * 32);
 }
 
-// CTAs an SM holds at once: their rings share 192 KB.
-int ctas_per_sm(int64_t dim) { return std::max(2, std::min(8, 512 / threads_for(dim))); }
+// CTAs an SM holds at once, by registers: their rings share 192 KB.
+int ctas_per_sm(int64_t dim) { return std::max(2, std::min(3, 512 / threads_for(dim))); }
 
 // Equal runs of the n sorted positions, one for each CTA that the GPU holds at
-// once, at least 16 each; and the CTAs, which share the vocabulary's rows too.
+// once beside the sort, at least 4 each; and the CTAs, which share the vocabulary's
+// rows too.  (CTAs that do not fit start when others end, with all their rows still to
+// look for: 40 us instead of 27 for 22315 x 192, four an SM and in the sort's place too.)
 struct SlabPlan {
   int64_t slab;        // positions of a slab
   int64_t slabs;
   int64_t ctas;
 };
 SlabPlan plan_slabs(int64_t n, int64_t vocab, int64_t dim) {
-  const int64_t want = 152 * ctas_per_sm(dim);
+  const int64_t want = (152 - kSortSms) * ctas_per_sm(dim);
   SlabPlan s;
-  s.slab = std::max<int64_t>(16, (n + want - 1) / want);
+  s.slab = std::max<int64_t>(4, (n + want - 1) / want);
   s.slabs = (n + s.slab - 1) / s.slab;
   s.ctas = std::max(s.slabs, std::min(want, (vocab + 15) / 16));
   return s;
@@ -196,8 +203,9 @@ struct GradKernelArgs {
   int32_t* n_cut;      // how many `cut` holds (zeroed by the sort)
   CutRow* cut;         // in no fixed order: each is added by itself
   int32_t* status;     // first wait that gave up (0: none)
+  int32_t threads;     // that add rows (the kernel may have more, which only look for unnamed rows)
   int32_t batch, stages, zero_bytes;   // rows of a batch, stages of the ring, bytes before it
-  uint32_t row_slot;   // bytes of a row in the ring
+  uint32_t row_slot, slot;   // bytes of a row of dout in the ring, and with the row of dW that accumulate adds to
   float* parts;        // two rows a slab: [0] of the row that began before it, [1] of the row that goes on after it
 };
 
@@ -289,8 +297,13 @@ __device__ __forceinline__ Slab slab_of(const GradKernelArgs& p, int64_t s) {
   Slab r;
   r.i0 = min(s * p.slab, a.n);
   r.i1 = min(r.i0 + p.slab, a.n);
-  r.began = r.i0 > 0 && r.i0 < a.n && a.keys[r.i0 - 1] == a.keys[r.i0];
-  r.goes_on = r.i1 > r.i0 && r.i1 < a.n && a.keys[r.i1 - 1] == a.keys[r.i1];
+  r.began = r.goes_on = false;
+  if (r.i0 >= a.n) return r;
+  // all four at once
+  const int32_t k0 = a.keys[max(r.i0 - 1, (int64_t)0)], k1 = a.keys[r.i0], k2 = a.keys[r.i1 - 1],
+                k3 = a.keys[min(r.i1, a.n - 1)];
+  r.began = r.i0 > 0 && k0 == k1;
+  r.goes_on = r.i1 < a.n && k2 == k3;
   return r;
 }
 
@@ -304,38 +317,73 @@ __device__ __forceinline__ void note_cut(const GradKernelArgs& p, const Slab& sl
   if ((threadIdx.x & 31) == 0) p.cut[atomicAdd(p.n_cut, 1)] = {v, (int32_t)first, (int32_t)s};
 }
 
-// A row's sum leaves the slab: into dW, or as a partial row.
+// A row's sum leaves the slab: into dW, with accumulate added to what it holds
+// (`old`), or as a partial row.
 template <bool kOutBf16, bool kVec>
 __device__ __forceinline__ void put_row(const GradKernelArgs& p, const Slab& sl, int64_t s, int64_t c0, int64_t v,
-                                        bool first, bool last, int tid, int threads, int cols, float (&acc)[kCols]) {
+                                        bool first, bool last, int tid, int threads, int cols, float (&acc)[kCols],
+                                        const Row8<kOutBf16, kVec>& old) {
   const EmbedGradArgs& a = p.a;
   const bool began = first && sl.began;
   if (began || (last && sl.goes_on)) {
     store8<false, kVec>(p.parts + (2 * s + (began ? 0 : 1)) * p.part_ld + c0, 0, tid, threads, cols, acc);
     return;
   }
-  const int64_t at = v * a.grad_ld + c0;
   if (a.accumulate) {
-    Row8<kOutBf16, kVec> old;
     float x[8];
-    old.load(a.grad, at, tid, threads, cols);
     old.get(x);
 #pragma unroll
     for (int k = 0; k < kCols; ++k) acc[k] += x[k];
   }
-  store8<kOutBf16, kVec>(a.grad, at, tid, threads, cols, acc);
+  store8<kOutBf16, kVec>(a.grad, v * a.grad_ld + c0, tid, threads, cols, acc);
 }
 
-// Layouts whose rows do not start on vector boundaries.
+// Layouts whose rows do not start on vector boundaries.  The CTA brings a batch
+// of rows into shared memory as fp32, an element a thread and 16 of each in
+// flight, then each thread adds up its columns.  (7709 rows of 588 fp32 columns: 30 us a
+// call; 37 with threads that load their columns of four rows at a time and add them.)
+template <bool kBf16>
+__device__ __forceinline__ float load_one(const void* base, int64_t i) {
+  return kBf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(base)[i] << 16)
+               : static_cast<const float*>(base)[i];
+}
+
+// `rows` rows of `cols` columns, the r-th from element at(r) (< 0: none).
+template <bool kBf16, typename At>
+__device__ __forceinline__ void gather_rows(float* to, const void* base, int rows, int cols, At at) {
+  constexpr int kAhead = 16;
+  const int dr = kMaxThreads / cols, dc = kMaxThreads % cols, total = rows * cols;
+  int r = threadIdx.x / cols, c = threadIdx.x % cols;
+  for (int e0 = threadIdx.x; e0 < total; e0 += kAhead * kMaxThreads) {
+    float x[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int64_t from = e0 + k * kMaxThreads < total ? at(r) : -1;
+      x[k] = from >= 0 ? load_one<kBf16>(base, from + c) : 0.f;
+      r += dr;
+      c += dc;
+      if (c >= cols) {
+        c -= cols;
+        ++r;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (e0 + k * kMaxThreads < total) to[e0 + k * kMaxThreads] = x[k];
+  }
+}
+
 template <bool kInBf16, bool kOutBf16>
-__global__ void __launch_bounds__(kMaxThreads, 2) embed_grad_kernel(const __grid_constant__ GradKernelArgs p) {
-  __shared__ int32_t keys[kStage], order[kStage];
-  constexpr int kAhead = 4;                            // positions in flight
+__global__ void __launch_bounds__(kMaxThreads, 3) embed_grad_kernel(const __grid_constant__ GradKernelArgs p) {
+  extern __shared__ __align__(128) uint8_t smem[];     // p.batch rows of dout, and of dW with accumulate
+  __shared__ int32_t keys[kMaxBatch], order[kMaxBatch], before;
   const EmbedGradArgs& a = p.a;
-  const int tid = threadIdx.x, threads = blockDim.x;
-  const int64_t c0 = (int64_t)blockIdx.y * threads * kCols;
-  const int cols = (int)min((int64_t)threads * kCols, a.dim - c0);
+  const int tid = threadIdx.x;
+  const int64_t c0 = (int64_t)blockIdx.y * kMaxThreads * kCols;
+  const int cols = (int)min((int64_t)kMaxThreads * kCols, a.dim - c0);
   const int64_t s = blockIdx.x;
+  float* const rows = reinterpret_cast<float*>(smem);
+  float* const olds = rows + p.batch * cols;
   zero_unnamed<true>(a, [&](int64_t r) {
     for (int c = tid & 31; c < cols; c += 32) {
       const int64_t at = r * a.grad_ld + c0 + c;
@@ -345,58 +393,58 @@ __global__ void __launch_bounds__(kMaxThreads, 2) embed_grad_kernel(const __grid
   });
   ptx::launch_dependents();
   const Slab sl = slab_of(p, s);
-  if (tid < 32 && blockIdx.y == 0) note_cut(p, sl, s);
-
   float acc[kCols] = {};
-  int64_t v = -1;
+  Row8<kOutBf16, false> old;                           // what row v of dW holds
+  int v = -1;
   bool first = true;                                   // row v is the slab's first
-  for (int64_t base = sl.i0; base < sl.i1; base += kStage) {
-    const int cnt = (int)min((int64_t)kStage, sl.i1 - base);
+  for (int64_t base = sl.i0; base < sl.i1; base += p.batch) {
+    const int cnt = (int)min((int64_t)p.batch, sl.i1 - base);
     __syncthreads();
-    for (int j = tid; j < cnt; j += threads) {
-      keys[j] = a.keys[base + j];
-      order[j] = a.order[base + j];
+    if (tid < cnt) {
+      keys[tid] = a.keys[base + tid];
+      order[tid] = a.order[base + tid];
     }
+    if (tid == 0) before = v;                          // (the same in every thread)
     __syncthreads();
-    for (int j0 = 0; j0 < cnt; j0 += kAhead) {
-      Row8<kInBf16, false> row[kAhead];
-#pragma unroll
-      for (int b = 0; b < kAhead; ++b)
-        if (j0 + b < cnt && keys[j0 + b] < a.vocab)
-          row[b].load(a.dout, (int64_t)order[j0 + b] * a.dout_ld + c0, tid, threads, cols);
-#pragma unroll
-      for (int b = 0; b < kAhead; ++b) {
-        if (j0 + b >= cnt) break;
-        const int key = keys[j0 + b];
-        if (key >= a.vocab) break;                     // masked: after every row
-        if (key != v) {
-          if (v >= 0) {
-            put_row<kOutBf16, false>(p, sl, s, c0, v, first, false, tid, threads, cols, acc);
-            first = false;
-          }
-          v = key;
-#pragma unroll
-          for (int k = 0; k < kCols; ++k) acc[k] = 0.f;
+    gather_rows<kInBf16>(rows, a.dout, cnt, cols,
+                         [&](int r) { return keys[r] < a.vocab ? (int64_t)order[r] * a.dout_ld + c0 : (int64_t)-1; });
+    if (a.accumulate)
+      gather_rows<kOutBf16>(olds, a.grad, cnt, cols, [&](int r) {
+        return keys[r] < a.vocab && keys[r] != (r > 0 ? keys[r - 1] : before) ? (int64_t)keys[r] * a.grad_ld + c0
+                                                                              : (int64_t)-1;
+      });
+    __syncthreads();
+    for (int b = 0; b < cnt; ++b) {
+      const int key = keys[b];
+      if (key >= a.vocab) break;                       // masked: after every row
+      if (key != v) {
+        if (v >= 0) {
+          put_row<kOutBf16, false>(p, sl, s, c0, v, first, false, tid, kMaxThreads, cols, acc, old);
+          first = false;
         }
-        float x[8];
-        row[b].get(x);
+        v = key;
 #pragma unroll
-        for (int k = 0; k < kCols; ++k) acc[k] = fmaf(a.scale, x[k], acc[k]);
+        for (int k = 0; k < kCols; ++k) {
+          acc[k] = 0.f;
+          const int c = tid + k * kMaxThreads;
+          if (a.accumulate && c < cols) old.w[k] = __float_as_uint(olds[b * cols + c]);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kCols; ++k) {
+        const int c = tid + k * kMaxThreads;
+        if (c < cols) acc[k] = fmaf(a.scale, rows[b * cols + c], acc[k]);
       }
     }
   }
   // (a masked key that goes on is no row: v is the last row before it)
-  if (v >= 0) put_row<kOutBf16, false>(p, sl, s, c0, v, first, a.keys[sl.i1 - 1] == v, tid, threads, cols, acc);
+  if (v >= 0) put_row<kOutBf16, false>(p, sl, s, c0, v, first, a.keys[sl.i1 - 1] == v, tid, kMaxThreads, cols, acc, old);
+  if (tid < 32 && blockIdx.y == 0) note_cut(p, sl, s);
 }
 
 // The same over rows on vector boundaries.  Warp 0 copies the slab's rows of
 // dout into the stages of a ring, a batch at a time (a lane each), and hands
 // on their keys; the other warps add the rows up, 8 columns a thread.
-constexpr int kMaxBatch = 32;              // a lane each
-constexpr int kMaxStages = 8;
-constexpr int kBatchBytes = 32768;         // a batch's rows, about
-constexpr int kRingBytes = 98304;          // of the CTAs an SM holds: two, or more with less each
-constexpr uint64_t kWaitNs = 2000000000ull;   // a stage is due within microseconds: longer is an error
 
 template <bool kInBf16, bool kOutBf16>
 __global__ void __launch_bounds__(32 + kMaxThreads) embed_rows_kernel(const __grid_constant__ GradKernelArgs p) {
@@ -405,7 +453,7 @@ __global__ void __launch_bounds__(32 + kMaxThreads) embed_rows_kernel(const __gr
   __shared__ int32_t keys[kMaxStages][kMaxBatch];
   __shared__ int32_t count[kMaxStages];                // positions of the batch; the last one: ~positions
   const EmbedGradArgs& a = p.a;
-  const int threads = blockDim.x - 32, lane = threadIdx.x & 31;
+  const int threads = p.threads, lane = threadIdx.x & 31;
   const int64_t c0 = (int64_t)blockIdx.y * threads * kCols;
   const int cols = (int)min((int64_t)threads * kCols, a.dim - c0);
   const uint32_t row_bytes = (uint32_t)cols * (kInBf16 ? 2 : 4), out_bytes = (uint32_t)cols * (kOutBf16 ? 2 : 4);
@@ -424,8 +472,9 @@ __global__ void __launch_bounds__(32 + kMaxThreads) embed_rows_kernel(const __gr
   __syncthreads();
   const uint64_t first_out = ptx::policy_evict_first();   // (90 us with it, 93 without)
   uint8_t* const out = static_cast<uint8_t*>(a.grad) + c0 * (kOutBf16 ? 2 : 4);
+  const int64_t out_stride = a.grad_ld * (kOutBf16 ? 2 : 4);
   const uint32_t zeros = ptx::smem_u32(smem);
-  zero_unnamed<false>(a, [&](int64_t r) { ptx::bulk_store(out + r * a.grad_ld * (kOutBf16 ? 2 : 4), zeros, out_bytes, first_out); });
+  zero_unnamed<false>(a, [&](int64_t r) { ptx::bulk_store(out + r * out_stride, zeros, out_bytes, first_out); });
   ptx::bulk_commit();
   ptx::launch_dependents();
   const Slab sl = slab_of(p, s);
@@ -436,7 +485,7 @@ __global__ void __launch_bounds__(32 + kMaxThreads) embed_rows_kernel(const __gr
     int stage = 0, use = 0;
     bool more = true;
     int64_t base = sl.i0;
-    int key = 0, from = 0;
+    int key = 0, from = 0, before = -1;                // the key before the batch
     if (lane < p.batch && base + lane < sl.i1) {
       key = a.keys[base + lane];
       from = a.order[base + lane];
@@ -455,23 +504,33 @@ __global__ void __launch_bounds__(32 + kMaxThreads) embed_rows_kernel(const __gr
         if (lane == 0) atomicCAS(p.status, 0, 1);
         break;
       }
+      // with accumulate a row's first position brings what dW holds
+      int left = __shfl_up_sync(0xffffffffu, this_key, 1);
+      if (lane == 0) left = before;
+      before = __shfl_sync(0xffffffffu, this_key, p.batch - 1);
+      const bool brings = a.accumulate && in_row && this_key != left;
+      const int olds = __popc(__ballot_sync(0xffffffffu, brings));
       if (in_row) keys[stage][lane] = this_key;
       if (lane == 0) {
         count[stage] = more ? cnt : ~cnt;
-        ptx::mbar_arrive_expect_tx(ptx::smem_u32(&full[stage]), (uint32_t)cnt * row_bytes);
+        ptx::mbar_arrive_expect_tx(ptx::smem_u32(&full[stage]), (uint32_t)cnt * row_bytes + (uint32_t)olds * out_bytes);
       }
       __syncwarp();
       if (in_row)
-        ptx::bulk_load(ptx::smem_u32(ring) + (uint32_t)(stage * p.batch + lane) * p.row_slot, in + this_from * in_stride,
+        ptx::bulk_load(ptx::smem_u32(ring) + (uint32_t)(stage * p.batch + lane) * p.slot, in + this_from * in_stride,
                        row_bytes, ptx::smem_u32(&full[stage]));
+      if (brings)
+        ptx::bulk_load(ptx::smem_u32(ring) + (uint32_t)(stage * p.batch + lane) * p.slot + p.row_slot,
+                       out + this_key * out_stride, out_bytes, ptx::smem_u32(&full[stage]));
       if (++stage == p.stages) { stage = 0; ++use; }
       base = next;
     }
     if (blockIdx.y == 0) note_cut(p, sl, s);
-  } else {
+  } else if ((int)threadIdx.x < 32 + threads) {
     const int tid = threadIdx.x - 32;
     float acc[kCols] = {};
-    int64_t v = -1;
+    Row8<kOutBf16, true> old;                          // what row v of dW holds
+    int v = -1;
     bool first = true;                                 // row v is the slab's first
     int stage = 0, use = 0;
     bool more = true, ok = true;
@@ -484,23 +543,24 @@ __global__ void __launch_bounds__(32 + kMaxThreads) embed_rows_kernel(const __gr
       const int c = count[stage];
       more = c >= 0;
       const int cnt = more ? c : ~c;
-      const uint8_t* rows = ring + (size_t)stage * p.batch * p.row_slot;
+      const uint8_t* rows = ring + (size_t)stage * p.batch * p.slot;
       constexpr int kAhead = 4;
       for (int b0 = 0; b0 < cnt; b0 += kAhead) {
         Row8<kInBf16, true> row[kAhead];
 #pragma unroll
         for (int b = 0; b < kAhead; ++b)
-          if (b0 + b < cnt) row[b].load_shared(rows + (size_t)(b0 + b) * p.row_slot, tid, cols);
+          if (b0 + b < cnt) row[b].load_shared(rows + (size_t)(b0 + b) * p.slot, tid, cols);
 #pragma unroll
         for (int b = 0; b < kAhead; ++b) {
           if (b0 + b >= cnt) break;
           const int key = keys[stage][b0 + b];
           if (key != v) {
             if (v >= 0) {
-              put_row<kOutBf16, true>(p, sl, s, c0, v, first, false, tid, threads, cols, acc);
+              put_row<kOutBf16, true>(p, sl, s, c0, v, first, false, tid, threads, cols, acc, old);
               first = false;
             }
             v = key;
+            if (a.accumulate) old.load_shared(rows + (size_t)(b0 + b) * p.slot + p.row_slot, tid, cols);
 #pragma unroll
             for (int k = 0; k < kCols; ++k) acc[k] = 0.f;
           }
@@ -516,7 +576,7 @@ __global__ void __launch_bounds__(32 + kMaxThreads) embed_rows_kernel(const __gr
     }
     // (a masked key that goes on is no row: v is the last row before it)
     if (ok && v >= 0)
-      put_row<kOutBf16, true>(p, sl, s, c0, v, first, a.keys[sl.i1 - 1] == v, tid, threads, cols, acc);
+      put_row<kOutBf16, true>(p, sl, s, c0, v, first, a.keys[sl.i1 - 1] == v, tid, threads, cols, acc, old);
   }
   ptx::bulk_wait_all();                                // the zero row is shared memory of this CTA
 }
@@ -594,6 +654,147 @@ __global__ void __launch_bounds__(32 * kFixParts) embed_fix_kernel(const __grid_
   }
 }
 
+// Few ids: one launch, no sort.  A CTA takes a share of the vocabulary's rows and
+// 256 of the columns, reads all ids, lists those of its share in order, and
+// writes its rows: zeros, or the sum of a row's positions in ascending order,
+// one row a warp.  A row with many positions is added by the eight warps, an
+// eighth of them each.  (257 ids of 768 columns: 17 us a call through the sort and two more
+// launches.)
+constexpr int kSmallIds = 512;
+constexpr int kSmallShare = 2048;          // rows of a share, at most: its bitmap
+constexpr int kSmallWarps = 8;
+constexpr int kSmallCols = 32 * kCols;
+constexpr int kSmallRow = 32;              // positions of a row that one warp adds
+
+template <bool kInBf16, bool kOutBf16, bool kVec>
+__global__ void __launch_bounds__(32 * kSmallWarps) embed_small_kernel(const __grid_constant__ EmbedGradArgs a) {
+  __shared__ int16_t pos[kSmallIds], row[kSmallIds];      // listed positions, and their rows in the share
+  __shared__ uint32_t named[kSmallShare / 32];
+  __shared__ int warp_count[kSmallWarps];
+  __shared__ float sums[kSmallWarps][kSmallCols];
+  constexpr int kAhead = 4;                               // rows in flight
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t c0 = (int64_t)blockIdx.y * kSmallCols;
+  const int cols = (int)min((int64_t)kSmallCols, a.dim - c0);
+  const int64_t share = (a.vocab + gridDim.x - 1) / gridDim.x;
+  const int64_t r0 = blockIdx.x * share;
+  const int len = (int)max((int64_t)0, min(share, a.vocab - r0));
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 2) a.header[threadIdx.x] = 0;
+  for (int i = threadIdx.x; i < (len + 31) / 32; i += blockDim.x) named[i] = 0;
+  __syncthreads();
+  int count = 0;
+  for (int base = 0; base < (int)a.n; base += 32 * kSmallWarps) {
+    const int t = base + threadIdx.x;
+    uint64_t id = ~0ull;                                  // outside every share
+    if (t < a.n)
+      id = (uint64_t)(a.ids64 ? static_cast<const int64_t*>(a.ids)[t] : static_cast<const int32_t*>(a.ids)[t]) - r0;
+    const bool in = id < (uint64_t)len;
+    const unsigned mask = __ballot_sync(0xffffffffu, in);
+    if (lane == 0) warp_count[warp] = __popc(mask);
+    __syncthreads();
+    int at = count;
+#pragma unroll
+    for (int w = 0; w < kSmallWarps; ++w) {
+      if (w < warp) at += warp_count[w];
+      count += warp_count[w];
+    }
+    if (in) {
+      at += __popc(mask & ((1u << lane) - 1));
+      pos[at] = (int16_t)t;
+      row[at] = (int16_t)id;
+      atomicOr(&named[id >> 5], 1u << (id & 31));
+    }
+    __syncthreads();
+  }
+
+  // adds the positions of row r from the first-th to the last-th
+  float acc[kCols];
+  auto add_positions = [&](int r, int first, int last) {
+#pragma unroll
+    for (int k = 0; k < kCols; ++k) acc[k] = 0.f;
+    int seen = 0;
+    for (int base = 0; base < count && seen < last; base += 32) {
+      unsigned mask = __ballot_sync(0xffffffffu, base + lane < count && row[base + lane] == r);
+      const int here = __popc(mask);
+      if (seen + here <= first) {
+        seen += here;
+        continue;
+      }
+      while (mask && seen < last) {
+        Row8<kInBf16, kVec> x[kAhead];
+        bool got[kAhead];
+#pragma unroll
+        for (int b = 0; b < kAhead; ++b) {
+          got[b] = false;
+          if (!mask) continue;
+          const int l = __ffs(mask) - 1;
+          mask &= mask - 1;
+          got[b] = seen >= first && seen < last;
+          ++seen;
+          if (got[b]) x[b].load(a.dout, (int64_t)pos[base + l] * a.dout_ld + c0, lane, 32, cols);
+        }
+#pragma unroll
+        for (int b = 0; b < kAhead; ++b) {
+          if (!got[b]) continue;
+          float v[8];
+          x[b].get(v);
+#pragma unroll
+          for (int k = 0; k < kCols; ++k) acc[k] = fmaf(a.scale, v[k], acc[k]);
+        }
+      }
+    }
+  };
+  auto put = [&](int r) {
+    const int64_t at = (r0 + r) * a.grad_ld + c0;
+    if (a.accumulate) {
+      Row8<kOutBf16, kVec> old;
+      float v[8];
+      old.load(a.grad, at, lane, 32, cols);
+      old.get(v);
+#pragma unroll
+      for (int k = 0; k < kCols; ++k) acc[k] += v[k];
+    }
+    store8<kOutBf16, kVec>(a.grad, at, lane, 32, cols, acc);
+  };
+  auto positions_of = [&](int r) {
+    int m = 0;
+    for (int base = 0; base < count; base += 32)
+      m += __popc(__ballot_sync(0xffffffffu, base + lane < count && row[base + lane] == r));
+    return m;
+  };
+
+  // rows of a few positions and of none, a warp each
+  for (int r = warp; r < len; r += kSmallWarps) {
+    if (named[r >> 5] >> (r & 31) & 1) {
+      if (count > kSmallRow && positions_of(r) > kSmallRow) continue;
+      add_positions(r, 0, kSmallIds);
+      put(r);
+    } else if (!a.accumulate) {
+#pragma unroll
+      for (int k = 0; k < kCols; ++k) acc[k] = 0.f;
+      store8<kOutBf16, kVec>(a.grad, (r0 + r) * a.grad_ld + c0, lane, 32, cols, acc);
+    }
+  }
+  if (count <= kSmallRow) return;
+  // rows of many positions, one at a time
+  for (int w = 0; w < (len + 31) / 32; ++w)
+    for (uint32_t bits = named[w]; bits; bits &= bits - 1) {
+      const int r = 32 * w + __ffs(bits) - 1, m = positions_of(r);
+      if (m <= kSmallRow) continue;
+      add_positions(r, m * warp / kSmallWarps, m * (warp + 1) / kSmallWarps);
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < kCols; ++k) sums[warp][32 * k + lane] = acc[k];
+      __syncthreads();
+      if (warp != 0) continue;
+#pragma unroll
+      for (int q = 1; q < kSmallWarps; ++q)
+#pragma unroll
+        for (int k = 0; k < kCols; ++k) acc[k] += sums[q][32 * k + lane];
+      put(r);
+    }
+}
+
 // Rows of a tensor start on the vector's boundary: 16 bytes of bf16, 32 of fp32.
 bool vec_rows(const void* p, int64_t ld, int64_t dim, int32_t bf16) {
   return ld % kCols == 0 && dim % kCols == 0 && aligned(p, bf16 ? 16 : 32);
@@ -603,22 +804,42 @@ template <bool kA, bool kB, bool kVec>
 void lookup_launch(const LookupArgs& a, dim3 grid, dim3 block, cudaStream_t s) {
   lookup_kernel<kA, kB, kVec><<<grid, block, 0, s>>>(a);
 }
+// Shares of the vocabulary for few ids: four CTAs an SM, more where a share would
+// not fit its bitmap.
+int64_t small_shares(int64_t vocab, int64_t dim) {
+  const int64_t blocks = (dim + kSmallCols - 1) / kSmallCols;
+  return std::max((vocab + kSmallShare - 1) / kSmallShare, std::min((vocab + 7) / 8, std::max<int64_t>(1, 608 / blocks)));
+}
+
+template <bool kIn, bool kOut>
+cudaError_t small_launch(const EmbedGradArgs& a, bool vec, cudaStream_t s) {
+  const dim3 grid((unsigned)small_shares(a.vocab, a.dim), (unsigned)((a.dim + kSmallCols - 1) / kSmallCols));
+  if (vec) embed_small_kernel<kIn, kOut, true><<<grid, 32 * kSmallWarps, 0, s>>>(a);
+  else embed_small_kernel<kIn, kOut, false><<<grid, 32 * kSmallWarps, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
 template <bool kIn, bool kOut>
 cudaError_t grad_launch(GradKernelArgs& p, int64_t ctas, bool vec, cudaStream_t s) {
   const EmbedGradArgs& a = p.a;
   const int threads = threads_for(a.dim);
   const dim3 grid((unsigned)ctas, (unsigned)((a.dim + threads * kCols - 1) / (threads * kCols)));
-  // The kernel writes before its wait, so what it may overlap has to be the sort:
-  // without ids there is none.
-  const bool after_sort = a.n > 0;
-  if (!vec) return launch_overlapped(embed_grad_kernel<kIn, kOut>, grid, dim3((unsigned)threads), 0, s, after_sort, p);
+  // The kernel writes dW before its wait, beside the sort, which is the kernel before it.
+  if (!vec) {
+    const size_t row = std::min<int64_t>(a.dim, (int64_t)kMaxThreads * kCols) * sizeof(float) * (a.accumulate ? 2 : 1);
+    p.batch = (int32_t)std::min<size_t>(kMaxBatch, kScalarBytes / row);
+    const dim3 blocks((unsigned)ctas, (unsigned)((a.dim + kMaxThreads * kCols - 1) / (kMaxThreads * kCols)));
+    return launch_overlapped(embed_grad_kernel<kIn, kOut>, blocks, dim3(kMaxThreads), p.batch * row, s, true, p);
+  }
+  p.threads = threads;
   const int cols = (int)std::min<int64_t>(a.dim, (int64_t)threads * kCols);
   p.row_slot = (uint32_t)round_up((size_t)cols * (kIn ? 2 : 4), 128);
   p.zero_bytes = (int32_t)round_up((size_t)cols * (kOut ? 2 : 4), 128);
+  p.slot = p.row_slot + (a.accumulate ? (uint32_t)p.zero_bytes : 0);
   const int ring = 2 * kRingBytes / ctas_per_sm(a.dim);
-  p.batch = (int32_t)std::max<int64_t>(4, std::min<int64_t>({kMaxBatch, kBatchBytes / p.row_slot, ring / (2 * p.row_slot)}));
-  p.stages = (int32_t)std::max<int64_t>(2, std::min<int64_t>(kMaxStages, ring / (p.batch * p.row_slot)));
-  const size_t smem = p.zero_bytes + (size_t)p.stages * p.batch * p.row_slot;
+  p.batch = (int32_t)std::max<int64_t>(2, std::min<int64_t>({kMaxBatch, kBatchBytes / p.slot, ring / (2 * p.slot)}));
+  p.stages = (int32_t)std::max<int64_t>(2, std::min<int64_t>(kMaxStages, ring / (p.batch * p.slot)));
+  const size_t smem = p.zero_bytes + (size_t)p.stages * p.batch * p.slot;
   static std::atomic<bool> ready[kMaxDevices];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -629,7 +850,8 @@ cudaError_t grad_launch(GradKernelArgs& p, int64_t ctas, bool vec, cudaStream_t 
     if (e != cudaSuccess) return e;
     ready[dev].store(true);
   }
-  return launch_overlapped(embed_rows_kernel<kIn, kOut>, grid, dim3((unsigned)(32 + threads)), smem, s, after_sort, p);
+  return launch_overlapped(embed_rows_kernel<kIn, kOut>, grid, dim3((unsigned)std::max(256, 32 + threads)), smem, s,
+                           true, p);
 }
 
 }  // namespace
@@ -653,7 +875,13 @@ size_t embed_grad_partial_bytes(int64_t n, int64_t vocab, int64_t dim) {
   return round_up(sp.slabs * sizeof(CutRow), 256) + (size_t)sp.slabs * 2 * round_up((size_t)dim, 8) * sizeof(float);
 }
 
+bool embed_grad_sorts(int64_t n) { return n > kSmallIds; }
+
 cudaError_t launch_embed_grad(const EmbedGradArgs& a, cudaStream_t s) {
+  const bool vec = vec_rows(a.dout, a.dout_ld, a.dim, a.dout_bf16) && vec_rows(a.grad, a.grad_ld, a.dim, a.grad_bf16);
+  if (!embed_grad_sorts(a.n))
+    return a.dout_bf16 ? (a.grad_bf16 ? small_launch<true, true>(a, vec, s) : small_launch<true, false>(a, vec, s))
+                       : (a.grad_bf16 ? small_launch<false, true>(a, vec, s) : small_launch<false, false>(a, vec, s));
   const SlabPlan sp = plan_slabs(a.n, a.vocab, a.dim);
   GradKernelArgs p;
   p.a = a;
@@ -664,10 +892,9 @@ cudaError_t launch_embed_grad(const EmbedGradArgs& a, cudaStream_t s) {
   p.n_cut = a.header + 1;
   p.cut = reinterpret_cast<CutRow*>(at);
   p.parts = reinterpret_cast<float*>(at + round_up(sp.slabs * sizeof(CutRow), 256));
-  const bool vec = vec_rows(a.dout, a.dout_ld, a.dim, a.dout_bf16) && vec_rows(a.grad, a.grad_ld, a.dim, a.grad_bf16);
   const cudaError_t e = a.dout_bf16 ? (a.grad_bf16 ? grad_launch<true, true>(p, sp.ctas, vec, s) : grad_launch<true, false>(p, sp.ctas, vec, s))
                                     : (a.grad_bf16 ? grad_launch<false, true>(p, sp.ctas, vec, s) : grad_launch<false, false>(p, sp.ctas, vec, s));
-  if (e != cudaSuccess || a.n == 0) return e;
+  if (e != cudaSuccess) return e;
   const int64_t items = sp.slabs * ((a.dim + kFixCols - 1) / kFixCols);      // at most
   const dim3 fix((unsigned)std::min<int64_t>(items, 4 * std::max(1, sm_count())));
   return launch_overlapped(a.grad_bf16 ? embed_fix_kernel<true> : embed_fix_kernel<false>, fix, dim3(32 * kFixParts),

@@ -94,6 +94,7 @@ struct SortArgs {
   int32_t* zero;         // two words the sort sets to 0 (may be null)
 };
 size_t sort_scratch_bytes(int64_t n, int64_t n_keys);
+constexpr int kSortSms = 8;            // SMs that a sort of few ids takes
 cudaError_t launch_sort(const SortArgs& a, cudaStream_t s);
 cudaError_t launch_key_starts(const int32_t* keys, int64_t n, int64_t n_keys, int32_t* starts, cudaStream_t s);
 
@@ -121,6 +122,8 @@ struct EmbedGradArgs {
   float scale;
 };
 size_t embed_grad_partial_bytes(int64_t n, int64_t vocab, int64_t dim);
+// Whether the gradient of n ids takes them sorted (few it takes as they are).
+bool embed_grad_sorts(int64_t n);
 cudaError_t launch_embed_grad(const EmbedGradArgs& a, cudaStream_t s);
 
 // --------------------------------------------- products grouped by expert

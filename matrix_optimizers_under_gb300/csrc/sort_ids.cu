@@ -47,7 +47,7 @@ constexpr int kClusterThreads = 1024;
 constexpr int kClusterWarps = kClusterThreads / 32;
 constexpr int kClusterSteps = 8;                                // pairs of a thread
 constexpr int kClusterTile = kClusterThreads * kClusterSteps;   // pairs of a CTA
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = kSortSms;
 constexpr int kQuarters = kClusterThreads / kDigits;             // threads that add up one digit's warps
 constexpr size_t kClusterSmem = (size_t)kClusterTile * 16 + (size_t)kClusterWarps * kDigits * 4;
 
