@@ -36,6 +36,7 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 
+#include <climits>
 #include <mutex>
 
 #include "ops_internal.h"
@@ -64,6 +65,7 @@ constexpr int kPartBytes(int mode) { return mode == kExpertWeightGrad ? 2048 : 1
 constexpr int kEpiWarps = 8;
 constexpr int kFirstEpiWarp = 4;
 constexpr int kThreads = 32 * (kFirstEpiWarp + kEpiWarps);
+constexpr int kSplitPairs = 76;                       // pairs that a split contraction is cut for
 constexpr int kAccCols = 256;
 constexpr int kTmemCols = 512;
 constexpr uint64_t kDrainNs = 2000000000ull;          // limit of the waits that end a CTA
@@ -74,6 +76,15 @@ struct Maps {
   CUtensorMap c;      // box 64 x 128 (K-major B); weight gradient: the padded ends of A, box 64 x 16
   CUtensorMap d;      // box 64 x 64 (K-major B); weight gradient: the padded ends of B, box 64 x 16
   CUtensorMap out;    // dW, box 128 bytes x 16; or Y, box 32 elements x 1 KB
+};
+
+// What adds up a split weight gradient.
+struct ChunkSumArgs {
+  const float* parts;
+  void* out;
+  const int32_t* starts;
+  int64_t n_rows, rows, cols, part_ld, out_ld, out_stride;
+  int32_t experts, chunk, slots, accumulate;
 };
 
 // First failing wait of a launch: (role << 0); the wait's limit.
@@ -106,6 +117,7 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const Ab
 // side (n_mma of them in the MMA), k_len of contraction.
 struct Tile {
   int32_t e;
+  int32_t z;          // matrix of the output stack
   int32_t group;      // first token of the group
   int32_t m0, n0;
   int32_t n, n_mma;
@@ -117,6 +129,7 @@ struct Shape {
   int32_t tiles_m;
   int32_t n;          // weight gradient: N side (cols)
   int32_t tiles_n, width_n;
+  int32_t chunk;      // weight gradient: tokens of a chunk of a split contraction
 };
 
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
@@ -134,6 +147,42 @@ __device__ __forceinline__ int even_width(int n, int parts, int step = kStepN) {
 // Rows of shared memory that one CTA's nh columns of a K-major B take: the copies' boxes.
 __device__ __forceinline__ uint32_t rows_b(int nh) { return nh > 96 ? 128 : ceil_div(nh, 32) * 32; }
 
+// Chunks of a split contraction of length k (none: one, of zeros).
+__host__ __device__ __forceinline__ int chunks_of(int k, int chunk) { return k <= chunk ? 1 : (k + chunk - 1) / chunk; }
+
+// The chunk of a launch, and the chunks of the experts before `e` and of e: by a
+// whole warp, with an expert or two a lane.  Groups whose starts fall overlap, and may make
+// more chunks than there is workspace for; then every group is one.
+struct Chunks {
+  int chunk, before, mine;
+};
+__device__ __forceinline__ Chunks find_chunks(const int32_t* starts, int experts, int n_rows, int chunk, int slots,
+                                              int e) {
+  static_assert(kSplitPairs / 2 <= 64, "two experts a lane");
+  const int lane = threadIdx.x & 31;
+  int len[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int i = min(lane + 32 * k, experts - 1);
+    const int to = starts[i + 1], from = starts[i];
+    len[k] = min(max(to, 0), n_rows) - (i == 0 ? 0 : min(max(from, 0), n_rows));
+  }
+  Chunks r{chunk, 0, 0};
+  auto count = [&](auto want) {
+    int sum = 0;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int i = lane + 32 * k;
+      if (i < experts && want(i)) sum += chunks_of(len[k], r.chunk);
+    }
+    return (int)__reduce_add_sync(0xffffffffu, (unsigned)sum);
+  };
+  if (count([](int) { return true; }) > slots) r.chunk = INT_MAX;
+  r.before = count([&](int i) { return i < e; });
+  r.mine = count([&](int i) { return i == e; });
+  return r;
+}
+
 // First token of expert e's group, kept inside the rows there are.
 __device__ __forceinline__ int start_of(const ExpertArgs& p, int e) {
   return e == 0 ? 0 : min(max(p.starts[e], 0), (int)p.n_rows);
@@ -143,22 +192,41 @@ template <int kMode>
 __device__ __forceinline__ Tile decode(const ExpertArgs& p, const Shape& sh, const int32_t* start,
                                        const int32_t* first, int t) {
   Tile r;
-  if (kMode == kExpertWeightGrad) {
-    const int per = sh.tiles_m * sh.tiles_n;
-    r.e = t / per;
-    const int i = t - r.e * per, j = i / sh.tiles_m;
-    r.m0 = (i - j * sh.tiles_m) * kPairM;
-    r.n0 = j * sh.width_n;
-    r.n = min(sh.width_n, sh.n - r.n0);
-    r.group = start_of(p, r.e);
-    r.k_len = max(0, start_of(p, r.e + 1) - r.group);
-  } else {
+  // the expert whose tiles begin last at or before t
+  auto expert_of = [&]() {
     int lo = 0, hi = p.n_experts - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
       if (first[mid] <= t) lo = mid; else hi = mid - 1;
     }
-    r.e = lo;
+    return lo;
+  };
+  if (kMode == kExpertWeightGrad) {
+    const int per = sh.tiles_m * sh.tiles_n;
+    int i, chunk = 0;
+    if (p.chunk > 0) {
+      r.e = expert_of();
+      i = t - first[r.e];
+      chunk = i / per;
+      i -= chunk * per;
+      r.z = first[r.e] / per + chunk;
+    } else {
+      r.e = r.z = t / per;
+      i = t - r.e * per;
+    }
+    const int j = i / sh.tiles_m;
+    r.m0 = (i - j * sh.tiles_m) * kPairM;
+    r.n0 = j * sh.width_n;
+    r.n = min(sh.width_n, sh.n - r.n0);
+    r.group = start_of(p, r.e);
+    r.k_len = max(0, start_of(p, r.e + 1) - r.group);
+    if (p.chunk > 0) {
+      r.group += chunk * sh.chunk;
+      r.k_len = min(r.k_len - chunk * sh.chunk, sh.chunk);
+    }
+  } else {
+    const int lo = expert_of();
+    r.e = r.z = lo;
     const int len = start[lo + 1] - start[lo];
     const int width = even_width(len, ceil_div(len, kMaxN));
     const int i = t - first[lo], j = i / sh.tiles_m;
@@ -216,6 +284,7 @@ struct TileWalk {
     const int lane = 32 - held;
     if (!kShape) {
       r.e = __shfl_sync(0xffffffffu, mine.e, lane);
+      r.z = __shfl_sync(0xffffffffu, mine.z, lane);
       r.group = __shfl_sync(0xffffffffu, mine.group, lane);
       r.m0 = __shfl_sync(0xffffffffu, mine.m0, lane);
       r.n0 = __shfl_sync(0xffffffffu, mine.n0, lane);
@@ -409,8 +478,9 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
   constexpr bool kWgrad = kMode == kExpertWeightGrad;
   constexpr bool kAmn = kMode != kExpertForward;
   extern __shared__ uint8_t smem_raw[];
-  // forward products: first token (clamped) and first tile of each expert
-  __shared__ int32_t start[kWgrad ? 1 : MFSDP_MAX_EXPERTS + 1], first[kWgrad ? 1 : MFSDP_MAX_EXPERTS + 1];
+  // first token (clamped) and first tile of each expert (weight gradient: of a split one)
+  constexpr int kListed = kWgrad ? kSplitPairs / 2 : MFSDP_MAX_EXPERTS;
+  __shared__ int32_t start[kListed + 1], first[kListed + 1];
   __shared__ int32_t widest;                            // columns of the launch's widest tile
   __shared__ __align__(8) uint64_t full_bar[kMaxStages];    // even CTA: both CTAs' operands have landed
   __shared__ __align__(8) uint64_t empty_bar[kMaxStages];
@@ -430,7 +500,9 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
   sh.tiles_n = ceil_div(sh.n, kMaxN);
   sh.width_n = even_width(sh.n, sh.tiles_n, 64);       // whole chunks of the epilogue, which writes them whole
 
-  if (!kWgrad)
+  const bool listed = !kWgrad || p.chunk > 0;
+  sh.chunk = kWgrad && listed ? find_chunks(p.starts, p.n_experts, n_rows, p.chunk, p.slots, 0).chunk : 0;
+  if (listed)
     for (int i = threadIdx.x; i <= p.n_experts; i += kThreads) start[i] = start_of(p, i);
   if (warp == 1) {
     ptx::tmem_alloc_pair(ptx::smem_u32(&tmem_slot), kTmemCols);
@@ -454,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
     ptx::fence_proxy_async_smem();
   }
   __syncthreads();
-  if (warp == 0 && !kWgrad) {
+  if (warp == 0 && listed) {
     // tiles before each expert, and the widest tile
     int base = 0, wide = kStepN;
     for (int e0 = 0; e0 < p.n_experts; e0 += 32) {
@@ -462,7 +534,8 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
       const int len = e < p.n_experts ? max(0, start[e + 1] - start[e]) : 0;
       const int nt = ceil_div(len, kMaxN);
       if (nt) wide = max(wide, even_width(len, nt));
-      int sum = nt * sh.tiles_m;
+      int sum = kWgrad ? chunks_of(len, sh.chunk) * sh.tiles_m * sh.tiles_n : nt * sh.tiles_m;
+      if (e >= p.n_experts) sum = 0;
       const int own = sum;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -487,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
   // packed operands and padded ends come from the kernels before this one
   ptx::wait_dependencies();
   ptx::fence_proxy_async_global();
-  const int n_tiles = kWgrad ? p.n_experts * sh.tiles_m * sh.tiles_n : first[p.n_experts];
+  const int n_tiles = listed ? first[p.n_experts] : p.n_experts * sh.tiles_m * sh.tiles_n;
   TileWalk<kMode> walk(p, sh, start, first, blockIdx.x >> 1, gridDim.x >> 1, n_tiles);
   Tile tl;
   // Shared memory of a stage: A, then this CTA's half of B.
@@ -642,7 +715,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
     uint32_t acc_it = 0, parts = 0;
     while (walk.next(tl)) {
       const int row0 = tl.m0 + (int)rank * kCtaM + quad * 32;
-      const int64_t at0 = kWgrad ? tl.e * p.out_stride + row0 * p.out_ld + tl.n0 : 0;      // the warp's first row
+      const int64_t at0 = kWgrad ? tl.z * p.out_stride + row0 * p.out_ld + tl.n0 : 0;      // the warp's first row
       if (kWgrad && tl.k_len == 0) {
         if (kAccumulate) continue;
         uint32_t z[32];
@@ -650,7 +723,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
         for (int j = 0; j < 32; ++j) z[j] = 0;
         for (int c = kWidth * half; c < tl.n; c += 2 * kWidth) {
           if (kVec)
-            put_rows(stage, z, &maps.out, tl.n0 + c, row0, tl.e, sh.m - row0, parts);
+            put_rows(stage, z, &maps.out, tl.n0 + c, row0, tl.z, sh.m - row0, parts);
           else
             put_plain<kBf16, false>(p, stage, z, at0 + c, sh.m - row0, tl.n - c);
         }
@@ -672,7 +745,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
         const bool last = c + 2 * kWidth >= tl.n_mma;
         __syncwarp();
         if constexpr (kWgrad && kVec) {
-          put_chunk<kBf16, kAccumulate>(p, &maps.out, stage, t_row + c, tl.n0 + c, row0, tl.e, sh.m - row0, tl.n - c, parts,
+          put_chunk<kBf16, kAccumulate>(p, &maps.out, stage, t_row + c, tl.n0 + c, row0, tl.z, sh.m - row0, tl.n - c, parts,
                                         last, release);
           continue;
         }
@@ -711,6 +784,70 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
   if (warp == 1) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc_pair(tmem_base, kTmemCols);
+  }
+}
+
+// Adds up a split weight gradient: dW_e (+)= the sum of its chunks, in their order.  An
+// item is 128 elements of a matrix, four a lane.  A warp adds the chunks of an item; where
+// there are many, the warps of a CTA take an eighth of them each.
+constexpr int kSumWarps = 8;
+constexpr int kFewChunks = 16;
+
+template <bool kBf16>
+__device__ __forceinline__ void put_sum(const ChunkSumArgs& a, int e, int64_t q, const float4& acc) {
+  const int64_t quads = a.part_ld / 4, r = q / quads, c = (q - r * quads) * 4;
+  const int64_t at = e * a.out_stride + r * a.out_ld + c;
+  const float v[4] = {acc.x, acc.y, acc.z, acc.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (c + k >= a.cols) break;
+    if constexpr (kBf16) {
+      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + at + k;
+      *o = __float2bfloat16_rn(a.accumulate ? v[k] + __bfloat162float(*o) : v[k]);
+    } else {
+      float* o = static_cast<float*>(a.out) + at + k;
+      *o = a.accumulate ? v[k] + *o : v[k];
+    }
+  }
+}
+
+template <bool kBf16>
+__global__ void __launch_bounds__(32 * kSumWarps) sum_chunks_kernel(const __grid_constant__ ChunkSumArgs a) {
+  __shared__ float4 sums[kSumWarps][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e = blockIdx.y;
+  const Chunks my = find_chunks(a.starts, a.experts, (int)a.n_rows, a.chunk, a.slots, e);
+  const int64_t size = a.rows * a.part_ld, quads = size / 4;
+  const float* part = a.parts + my.before * size;
+  auto add = [&](int64_t q, int lo, int hi) {
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int c = lo; c < hi; ++c) {
+      const float4 x = *reinterpret_cast<const float4*>(part + c * size + 4 * q);
+      acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
+    }
+    return acc;
+  };
+  ptx::wait_dependencies();
+  if (my.mine <= kFewChunks) {
+    for (int64_t q = ((int64_t)blockIdx.x * kSumWarps + warp) * 32 + lane; q < quads;
+         q += (int64_t)gridDim.x * kSumWarps * 32)
+      put_sum<kBf16>(a, e, q, add(q, 0, my.mine));
+    return;
+  }
+  for (int64_t q0 = (int64_t)blockIdx.x * 32; q0 < quads; q0 += (int64_t)gridDim.x * 32) {
+    const int64_t q = q0 + lane;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (q < quads) acc = add(q, my.mine * warp / kSumWarps, my.mine * (warp + 1) / kSumWarps);
+    __syncthreads();
+    sums[warp][lane] = acc;
+    __syncthreads();
+    if (warp != 0 || q >= quads) continue;
+#pragma unroll
+    for (int w = 1; w < kSumWarps; ++w) {
+      const float4 x = sums[w][lane];
+      acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
+    }
+    put_sum<kBf16>(a, e, q, acc);
   }
 }
 
@@ -874,6 +1011,7 @@ cudaError_t launch_mode(const ExpertArgs& a, const Maps& maps, int64_t max_tiles
   return go(a, maps, max_tiles, s);
 }
 
+int64_t up4(int64_t x) { return (x + 3) / 4 * 4; }
 int64_t up8(int64_t x) { return (x + 7) / 8 * 8; }
 
 // The jobs of one call and the workspace they fill.
@@ -918,14 +1056,36 @@ struct Prepare {
   }
 };
 
+// A weight gradient whose tiles leave half of the GPU idle has its contraction cut: chunks
+// of this many tokens (0: not cut), whose matrices go to the workspace in fp32 and are
+// added by a second kernel.  As many as the pairs take in one turn, 512 tokens at least.
+// With and without, us: 1 expert, 4096 tokens, 512 x 512: 14.3 and 24.0; 4 experts, 4096,
+// 256 x 1024: 17.3 and 16.8; 8 experts, 8192, 128 x 512: 15.8 and 17.7; 4 experts (two of them
+// with tokens), 11922, 112 x 1664: 23 and 41.
+int64_t split_chunk(int64_t experts, int64_t n, int64_t rows, int64_t cols) {
+  const int64_t tiles = ((rows + kPairM - 1) / kPairM) * ((cols + kMaxN - 1) / kMaxN);
+  const int64_t most = kSplitPairs / tiles;          // chunks in all
+  if (2 * experts > most || n < 4096 || n < 1024 * experts) return 0;
+  const int64_t parts = most - experts + 1;          // every expert's last chunk is short
+  return std::max<int64_t>(512, ((n + parts - 1) / parts + kBlockK - 1) / kBlockK * kBlockK);
+}
+// Chunks that there can be.
+int64_t split_slots(int64_t experts, int64_t n, int64_t chunk) { return n / chunk + experts; }
+
 }  // namespace
+
+size_t expert_split_bytes(int64_t experts, int64_t n, int64_t rows, int64_t cols) {
+  const int64_t chunk = split_chunk(experts, n, rows, cols);
+  return chunk == 0 ? 0 : round_up((size_t)split_slots(experts, n, chunk) * rows * up4(cols) * sizeof(float), 256);
+}
 
 cudaError_t launch_expert(const ExpertArgs& in, cudaStream_t s) {
   ExpertArgs a = in;
   const int64_t n = a.n_rows, mt = ((a.mode == kExpertInputGrad ? a.cols : a.rows) + kPairM - 1) / kPairM;
   Prepare prep(a);
   Maps maps{};
-  bool ok = true;
+  ChunkSumArgs sum{};
+  bool ok = true, sum_bf16 = false;
   // The longest wait is the epilogue's for a tile's whole contraction: 2 s, and
   // 64 ns for each of its K (8 clocks at the MMA's rate, at 1 GHz, 8 times over).
   const int64_t k_max = a.mode == kExpertWeightGrad ? n : (a.mode == kExpertForward ? a.cols : a.rows);
@@ -944,7 +1104,21 @@ cudaError_t launch_expert(const ExpertArgs& in, cudaStream_t s) {
     const int64_t esz = a.out_bf16 ? 2 : 4;
     a.out_vec = a.cols * esz % 16 == 0 && (a.n_experts == 1 || a.out_stride * esz % 16 == 0);
     const int64_t stride = a.n_experts > 1 ? a.out_stride : a.rows * a.out_ld;
-    if (a.out_vec) ok = ok && encode(&maps.out, a.out, a.cols, a.rows, a.out_ld, a.n_experts, stride, 16, 128 / (int)esz, !a.out_bf16);
+    a.chunk = (int32_t)split_chunk(a.n_experts, n, a.rows, a.cols);
+    a.slots = a.chunk > 0 ? (int32_t)split_slots(a.n_experts, n, a.chunk) : 0;
+    int64_t out_stride = stride;
+    if (a.chunk > 0) {                             // the chunks' matrices, in fp32, in place of dW
+      sum = {reinterpret_cast<const float*>(prep.at), a.out, a.starts, n, a.rows, a.cols, up4(a.cols), a.out_ld,
+             a.out_stride, a.n_experts, a.chunk, a.slots, a.accumulate};
+      sum_bf16 = a.out_bf16;
+      a.out = prep.at;
+      a.out_ld = up4(a.cols);
+      a.out_stride = out_stride = a.rows * a.out_ld;
+      a.out_bf16 = a.accumulate = 0;
+      a.out_vec = 1;
+    }
+    if (a.out_vec)
+      ok = ok && encode(&maps.out, a.out, a.cols, a.rows, a.out_ld, a.chunk > 0 ? a.slots : a.n_experts, out_stride, 16, a.out_bf16 ? 64 : 32, !a.out_bf16);
   } else {
     const int64_t k = a.mode == kExpertForward ? a.cols : a.rows;
     if (a.cols % 8 != 0 || (a.n_experts > 1 && a.b_stride % 8 != 0)) {
@@ -967,8 +1141,15 @@ cudaError_t launch_expert(const ExpertArgs& in, cudaStream_t s) {
   a.prepared = prep.a.jobs > 0;
   const cudaError_t e = prep.launch(s);
   if (e != cudaSuccess) return e;
-  if (a.mode == kExpertWeightGrad)
-    return launch_mode<kExpertWeightGrad>(a, maps, a.n_experts * mt * ((a.cols + kMaxN - 1) / kMaxN), s);
+  if (a.mode == kExpertWeightGrad) {
+    const int64_t stack = a.chunk > 0 ? a.slots : a.n_experts;
+    const cudaError_t err = launch_mode<kExpertWeightGrad>(a, maps, stack * mt * ((a.cols + kMaxN - 1) / kMaxN), s);
+    if (err != cudaSuccess || a.chunk == 0) return err;
+    const int64_t items = (a.rows * (a.out_ld / 4) + 31) / 32;
+    const dim3 grid((unsigned)std::min<int64_t>(items, (1216 + a.n_experts - 1) / a.n_experts), (unsigned)a.n_experts);
+    return launch_overlapped(sum_bf16 ? sum_chunks_kernel<true> : sum_chunks_kernel<false>, grid, dim3(32 * kSumWarps),
+                             0, s, true, sum);
+  }
   const int64_t tiles = mt * (n / kMaxN + std::min<int64_t>(a.n_experts, n));
   return a.mode == kExpertForward ? launch_mode<kExpertForward>(a, maps, tiles, s)
                                   : launch_mode<kExpertInputGrad>(a, maps, tiles, s);

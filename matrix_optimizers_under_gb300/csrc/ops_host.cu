@@ -436,6 +436,7 @@ extern "C" size_t mfsdp_expert_workspace_bytes(int32_t n_experts, int64_t n_rows
   if (n_rows > 1 && cols_ld % 8 != 0) bytes += packed_bytes(n_rows, cols);
   // weight gradient: the last rows of each group, padded to 16, of both operands
   if (n_rows > 0) bytes += packed_bytes(16 * (int64_t)n_experts, rows) + packed_bytes(16 * (int64_t)n_experts, cols);
+  bytes += expert_split_bytes(n_experts, n_rows, rows, cols);
   return bytes;
 }
 

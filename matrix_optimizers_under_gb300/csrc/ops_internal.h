@@ -149,11 +149,15 @@ struct ExpertArgs {
   uint8_t* packs;         // workspace for operands whose rows are not 16-byte aligned
   uint64_t wait_limit_ns;
   int32_t prepared;       // kernels of this call that prepare operands run right before
+  int32_t chunk;          // weight gradient: tokens of a chunk of a split contraction (0: whole groups)
+  int32_t slots;          // and chunks that there can be in all
 };
 // Bytes of a copy of n rows of `width` bf16 elements, each padded to 16 bytes.
 inline size_t packed_bytes(int64_t n, int64_t width) {
   return round_up((size_t)n * (size_t)((width + 7) / 8 * 8) * 2, 256);
 }
+// Workspace of a weight gradient whose contraction is split (0: it is not).
+size_t expert_split_bytes(int64_t n_experts, int64_t n_rows, int64_t rows, int64_t cols);
 cudaError_t launch_expert(const ExpertArgs& a, cudaStream_t s);
 
 }  // namespace ops

@@ -340,6 +340,34 @@ def test_expert_weight_grad(mfsdp, out, accumulate, counts, rows, cols, extra, t
     assert np.all(host(flat)[:, rows * cols:] == 7.0)
 
 
+@pytest.mark.parametrize("out,accumulate", [("bf16", False), ("f32", False), ("f32", True), ("bf16", True)])
+@pytest.mark.parametrize("counts,rows,cols", [([4096], 64, 72), ([11_003], 300, 260), ([4096, 0, 1, 700], 130, 264),
+                                              ([0, 9000], 1000, 500), ([2048, 2049, 2047, 2040], 33, 21)])
+@pytest.mark.parametrize("extra,tail", [(0, 0), (3, 5)])
+def test_expert_weight_grad_long_groups(mfsdp, out, accumulate, counts, rows, cols, extra, tail):
+    """Few tiles and many tokens: the contraction is cut, and its parts added."""
+    test_expert_weight_grad(mfsdp, out, accumulate, counts, rows, cols, extra, tail)
+
+
+def test_expert_weight_grad_starts_that_fall(mfsdp):
+    """Starts outside the rows are clamped, and a group that ends before it starts
+    is empty: the experts beside it still get theirs, and nothing else is written."""
+    n, rows, cols = 6000, 64, 40
+    rng = np.random.default_rng(8)
+    dy, x = dev(rng.standard_normal((n, rows)), "bf16"), dev(rng.standard_normal((n, cols)), "bf16")
+    starts = torch.tensor([0, 5000, 200, 90_000, -4], dtype=torch.int32, device="cuda")
+    flat = torch.full((4 * rows * cols + 64,), 7.0, device="cuda")
+    dw = flat[:4 * rows * cols].view(4, rows, cols)
+    ws = scratch(mfsdp.expert_workspace_bytes(4, rows, cols, n))
+    mfsdp.expert_weight_grad(dy, x, starts, dw, ws)
+    assert mfsdp.op_device_status(ws)[0] == 0
+    hx, hdy, got = host(x), host(dy), host(dw)
+    for e, (lo, hi) in enumerate([(0, 5000), (0, 0), (200, 6000), (0, 0)]):
+        want, mag = hdy[lo:hi].T @ hx[lo:hi], np.abs(hdy[lo:hi]).T @ np.abs(hx[lo:hi])
+        close(got[e], want, (max(hi - lo, 32) + 1) * U * mag + U * np.abs(want), f"expert {e}")
+    assert torch.all(flat[4 * rows * cols:] == 7.0)
+
+
 def test_expert_neighbours_do_not_leak(mfsdp):
     """NaN and Inf in one expert's rows or matrix stay inside that expert."""
     counts, rows, cols = [19, 45, 8, 37], 96, 72
