@@ -242,6 +242,17 @@ def test_embedding_grad(mfsdp, dout, grad, n, vocab, dim, kind, extra, accumulat
     assert np.all(host(buf)[:, dim:] == 7.0)
 
 
+@pytest.mark.parametrize("dout,grad", [("bf16", "f32"), ("f32", "bf16")])
+@pytest.mark.parametrize("n,vocab,dim,kind", [(512, 3, 300, "one"), (513, 900, 264, "zipf"), (480, 5, 520, "uniform"),
+                                              (200, 1_500_000, 8, "uniform"), (65_537, 30_000, 48, "zipf"),
+                                              (90_000, 70_000, 17, "uniform"), (600, 1_300_000, 8, "uniform"),
+                                              (6000, 4000, 1100, "uniform"), (2500, 9, 2048, "zipf")])
+@pytest.mark.parametrize("extra,accumulate", [(0, False), (0, True), (3, True)])
+def test_embedding_grad_lengths(mfsdp, dout, grad, n, vocab, dim, kind, extra, accumulate):
+    """Few ids and many, few rows and many, on both sides of where the launches change."""
+    test_embedding_grad(mfsdp, dout, grad, n, vocab, dim, kind, extra, accumulate)
+
+
 def test_embedding_grad_masked_values_do_not_leak(mfsdp):
     """NaN and Inf in rows whose id is masked stay out of every sum."""
     d = torch.full((40, 48), float("nan"), device="cuda")
