@@ -557,9 +557,13 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
   ptx::tc_fence_after();
   const uint32_t tmem_base = tmem_slot;
   const Abort ab{&abort_flag, p.status, p.wait_limit_ns};
-  // packed operands and padded ends come from the kernels before this one
-  ptx::wait_dependencies();
-  ptx::fence_proxy_async_global();
+  // Packed operands come from the kernel before this one.  Padded ends too, but the
+  // producers wait for those at the first one they meet (where there is none, that kernel
+  // has nothing to do): 25.6 and 24.5 us for 8 groups of 285.
+  if (!p.only_ends) {
+    ptx::wait_dependencies();
+    ptx::fence_proxy_async_global();
+  }
   const int n_tiles = listed ? first[p.n_experts] : p.n_experts * sh.tiles_m * sh.tiles_n;
   TileWalk<kMode> walk(p, sh, start, first, blockIdx.x >> 1, gridDim.x >> 1, n_tiles);
   Tile tl;
@@ -583,9 +587,14 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
     }
     __syncwarp();
     uint32_t s = 0, use = 0;
-    bool ok = true;
+    bool ok = true, ends_there = !kWgrad || !p.only_ends;
     while (walk.next(tl)) {
       const int blocks = blocks_of<kWgrad>(tl.k_len);
+      if (!ends_there && (tl.k_len & (kEnd - 1)) != 0) {
+        ptx::wait_dependencies();
+        ptx::fence_proxy_async_global();
+        ends_there = true;
+      }
       const int nh = tl.n_mma >> 1;                         // this CTA's columns of B
       const int mc = tl.m0 + (int)rank_u * kCtaM;
       // rows wholly past the matrix are not loaded (their output is not stored)
@@ -1139,6 +1148,7 @@ cudaError_t launch_expert(const ExpertArgs& in, cudaStream_t s) {
   }
   if (!ok) return cudaErrorInvalidValue;
   a.prepared = prep.a.jobs > 0;
+  a.only_ends = a.mode == kExpertWeightGrad && prep.a.jobs == 2;
   const cudaError_t e = prep.launch(s);
   if (e != cudaSuccess) return e;
   if (a.mode == kExpertWeightGrad) {

@@ -149,6 +149,7 @@ struct ExpertArgs {
   uint8_t* packs;         // workspace for operands whose rows are not 16-byte aligned
   uint64_t wait_limit_ns;
   int32_t prepared;       // kernels of this call that prepare operands run right before
+  int32_t only_ends;      // and what they prepare is the groups' padded ends
   int32_t chunk;          // weight gradient: tokens of a chunk of a split contraction (0: whole groups)
   int32_t slots;          // and chunks that there can be in all
 };
