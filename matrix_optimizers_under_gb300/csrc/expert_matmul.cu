@@ -1142,7 +1142,9 @@ cudaError_t launch_expert(const ExpertArgs& in, cudaStream_t s) {
          encode(&maps.d, a.a, k, n, a.a_ld, 1, n * a.a_ld, 64);
     // (a single row's leading dimension says nothing)
     const int64_t width = a.mode == kExpertForward ? a.rows : a.cols, y_ld = n > 1 ? a.out_ld : up8(width);
-    a.out_vec = y_ld * (a.out_bf16 ? 2 : 4) % 16 == 0;
+    // A tensor copy writes whole 16 bytes: a row that ends inside them would lose what lies beside it.
+    const int64_t esz = a.out_bf16 ? 2 : 4;
+    a.out_vec = y_ld * esz % 16 == 0 && width * esz % 16 == 0;
     if (a.out_vec)
       ok = ok && encode(&maps.out, a.out, width, n, y_ld, 1, n * y_ld, a.out_bf16 ? 16 : 8, 32, !a.out_bf16, false);
   }

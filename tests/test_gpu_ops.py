@@ -329,6 +329,14 @@ def test_expert_matmul(mfsdp, out, counts, rows, cols, extra, tail, input_grad):
     assert np.all(host(buf)[:, width:] == 7.0)
 
 
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("counts,rows,cols", [([1] * 16, 100, 1096), ([16], 37, 2056), ([5, 0, 11], 64, 300), ([4] * 4, 9, 8),
+                                              ([0, 1, 0], 1408, 2048), ([17], 65, 1000), ([3, 1, 0, 2] * 2, 33, 4099)])
+@pytest.mark.parametrize("extra,tail", [(0, 0), (8, 3), (3, 1)])
+def test_expert_matmul_few_tokens(mfsdp, out, counts, rows, cols, extra, tail):
+    test_expert_matmul(mfsdp, out, counts, rows, cols, extra, tail, False)
+
+
 @pytest.mark.parametrize("out,accumulate", [("bf16", False), ("f32", False), ("f32", True), ("bf16", True)])
 @pytest.mark.parametrize("counts,rows,cols", EXP)
 @pytest.mark.parametrize("extra,tail", [(0, 0), (8, 2), (3, 0)])
@@ -393,6 +401,35 @@ def test_expert_neighbours_do_not_leak(mfsdp):
     for t in (y, dx):
         assert torch.isfinite(t[:19]).all() and torch.isfinite(t[64:]).all() and not torch.isfinite(t[19:64]).any()
     assert torch.isfinite(dw[[0, 2, 3]]).all() and not torch.isfinite(dw[1]).any()
+
+
+@pytest.mark.parametrize("n,rows,cols", [(70, 37, 301), (9, 45, 29), (300, 131, 1021)])
+def test_expert_padding_is_neither_read_nor_written(mfsdp, n, rows, cols):
+    """Rows that end inside 16 bytes, with NaN between them."""
+    up = lambda v: -(-v // 8) * 8
+    rng = np.random.default_rng(n)
+    nan = float("nan")
+    starts = torch.tensor([0, n // 3, n], dtype=torch.int32, device="cuda")
+    x, _ = padded(n, cols, "bf16", up(cols) - cols, nan)
+    dy, _ = padded(n, rows, "bf16", up(rows) - rows, nan)
+    x.copy_(dev(rng.standard_normal((n, cols)), "bf16"))
+    dy.copy_(dev(rng.standard_normal((n, rows)), "bf16"))
+    w = dev(rng.standard_normal((2, rows, cols)), "bf16")
+    ws = scratch(mfsdp.expert_workspace_bytes(2, rows, cols, n, rows_ld=up(rows), cols_ld=up(cols)))
+    y, ybuf = padded(n, rows, "f32", up(rows) - rows, 7.0)
+    dx, dxbuf = padded(n, cols, "bf16", up(cols) - cols, 7.0)
+    dw = torch.empty(2, rows, cols, device="cuda")
+    mfsdp.expert_matmul(x, w, starts, y, ws)
+    mfsdp.expert_matmul(dy, w, starts, dx, ws, input_grad=True)
+    mfsdp.expert_weight_grad(dy, x, starts, dw, ws)
+    hs, hx, hdy, hw = starts.cpu().numpy(), host(x), host(dy), host(w)
+    for got, a, grad, k, h in ((y, hx, False, cols, U), (dx, hdy, True, rows, H)):
+        want, mag = expert_matmul_ref(a, hw, hs, grad), expert_matmul_ref(np.abs(a), np.abs(hw), hs, grad)
+        close(host(got), want, max(k, 32) * U * mag + h * np.abs(want), "product")
+    want = expert_weight_grad_ref(hdy, hx, hs, None)
+    mag = expert_weight_grad_ref(np.abs(hdy), np.abs(hx), hs, None)
+    close(host(dw), want, (n + 33) * U * mag + U * np.abs(want), "weight gradient")
+    assert torch.all(ybuf[:, rows:] == 7.0) and torch.all(dxbuf[:, cols:] == 7.0)
 
 
 def test_expert_gradients_are_adjoints(mfsdp):
