@@ -649,8 +649,9 @@ size_t mfsdp_expert_workspace_bytes(int32_t n_experts, int64_t n_rows, int64_t r
  * A layout whose rows all start on 16-byte boundaries (cols, w_stride and x_ld
  * multiples of 8) is read in place; any other is first copied, padded, into the
  * workspace.  n_rows = 0 is a no-op.  n_experts <= MFSDP_MAX_EXPERTS, n_rows <=
- * 2^30, rows, cols <= 2^24, and 2^30 tiles of 256 x 256 in each product.  Errors: INVALID_ARG, UNSUPPORTED_DTYPE, UNSUPPORTED_SHAPE,
- * MISALIGNED, OVERLAP, WORKSPACE_TOO_SMALL, CUDA. */
+ * 2^30, rows, cols <= 2^24, and 2^30 tiles of 256 x 256 in each product.
+ * Errors: INVALID_ARG, UNSUPPORTED_DTYPE, UNSUPPORTED_SHAPE, MISALIGNED, OVERLAP,
+ * WORKSPACE_TOO_SMALL, CUDA. */
 int mfsdp_expert_matmul(const void* x, int64_t x_ld, const void* w, int64_t w_stride, int32_t in_dtype,
                         const int32_t* starts, int32_t n_experts, int64_t n_rows, int64_t rows, int64_t cols,
                         int32_t input_grad, void* y, int32_t y_dtype, int64_t y_ld, void* workspace,

@@ -12,21 +12,23 @@
 // a row (layouts whose rows do not start on such a boundary: 8 columns a block
 // apart, so a warp's scalar accesses are still contiguous).
 //
-// Gradient, in three launches: the sort of positions by token (stable), the rows, and the
-// rows that the division of work cut.
+// Gradient, of more ids than a few, in three launches: the sort of positions by token
+// (stable), the rows, and the rows that the division of work cut.
 //   - Most of the vocabulary is unnamed in a batch, and its rows' zeros need no
-//     order: the second kernel starts while the sort runs (on 8 SMs, ~15 us),
+//     order: the second kernel starts beside the sort (on 8 SMs, ~13 us),
 //     finds the unnamed ones among its share of the rows from the ids
 //     themselves, and writes them.
-//   - Then every CTA adds up an equal run of the sorted positions (a slab): a token may
-//     be named once or fill the batch, so rows are no fair share of work.  A row
-//     whose positions lie in one slab is written there; a row cut by slab ends leaves one partial
-//     row a slab in the workspace, and the third kernel adds them in slab
+//   - Then every CTA adds up an equal run of the sorted positions (a slab): a token
+//     may be named once or fill the batch, so rows are no fair share of work.  A row
+//     whose positions lie in one slab is written there; a row cut by slab ends leaves
+//     one partial row a slab in the workspace, and the third kernel adds them in slab
 //     order.  The slabs depend on the sizes alone, so every sum has a fixed
 //     order: no atomics on sums, bitwise reproducible, in fp32.
 //   - Rows of dout arrive in shared memory as bulk copies, an instruction a row,
-//     and a zero row leaves as one: with plain loads and stores in one kernel after the
-//     sort, the rows took 72 us for 32768 x 2048 (34 M warp instructions).
+//     and a zero row leaves as one.  32768 ids, 32000 x 2048 fp32: 86 us in all, of which
+//     ~10 before the zeros and ~10 after the rows; 396 MB in between at 6.3 TB/s (a
+//     fill alone writes at 6.2, a copy runs at 6.8).  With plain loads and stores after
+//     the sort, the rows alone took 72 us.
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -227,10 +229,10 @@ __device__ __forceinline__ int64_t warp_lower_bound(const int32_t* keys, int64_t
   return lo;
 }
 
-// Calls zero(row) for the unnamed rows of this CTA's share of the vocabulary,
-// each from one thread (or one whole warp), and waits for the sort: a short list of ids is read
-// before the wait by every CTA; a long one would take longer than the sort, so then each
-// CTA looks up its part of the sorted keys.  All threads call it.
+// Calls zero(row) for the unnamed rows of this CTA's share of the vocabulary, each from
+// one thread (or one whole warp), and waits for the sort: a short list of ids is read
+// before the wait by every CTA; a long one would take longer than the sort, so then
+// each CTA looks up its part of the sorted keys.  All threads call it.
 constexpr int kWindow = 8192;              // rows marked at a time
 constexpr int64_t kScanIds = 65536;
 
@@ -438,7 +440,8 @@ __global__ void __launch_bounds__(kMaxThreads, 3) embed_grad_kernel(const __grid
     }
   }
   // (a masked key that goes on is no row: v is the last row before it)
-  if (v >= 0) put_row<kOutBf16, false>(p, sl, s, c0, v, first, a.keys[sl.i1 - 1] == v, tid, kMaxThreads, cols, acc, old);
+  if (v >= 0)
+    put_row<kOutBf16, false>(p, sl, s, c0, v, first, a.keys[sl.i1 - 1] == v, tid, kMaxThreads, cols, acc, old);
   if (tid < 32 && blockIdx.y == 0) note_cut(p, sl, s);
 }
 
@@ -640,7 +643,8 @@ __global__ void __launch_bounds__(32 * kFixParts) embed_fix_kernel(const __grid_
     const int64_t slabs = cut.last - cut.first + 1;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     if (c < p.part_ld)
-      add_parts(p, cut, cut.first + (int)(slabs * warp / kFixParts), cut.first + (int)(slabs * (warp + 1) / kFixParts), c, acc);
+      add_parts(p, cut, cut.first + (int)(slabs * warp / kFixParts),
+                cut.first + (int)(slabs * (warp + 1) / kFixParts), c, acc);
     __syncthreads();
     sum[warp][lane] = acc;
     __syncthreads();
@@ -808,7 +812,8 @@ void lookup_launch(const LookupArgs& a, dim3 grid, dim3 block, cudaStream_t s) {
 // not fit its bitmap.
 int64_t small_shares(int64_t vocab, int64_t dim) {
   const int64_t blocks = (dim + kSmallCols - 1) / kSmallCols;
-  return std::max((vocab + kSmallShare - 1) / kSmallShare, std::min((vocab + 7) / 8, std::max<int64_t>(1, 608 / blocks)));
+  const int64_t want = std::min((vocab + 7) / 8, std::max<int64_t>(1, 608 / blocks));
+  return std::max((vocab + kSmallShare - 1) / kSmallShare, want);
 }
 
 template <bool kIn, bool kOut>
@@ -846,7 +851,8 @@ cudaError_t grad_launch(GradKernelArgs& p, int64_t ctas, bool vec, cudaStream_t 
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
   if (!ready[dev].load()) {
-    e = cudaFuncSetAttribute(embed_rows_kernel<kIn, kOut>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes + 16384);
+    e = cudaFuncSetAttribute(embed_rows_kernel<kIn, kOut>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kRingBytes + 16384);
     if (e != cudaSuccess) return e;
     ready[dev].store(true);
   }
@@ -862,11 +868,16 @@ cudaError_t launch_lookup(const LookupArgs& a, cudaStream_t s) {
   const dim3 block(tx, ty);
   const dim3 grid((unsigned)((a.n + ty * kLookupRows - 1) / (ty * kLookupRows)),
                   (unsigned)((a.dim + tx * kCols - 1) / (tx * kCols)));
-  const auto go = vec ? (a.w_bf16 ? (a.out_bf16 ? lookup_launch<true, true, true> : lookup_launch<true, false, true>)
-                                  : (a.out_bf16 ? lookup_launch<false, true, true> : lookup_launch<false, false, true>))
-                      : (a.w_bf16 ? (a.out_bf16 ? lookup_launch<true, true, false> : lookup_launch<true, false, false>)
-                                  : (a.out_bf16 ? lookup_launch<false, true, false> : lookup_launch<false, false, false>));
-  go(a, grid, block, s);
+  if (vec)
+    a.w_bf16 ? (a.out_bf16 ? lookup_launch<true, true, true>(a, grid, block, s)
+                           : lookup_launch<true, false, true>(a, grid, block, s))
+             : (a.out_bf16 ? lookup_launch<false, true, true>(a, grid, block, s)
+                           : lookup_launch<false, false, true>(a, grid, block, s));
+  else
+    a.w_bf16 ? (a.out_bf16 ? lookup_launch<true, true, false>(a, grid, block, s)
+                           : lookup_launch<true, false, false>(a, grid, block, s))
+             : (a.out_bf16 ? lookup_launch<false, true, false>(a, grid, block, s)
+                           : lookup_launch<false, false, false>(a, grid, block, s));
   return cudaGetLastError();
 }
 
@@ -892,8 +903,10 @@ cudaError_t launch_embed_grad(const EmbedGradArgs& a, cudaStream_t s) {
   p.n_cut = a.header + 1;
   p.cut = reinterpret_cast<CutRow*>(at);
   p.parts = reinterpret_cast<float*>(at + round_up(sp.slabs * sizeof(CutRow), 256));
-  const cudaError_t e = a.dout_bf16 ? (a.grad_bf16 ? grad_launch<true, true>(p, sp.ctas, vec, s) : grad_launch<true, false>(p, sp.ctas, vec, s))
-                                    : (a.grad_bf16 ? grad_launch<false, true>(p, sp.ctas, vec, s) : grad_launch<false, false>(p, sp.ctas, vec, s));
+  const cudaError_t e = a.dout_bf16 ? (a.grad_bf16 ? grad_launch<true, true>(p, sp.ctas, vec, s)
+                                                   : grad_launch<true, false>(p, sp.ctas, vec, s))
+                                    : (a.grad_bf16 ? grad_launch<false, true>(p, sp.ctas, vec, s)
+                                                   : grad_launch<false, false>(p, sp.ctas, vec, s));
   if (e != cudaSuccess) return e;
   const int64_t items = sp.slabs * ((a.dim + kFixCols - 1) / kFixCols);      // at most
   const dim3 fix((unsigned)std::min<int64_t>(items, 4 * std::max(1, sm_count())));

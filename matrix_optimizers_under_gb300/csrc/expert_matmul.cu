@@ -24,15 +24,15 @@
 // cost the issuer 1800-1950 cycles a tile of 5300; zeroing one operand
 // would let a NaN of the other through.)
 //
-// CTA pairs (one CTA per SM, cta_group::2) take tiles of 256 x up to 256
-// round-robin from a list that every CTA works out from `starts`, expert by
-// expert, so a wave's tiles share their operands in L2.  A CTA loads its 128
-// rows of A and its half of B, 32 KB per 64 of K: 64 bytes a clock at the full
-// MMA rate, where a CTA alone on 128 x 256 would need 96.  Warp roles: 0
-// producer, 1 MMA issuer (even CTA), 4-11 epilogue; two accumulators in TMEM let the epilogue overlap the next
-// tile.  The pipeline has as many stages of K = 64 as shared memory holds at the
-// launch's widest tile: 6 of 32 KB for 256 tokens, 10 of 20 KB for a few tokens,
-// where the product is bound by reading W.
+// CTA pairs (one CTA per SM, cta_group::2) take tiles of 256 x up to 256 round-robin
+// from a list that every CTA works out from `starts`, expert by expert, so a wave's
+// tiles share their operands in L2.  A CTA loads its 128 rows of A and its half of B,
+// 32 KB per 64 of K: 64 bytes a clock at the full MMA rate, where a CTA alone on 128 x
+// 256 would need 96.  Warp roles: 0 producer, 1 MMA issuer (even CTA), 4-11 epilogue;
+// two accumulators in TMEM let the epilogue overlap the next tile.  The pipeline has as
+// many stages of K = 64 as shared memory holds at the launch's widest tile: 6 of 32 KB
+// for 256 tokens, 10 of 20 KB for a few tokens, where the product is bound by reading
+// W.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -691,7 +691,9 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
               const uint64_t bdesc = ptx::smem_desc_sw128(sa + kBytesA, kWgrad ? kMnBlock : 16, 1024);
               // K-major operands past the contraction's end are zeros of the copy's fill
               const int left = tl.k_len - (kb + h) * kBlockK;
-              const int steps = ragged && kb + h == blocks - 1 ? 1 : min(kBlockK / 16, kWgrad ? left / 16 : ceil_div(left, 16));
+              const int steps = ragged && kb + h == blocks - 1
+                                    ? 1
+                                    : min(kBlockK / 16, kWgrad ? left / 16 : ceil_div(left, 16));
 #pragma unroll
               for (int k = 0; k < kBlockK / 16; ++k)
                 if (k < steps)
@@ -755,8 +757,8 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
         const bool last = c + 2 * kWidth >= tl.n_mma;
         __syncwarp();
         if constexpr (kWgrad && kVec) {
-          put_chunk<kBf16, kAccumulate>(p, &maps.out, stage, t_row + c, tl.n0 + c, row0, tl.z, sh.m - row0, tl.n - c, parts,
-                                        last, release);
+          put_chunk<kBf16, kAccumulate>(p, &maps.out, stage, t_row + c, tl.n0 + c, row0, tl.z, sh.m - row0, tl.n - c,
+                                        parts, last, release);
           continue;
         }
         uint32_t r[32];
@@ -861,12 +863,12 @@ __global__ void __launch_bounds__(32 * kSumWarps) sum_chunks_kernel(const __grid
   }
 }
 
-// What a call prepares for its tensor copies, in one launch: copies of operands
-// whose rows do not start on 16-byte boundaries (`rows` rows of `width` elements, ld
-// apart, of each of n matrices `stride` apart, into rows of width8 elements, zero-filled; a matrix
-// without tokens is left out), and the padded ends of the groups (rows 16 e ..
-// 16 e + 15: the last len % 16 rows of group e, then zeros; a length that is
-// a multiple of 16 needs none).
+// What a call prepares for its tensor copies, in one launch: copies of operands whose
+// rows do not start on 16-byte boundaries (`rows` rows of `width` elements, ld apart,
+// of each of n matrices `stride` apart, into rows of width8 elements, zero-filled; a
+// matrix without tokens is left out), and the padded ends of the groups (rows 16 e ..
+// 16 e + 15: the last len % 16 rows of group e, then zeros; a length that is a multiple
+// of 16 needs none).
 struct PrepareJob {
   const uint16_t* src;
   uint16_t* dst;
@@ -915,7 +917,8 @@ __global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(const __grid_c
     const bool vec = j.ld % 8 == 0 && j.width % 8 == 0;
     for (int i = part * kPrepareThreads + threadIdx.x; i < kEnd * chunks; i += j.per * kPrepareThreads) {
       const int r = i / chunks, c = (i - r * chunks) * 8;
-      const uint4 v = r < rest ? load8(j.src + (int64_t)(hi - rest + r) * j.ld, c, j.width, vec) : make_uint4(0, 0, 0, 0);
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (r < rest) v = load8(j.src + (int64_t)(hi - rest + r) * j.ld, c, j.width, vec);
       *reinterpret_cast<uint4*>(j.dst + ((int64_t)e * kEnd + r) * j.width8 + c) = v;
     }
     return;
@@ -945,7 +948,9 @@ constexpr int kFewAtOnce = 4;                             // tokens
 
 template <bool kBf16, bool kVec>
 __global__ void __launch_bounds__(kFewThreads, 4) few_tokens_kernel(const __grid_constant__ ExpertArgs p) {
-  __shared__ int32_t experts[kFewTokens], tokens[kFewTokens], count;     // of the items, in no fixed order
+  __shared__ int32_t experts[kFewTokens], tokens[kFewTokens];            // of the items, by token
+  __shared__ int2 found[kFewTokens];                                     // as the threads come upon them
+  __shared__ int count;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     count = 0;
@@ -956,11 +961,18 @@ __global__ void __launch_bounds__(kFewThreads, 4) few_tokens_kernel(const __grid
     const int hi = start_of(p, e + 1);
     for (int t = start_of(p, e); t < hi; t += kFewAtOnce) {
       const int at = atomicAdd(&count, 1);
-      if (at < kFewTokens) {
-        experts[at] = e;
-        tokens[at] = t;
-      }
+      if (at < kFewTokens) found[at] = make_int2(e, t);
     }
+  }
+  __syncthreads();
+  // every CTA needs them in the same order: its rows are a share of the whole list
+  if ((int)threadIdx.x < min(count, kFewTokens)) {
+    const int2 mine = found[threadIdx.x];
+    int at = 0;
+    for (int k = 0; k < min(count, kFewTokens); ++k)
+      at += found[k].y < mine.y || (found[k].y == mine.y && found[k].x < mine.x);
+    experts[at] = mine.x;
+    tokens[at] = mine.y;
   }
   __syncthreads();
   const int rows = (int)p.rows, cols = (int)p.cols;
@@ -1059,6 +1071,7 @@ bool encode(CUtensorMap* map, const void* base, int64_t width, int64_t height, i
 template <int kMode, bool kBf16, bool kAccumulate, bool kVec>
 cudaError_t launch_kernel(const ExpertArgs& a, const Maps& maps, int64_t max_tiles, cudaStream_t s) {
   constexpr size_t kSmemBytes = kRingBytes(kMode) + kEpiWarps * 2 * kPartBytes(kMode) + 1024;
+  const auto kernel = expert_kernel<kMode, kBf16, kAccumulate, kVec>;
   static std::mutex mu;
   static int resident[kMaxDevices] = {};      // CTA pairs on the device at once
   int dev = 0;
@@ -1081,11 +1094,11 @@ cudaError_t launch_kernel(const ExpertArgs& a, const Maps& maps, int64_t max_til
   {
     std::lock_guard<std::mutex> lock(mu);
     if (resident[dev] == 0) {
-      e = cudaFuncSetAttribute(expert_kernel<kMode, kBf16, kAccumulate, kVec>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
       if (e != cudaSuccess) return e;
       cfg.gridDim = dim3((unsigned)(2 * (sm_count() / 2)), 1, 1);
       int n = 0;
-      e = cudaOccupancyMaxActiveClusters(&n, expert_kernel<kMode, kBf16, kAccumulate, kVec>, &cfg);
+      e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
       if (e != cudaSuccess) return e;
       if (n < 1) return cudaErrorInvalidConfiguration;
       resident[dev] = n;
@@ -1095,22 +1108,23 @@ cudaError_t launch_kernel(const ExpertArgs& a, const Maps& maps, int64_t max_til
   cfg.numAttrs = a.prepared ? 2 : 1;      // may start beside the kernels that prepare its operands
   cfg.stream = s;
   cfg.gridDim = dim3((unsigned)(2 * std::max<int64_t>(1, std::min<int64_t>(pairs, max_tiles))), 1, 1);
-  e = cudaLaunchKernelEx(&cfg, expert_kernel<kMode, kBf16, kAccumulate, kVec>, a, maps);
+  e = cudaLaunchKernelEx(&cfg, kernel, a, maps);
   return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
 template <int kMode>
 cudaError_t launch_mode(const ExpertArgs& a, const Maps& maps, int64_t max_tiles, cudaStream_t s) {
   if constexpr (kMode == kExpertWeightGrad) {
-    const auto go = a.out_vec ? (a.out_bf16 ? (a.accumulate ? launch_kernel<kMode, true, true, true> : launch_kernel<kMode, true, false, true>)
-                                            : (a.accumulate ? launch_kernel<kMode, false, true, true> : launch_kernel<kMode, false, false, true>))
-                              : (a.out_bf16 ? (a.accumulate ? launch_kernel<kMode, true, true, false> : launch_kernel<kMode, true, false, false>)
-                                            : (a.accumulate ? launch_kernel<kMode, false, true, false> : launch_kernel<kMode, false, false, false>));
-    return go(a, maps, max_tiles, s);
+    if (a.accumulate)
+      return a.out_vec ? (a.out_bf16 ? launch_kernel<kMode, true, true, true>(a, maps, max_tiles, s)
+                                     : launch_kernel<kMode, false, true, true>(a, maps, max_tiles, s))
+                       : (a.out_bf16 ? launch_kernel<kMode, true, true, false>(a, maps, max_tiles, s)
+                                     : launch_kernel<kMode, false, true, false>(a, maps, max_tiles, s));
   }
-  const auto go = a.out_vec ? (a.out_bf16 ? launch_kernel<kMode, true, false, true> : launch_kernel<kMode, false, false, true>)
-                            : (a.out_bf16 ? launch_kernel<kMode, true, false, false> : launch_kernel<kMode, false, false, false>);
-  return go(a, maps, max_tiles, s);
+  return a.out_vec ? (a.out_bf16 ? launch_kernel<kMode, true, false, true>(a, maps, max_tiles, s)
+                                 : launch_kernel<kMode, false, false, true>(a, maps, max_tiles, s))
+                   : (a.out_bf16 ? launch_kernel<kMode, true, false, false>(a, maps, max_tiles, s)
+                                 : launch_kernel<kMode, false, false, false>(a, maps, max_tiles, s));
 }
 
 int64_t up4(int64_t x) { return (x + 3) / 4 * 4; }
@@ -1140,7 +1154,8 @@ struct Prepare {
     j.ends = ends;
     j.block0 = a.blocks;
     const int64_t share = std::max<int64_t>(1, (int64_t)sm_count() * 8 / n);       // enough blocks to fill the GPU
-    j.per = (int32_t)std::min<int64_t>(ends ? 1 : share, (rows * (up8(width) / 8) + kPrepareThreads - 1) / kPrepareThreads);
+    const int64_t blocks = (rows * (up8(width) / 8) + kPrepareThreads - 1) / kPrepareThreads;
+    j.per = (int32_t)std::min<int64_t>(ends ? 1 : share, blocks);
     a.blocks += j.per * n;
     at += packed_bytes(n * rows, width);
     return j.dst;
@@ -1202,7 +1217,8 @@ cudaError_t launch_expert(const ExpertArgs& in, cudaStream_t s) {
       const int64_t m = (int64_t)a.n_experts * kEnd, ea = up8(a.rows), eb = up8(a.cols);
       ok = encode(&maps.a, a.a, a.rows, n, a.a_ld, 1, n * a.a_ld, 64) &&
            encode(&maps.b, a.b, a.cols, n, a.b_ld, 1, n * a.b_ld, 64) &&
-           encode(&maps.c, end_a, a.rows, m, ea, 1, m * ea, kEnd) && encode(&maps.d, end_b, a.cols, m, eb, 1, m * eb, kEnd);
+           encode(&maps.c, end_a, a.rows, m, ea, 1, m * ea, kEnd) &&
+           encode(&maps.d, end_b, a.cols, m, eb, 1, m * eb, kEnd);
     }
     const int64_t esz = a.out_bf16 ? 2 : 4;
     a.out_vec = a.cols * esz % 16 == 0 && (a.n_experts == 1 || a.out_stride * esz % 16 == 0);
@@ -1221,7 +1237,8 @@ cudaError_t launch_expert(const ExpertArgs& in, cudaStream_t s) {
       a.out_vec = 1;
     }
     if (a.out_vec)
-      ok = ok && encode(&maps.out, a.out, a.cols, a.rows, a.out_ld, a.chunk > 0 ? a.slots : a.n_experts, out_stride, 16, a.out_bf16 ? 64 : 32, !a.out_bf16);
+      ok = ok && encode(&maps.out, a.out, a.cols, a.rows, a.out_ld, a.chunk > 0 ? a.slots : a.n_experts, out_stride, 16,
+                        a.out_bf16 ? 64 : 32, !a.out_bf16);
   } else {
     const int64_t k = a.mode == kExpertForward ? a.cols : a.rows;
     if (a.cols % 8 != 0 || (a.n_experts > 1 && a.b_stride % 8 != 0)) {
@@ -1232,11 +1249,13 @@ cudaError_t launch_expert(const ExpertArgs& in, cudaStream_t s) {
     prep.rows(&a.a, &a.a_ld, n, k);
     const int64_t w_stride = a.n_experts > 1 ? a.b_stride : a.rows * a.b_ld;
     ok = encode(&maps.a, a.b, a.cols, a.rows, a.b_ld, a.n_experts, w_stride, a.mode == kExpertForward ? 128 : 64) &&
-         encode(&maps.b, a.a, k, n, a.a_ld, 1, n * a.a_ld, 32) && encode(&maps.c, a.a, k, n, a.a_ld, 1, n * a.a_ld, 128) &&
+         encode(&maps.b, a.a, k, n, a.a_ld, 1, n * a.a_ld, 32) &&
+         encode(&maps.c, a.a, k, n, a.a_ld, 1, n * a.a_ld, 128) &&
          encode(&maps.d, a.a, k, n, a.a_ld, 1, n * a.a_ld, 64);
     // (a single row's leading dimension says nothing)
     const int64_t width = a.mode == kExpertForward ? a.rows : a.cols, y_ld = n > 1 ? a.out_ld : up8(width);
-    // A tensor copy writes whole 16 bytes: a row that ends inside them would lose what lies beside it.
+    // A tensor copy writes whole 16 bytes: where a row ends inside them, what lies
+    // beside it would be lost.
     const int64_t esz = a.out_bf16 ? 2 : 4;
     a.out_vec = y_ld * esz % 16 == 0 && width * esz % 16 == 0;
     if (a.out_vec)

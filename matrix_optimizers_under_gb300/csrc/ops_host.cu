@@ -89,7 +89,7 @@ bool by_lo(const Interval& a, const Interval& b) { return a.lo < b.lo; }
 
 // Destinations must be apart from each other, from the other tensors' sources,
 // and from their own source unless they are it (in place, one dtype).
-int check_clip_overlap(const mfsdp_grad_tensor* t, int32_t n, const void* out, const void* ws, size_t ws_bytes) {
+int check_clip_overlap(const mfsdp_grad_tensor* t, int32_t n, const void* out, const void* ws, size_t ws_bytes) try {
   std::vector<Interval> src, dst;
   src.reserve(n);
   dst.reserve(n);
@@ -123,6 +123,8 @@ int check_clip_overlap(const mfsdp_grad_tensor* t, int32_t n, const void* out, c
     }
   }
   return MFSDP_OK;
+} catch (...) {                                           // no host memory for the tables: nothing leaves a C entry
+  return MFSDP_ERR_CUDA;
 }
 
 int clip_blocks(int64_t chunks, int sms) {

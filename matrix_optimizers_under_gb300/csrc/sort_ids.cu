@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) sort_cluster_kernel(const 
   int (*cnt)[kDigits] = reinterpret_cast<int (*)[kDigits]>(smem + (size_t)kClusterTile * 16);
   __shared__ int hist[kDigits];                                              // this CTA's digits
   __shared__ int quarter[kQuarters][kDigits];
-  __shared__ int start[kDigits], shift_to[kDigits];                          // of a digit in `local`; from there to its place
+  __shared__ int start[kDigits], shift_to[kDigits];      // of a digit in `local`; from there to its place
   __shared__ int scan[2][kDigits / 32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = blockIdx.x, ctas = gridDim.x;                             // the grid is one cluster

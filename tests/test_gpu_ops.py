@@ -403,6 +403,16 @@ def test_expert_neighbours_do_not_leak(mfsdp):
     assert torch.isfinite(dw[[0, 2, 3]]).all() and not torch.isfinite(dw[1]).any()
 
 
+@pytest.mark.parametrize("experts,n", [(128, 8), (1024, 16), (300, 13)])
+def test_expert_matmul_few_tokens_of_many_experts(mfsdp, experts, n):
+    """Experts that different warps look at, on every SM: all rows of all tokens are there."""
+    rng = np.random.default_rng(experts)
+    counts = np.zeros(experts, np.int64)
+    np.add.at(counts, rng.integers(0, experts, n), 1)
+    for _ in range(5):
+        test_expert_matmul(mfsdp, "f32", list(counts), 700, 264, 0, 0, False)
+
+
 @pytest.mark.parametrize("n,rows,cols", [(70, 37, 301), (9, 45, 29), (300, 131, 1021)])
 def test_expert_padding_is_neither_read_nor_written(mfsdp, n, rows, cols):
     """Rows that end inside 16 bytes, with NaN between them."""
