@@ -62,6 +62,12 @@ constexpr int kTurn = 2;
 // epilogue warp's staging, which has two.
 constexpr int kRingBytes(int mode) { return mode == kExpertWeightGrad ? 6 * 32768 : 10 * 20480; }
 constexpr int kPartBytes(int mode) { return mode == kExpertWeightGrad ? 2048 : 1024; }
+// Contraction of an fp32 output that one accumulator takes.  The tensor cores' additions
+// cut off low bits, always towards zero: off by 1.0e-6 of the result (2-norms, normal operands)
+// at K = 1024, 2.1e-6 at 2048, 1.9e-5 at 16384, 7.6e-5 at 65536, where a loop of fp32
+// additions is off by 3e-7.  So a longer one is taken in turns, and the turns' sums
+// are added, rounded to nearest, where the output lies.  (A bf16 output is off by 1.7e-3.)
+constexpr int kMaxK = 2048;
 constexpr int kEpiWarps = 8;
 constexpr int kFirstEpiWarp = 4;
 constexpr int kThreads = 32 * (kFirstEpiWarp + kEpiWarps);
@@ -122,7 +128,7 @@ struct Tile {
   int32_t group;      // first token of the group
   int32_t m0, n0;
   int32_t n, n_mma;
-  int32_t k_len;
+  int32_t k_from, k_len;     // of the contraction: where it starts, how long it is
 };
 
 struct Shape {
@@ -259,7 +265,7 @@ __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xf
 // The tiles a pair takes: pair0, pair0 + pairs, ...  Finding a tile's place
 // takes divisions and a search, ~1000 cycles, of the ~3000 a small tile takes
 // in all; so a warp finds 32 tiles at a time, one a lane, and hands them out.
-template <int kMode>
+template <int kMode, bool kTurns>
 struct TileWalk {
   const ExpertArgs& p;
   const Shape& sh;
@@ -267,14 +273,21 @@ struct TileWalk {
   const int32_t* first;
   int t, pairs, n_tiles;
   int held;               // tiles left in `mine`
+  int rest;               // kTurns: what is left of the tile's contraction
   Tile mine;
 
   __device__ __forceinline__ TileWalk(const ExpertArgs& p_, const Shape& sh_, const int32_t* start_,
                                       const int32_t* first_, int pair0, int pairs_, int n_tiles_)
-      : p(p_), sh(sh_), start(start_), first(first_), t(pair0), pairs(pairs_), n_tiles(n_tiles_), held(0) {}
-  // The next tile, the same in all lanes (kShape: only its n_mma and k_len); false after the last.
+      : p(p_), sh(sh_), start(start_), first(first_), t(pair0), pairs(pairs_), n_tiles(n_tiles_), held(0), rest(0) {}
+  // The next tile, or the next turn of the same one, the same in all lanes (kShape: only its n_mma and k_len); false after the last.
   template <bool kShape = false>
   __device__ __forceinline__ bool next(Tile& r) {
+    if (kTurns && rest > 0) {
+      r.k_from += r.k_len;
+      r.k_len = min(rest, kMaxK);
+      rest -= r.k_len;
+      return true;
+    }
     if (t >= n_tiles) return false;
     if (held == 0) {
       const int64_t ahead = t + (int64_t)(threadIdx.x & 31) * pairs;
@@ -293,6 +306,11 @@ struct TileWalk {
     }
     r.n_mma = __shfl_sync(0xffffffffu, mine.n_mma, lane);
     r.k_len = __shfl_sync(0xffffffffu, mine.k_len, lane);
+    r.k_from = 0;
+    if (kTurns) {
+      rest = max(0, r.k_len - kMaxK);
+      r.k_len -= rest;
+    }
     --held;
     t += pairs;
     return true;
@@ -308,7 +326,7 @@ __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w 
 // out: the first row's first element.
 template <bool kBf16, bool kAccumulate>
 __device__ __forceinline__ void put_plain(const ExpertArgs& p, uint8_t* stage, const uint32_t (&v)[32], int64_t at,
-                                          int rows, int cols) {
+                                          int rows, int cols, bool add = false) {
   const int lane = threadIdx.x & 31;
   float* const part = reinterpret_cast<float*>(stage);      // 16 rows of 33 floats
 #pragma unroll
@@ -330,7 +348,7 @@ __device__ __forceinline__ void put_plain(const ExpertArgs& p, uint8_t* stage, c
         *o = __float2bfloat16_rn(kAccumulate ? x + __bfloat162float(*o) : x);
       } else {
         float* o = static_cast<float*>(p.out) + i;
-        *o = kAccumulate ? x + *o : x;
+        *o = kAccumulate || add ? x + *o : x;
       }
     }
   }
@@ -344,7 +362,7 @@ __device__ __forceinline__ void put_plain(const ExpertArgs& p, uint8_t* stage, c
 // 3800 cycles a tile of 2300 cycles of MMAs; with each lane's to its own row
 // 5000.  Chunk c of row r sits at c ^ (r & 7), the copy's swizzle.
 __device__ __forceinline__ void put_rows(uint8_t* stage, const uint32_t (&w)[32], const CUtensorMap* map, int x, int y,
-                                         int z, int rows, uint32_t& parts) {
+                                         int z, int rows, uint32_t& parts, bool add = false) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -361,7 +379,8 @@ __device__ __forceinline__ void put_rows(uint8_t* stage, const uint32_t (&w)[32]
     }
     __syncwarp();
     if (lane == 0) {
-      ptx::tma_store_3d(map, ptx::smem_u32(part), x, y + 16 * h, z);
+      if (add) ptx::tma_add_3d(map, ptx::smem_u32(part), x, y + 16 * h, z);
+      else ptx::tma_store_3d(map, ptx::smem_u32(part), x, y + 16 * h, z);
       ptx::bulk_commit();
     }
   }
@@ -397,11 +416,11 @@ __device__ __forceinline__ void get_rows(uint8_t* stage, uint32_t (&w)[32], cons
 // columns to bf16, or 32 to fp32.  `last`: then hands the accumulator back.
 template <bool kBf16, bool kAccumulate, typename Release>
 __device__ __forceinline__ void put_chunk(const ExpertArgs& p, const CUtensorMap* map, uint8_t* stage, uint32_t taddr,
-                                          int x, int y, int z, int rows, int cols, uint32_t& parts, bool last,
-                                          Release release) {
+                                          int x, int y, int z, int rows, int cols, uint32_t& parts, bool add,
+                                          bool last, Release release) {
   constexpr int kEsz = kBf16 ? 2 : 4;
   uint32_t w[32], acc[32];
-  if constexpr (kAccumulate)
+  if (kAccumulate && !add)
     get_rows(stage, w, static_cast<const uint8_t*>(p.out) + (z * p.out_stride + y * p.out_ld + x) * kEsz,
              p.out_ld * kEsz, rows, min(8, cols * kEsz / 16));
 #pragma unroll
@@ -420,11 +439,11 @@ __device__ __forceinline__ void put_chunk(const ExpertArgs& p, const CUtensorMap
         const __nv_bfloat162 q = __floats2bfloat162_rn(a, b);
         w[16 * h + k] = *reinterpret_cast<const uint32_t*>(&q);
       } else {
-        w[k] = kAccumulate ? __float_as_uint(__uint_as_float(acc[k]) + __uint_as_float(w[k])) : acc[k];
+        w[k] = kAccumulate && !add ? __float_as_uint(__uint_as_float(acc[k]) + __uint_as_float(w[k])) : acc[k];
       }
     }
   }
-  put_rows(stage, w, map, x, y, z, rows, parts);
+  put_rows(stage, w, map, x, y, z, rows, parts, !kBf16 && add);
 }
 
 // 32 tokens (`cnt` of them the group's) of a warp's 32 rows of M, lane l holding
@@ -436,7 +455,7 @@ __device__ __forceinline__ void put_chunk(const ExpertArgs& p, const CUtensorMap
 template <bool kBf16, bool kVec>
 __device__ __forceinline__ void put_tokens(const ExpertArgs& p, const CUtensorMap* map, uint8_t* stage,
                                            const uint32_t (&r)[32], int row0, int rows, int token, int cnt,
-                                           uint32_t& parts) {
+                                           uint32_t& parts, bool add) {
   constexpr int kPiece = kBf16 ? 16 : 8;
   const int lane = threadIdx.x & 31;
 #pragma unroll
@@ -455,7 +474,8 @@ __device__ __forceinline__ void put_tokens(const ExpertArgs& p, const CUtensorMa
       ptx::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        ptx::tma_store_3d(map, ptx::smem_u32(part), row0, token + q * kPiece, 0);
+        if (!kBf16 && add) ptx::tma_add_3d(map, ptx::smem_u32(part), row0, token + q * kPiece, 0);
+        else ptx::tma_store_3d(map, ptx::smem_u32(part), row0, token + q * kPiece, 0);
         ptx::bulk_commit();
       }
     } else if (lane < rows) {
@@ -465,7 +485,10 @@ __device__ __forceinline__ void put_tokens(const ExpertArgs& p, const CUtensorMa
         if (q * kPiece + j >= cnt) break;
         const float x = __uint_as_float(r[q * kPiece + j]);
         if constexpr (kBf16) static_cast<__nv_bfloat16*>(p.out)[at + j * p.out_ld] = __float2bfloat16_rn(x);
-        else static_cast<float*>(p.out)[at + j * p.out_ld] = x;
+        else {
+          float* const o = static_cast<float*>(p.out) + at + j * p.out_ld;
+          *o = add ? x + *o : x;
+        }
       }
     }
   }
@@ -566,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
     ptx::fence_proxy_async_global();
   }
   const int n_tiles = listed ? first[p.n_experts] : p.n_experts * sh.tiles_m * sh.tiles_n;
-  TileWalk<kMode> walk(p, sh, start, first, blockIdx.x >> 1, gridDim.x >> 1, n_tiles);
+  TileWalk<kMode, !kBf16> walk(p, sh, start, first, blockIdx.x >> 1, gridDim.x >> 1, n_tiles);
   Tile tl;
   // Shared memory of a stage: A, then this CTA's half of B.
   const int wide = kWgrad ? sh.width_n : widest;
@@ -617,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
             ok = ok && wait_bar<false>(empty0 + 8 * slot, (slot_use & 1) ^ 1, ab, kRoleStage);
             if (!ok) break;
             const uint32_t sa = base_u + slot * stage_bytes, sb = sa + kBytesA, bar = pair_full0 + 8 * slot;
-            const int k0 = (kb + h) * kBlockK;
+            const int k0 = tl.k_from + (kb + h) * kBlockK;
             const bool last = ragged && kb + h == blocks - 1;       // 16 rows: a quarter of the bytes
             if (rank_u == 0)
               ptx::mbar_arrive_expect_tx(full0 + 8 * slot, last ? pair_bytes * kEnd / kBlockK : pair_bytes);
@@ -753,12 +776,17 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
         if (lane == 0) ptx::mbar_arrive_signal(ptx::mapa_shared(ptx::smem_u32(&tempty_bar[a]), 0));
       };
       if (kWidth * half >= tl.n_mma) release();           // no chunk for this warp
+      const bool add = !kBf16 && tl.k_from > 0;
+      if (kVec && add) {                                   // what is added to is there
+        if (lane == 0) ptx::bulk_wait_all();
+        __syncwarp();
+      }
       for (int c = kWidth * half; c < tl.n_mma; c += 2 * kWidth) {
         const bool last = c + 2 * kWidth >= tl.n_mma;
         __syncwarp();
         if constexpr (kWgrad && kVec) {
           put_chunk<kBf16, kAccumulate>(p, &maps.out, stage, t_row + c, tl.n0 + c, row0, tl.z, sh.m - row0, tl.n - c,
-                                        parts, last, release);
+                                        parts, add, last, release);
           continue;
         }
         uint32_t r[32];
@@ -766,10 +794,11 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
         ptx::tmem_ld_wait();
         if (last) release();
         if constexpr (kWgrad) {
-          put_plain<kBf16, kAccumulate>(p, stage, r, at0 + c, sh.m - row0, tl.n - c);
+          put_plain<kBf16, kAccumulate>(p, stage, r, at0 + c, sh.m - row0, tl.n - c, add);
         } else {
           if (row0 < sh.m)
-            put_tokens<kBf16, kVec>(p, &maps.out, stage, r, row0, sh.m - row0, tl.group + tl.n0 + c, tl.n - c, parts);
+            put_tokens<kBf16, kVec>(p, &maps.out, stage, r, row0, sh.m - row0, tl.group + tl.n0 + c, tl.n - c,
+                                    parts, add);
         }
       }
       ++acc_it;

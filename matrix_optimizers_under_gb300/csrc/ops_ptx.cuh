@@ -69,6 +69,13 @@ __device__ __forceinline__ void tma_store_3d(const void* tmap, uint32_t src, int
                "r"(y), "r"(z), "r"(src)
                : "memory");
 }
+// The same, added in fp32 to what is there.
+__device__ __forceinline__ void tma_add_3d(const void* tmap, uint32_t src, int32_t x, int32_t y, int32_t z) {
+  asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                   tmap),
+               "r"(x), "r"(y), "r"(z), "r"(src)
+               : "memory");
+}
 // This thread's bulk stores but for the last kLeft groups have read their shared memory.
 template <int kLeft>
 __device__ __forceinline__ void bulk_wait_read() {

@@ -413,6 +413,43 @@ def test_expert_matmul_few_tokens_of_many_experts(mfsdp, experts, n):
         test_expert_matmul(mfsdp, "f32", list(counts), 700, 264, 0, 0, False)
 
 
+@pytest.mark.parametrize("counts,rows,cols", [([40, 0, 300], 72, 5000), ([17, 33], 4100, 2049), ([7000], 2100, 1304),
+                                              ([2100, 5001], 1100, 1299)])
+@pytest.mark.parametrize("extra,accumulate", [(0, False), (3, True)])
+def test_expert_long_contractions(mfsdp, counts, rows, cols, extra, accumulate):
+    """Contractions past what one accumulator takes, in each of the products."""
+    for grad in (False, True):
+        test_expert_matmul(mfsdp, "f32", counts, rows, cols, extra, 0, grad)
+    test_expert_weight_grad(mfsdp, "f32", accumulate, counts, rows, cols, extra, 0)
+
+
+@pytest.mark.parametrize("k", [2048, 16_384, 70_000])
+def test_expert_fp32_outputs_keep_their_bits(mfsdp, k):
+    """Positive operands, so no partial sum is larger than the result: 2048 / 16 + 1
+    additions on a tensor core, each cutting off 2 u of it at most, and k / 2048 + 1
+    rounded ones."""
+    rng = np.random.default_rng(k)
+    bound = (2 * 129 + k / 2048 + 1) * U
+    x, w = dev(np.abs(rng.standard_normal((64, k))), "bf16"), dev(np.abs(rng.standard_normal((1, 96, k))), "bf16")
+    starts = torch.tensor([0, 64], dtype=torch.int32, device="cuda")
+    y = torch.empty(64, 96, device="cuda")
+    mfsdp.expert_matmul(x, w, starts, y, scratch(mfsdp.expert_workspace_bytes(1, 96, k, 64)))
+    want = host(x) @ host(w)[0].T
+    close(host(y), want, bound * want, "forward")
+    starts[1] = k
+    dy, xs = x.T.contiguous(), w[0].T.contiguous()
+    dy, xs = torch.cat([dy] * 40, 1), torch.cat([xs] * 10, 1)                     # 2560 x 960: not cut for the GPU's sake
+    dw = torch.empty(1, 2560, 960, device="cuda")
+    mfsdp.expert_weight_grad(dy, xs, starts, dw, scratch(mfsdp.expert_workspace_bytes(1, 2560, 960, k)))
+    got = host(dw)[0].reshape(40, 64, 10, 96)
+    close(got, np.broadcast_to(want[None, :, None, :], got.shape), bound * want[None, :, None, :], "weight gradient")
+    wt = w.transpose(1, 2).contiguous()                                           # k rows: the input gradient's contraction
+    dxx = torch.empty(64, 96, device="cuda")
+    starts[1] = 64
+    mfsdp.expert_matmul(x, wt, starts, dxx, scratch(mfsdp.expert_workspace_bytes(1, k, 96, 64)), input_grad=True)
+    close(host(dxx), want, bound * want, "input gradient")
+
+
 @pytest.mark.parametrize("n,rows,cols", [(70, 37, 301), (9, 45, 29), (300, 131, 1021)])
 def test_expert_padding_is_neither_read_nor_written(mfsdp, n, rows, cols):
     """Rows that end inside 16 bytes, with NaN between them."""
