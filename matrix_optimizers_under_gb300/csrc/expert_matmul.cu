@@ -60,7 +60,9 @@ constexpr int kMaxStages = 10;
 constexpr int kTurn = 2;
 // Shared memory of the stages (six of 32 KB, or ten of 20 KB), and of a part of an
 // epilogue warp's staging, which has two.
-constexpr int kRingBytes(int mode) { return mode == kExpertWeightGrad ? 6 * 32768 : 10 * 20480; }
+constexpr int kRingBytes(int mode, bool accumulate) {
+  return mode != kExpertWeightGrad ? 10 * 20480 : accumulate ? 4 * 32768 : 6 * 32768;
+}
 constexpr int kPartBytes(int mode) { return mode == kExpertWeightGrad ? 2048 : 1024; }
 // Contraction of an fp32 output that one accumulator takes.  The tensor cores' additions
 // cut off low bits, always towards zero: off by 1.0e-6 of the result (2-norms, normal operands)
@@ -385,44 +387,37 @@ __device__ __forceinline__ void put_rows(uint8_t* stage, const uint32_t (&w)[32]
     }
   }
 }
-// The way back: each lane receives its row's 128 bytes.
-__device__ __forceinline__ void get_rows(uint8_t* stage, uint32_t (&w)[32], const uint8_t* in, int64_t pitch, int rows,
-                                         int chunks) {
+// The way back, in two steps: 128 bytes of each of a warp's 32 rows (`rows` and
+// `chunks` of 16 bytes of them in the matrix) on their way into `buf`, which nothing waits for
+// here; and each lane's row from there.
+constexpr int kFetchBytes = 32 * 128;
+constexpr int kFetches = 2;                            // of a warp, ahead of the one it adds
+__device__ __forceinline__ void fetch_rows(uint8_t* buf, const uint8_t* in, int64_t pitch, int rows, int chunks) {
+  const int lane = threadIdx.x & 31, c = lane & 7;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int r = 4 * k + (lane >> 3);
+    if (r < rows && c < chunks)
+      ptx::copy_async_16(ptx::smem_u32(buf) + r * 128 + ((c ^ (r & 7)) << 4), in + r * pitch + 16 * c);
+  }
+}
+__device__ __forceinline__ void fetched_row(const uint8_t* buf, uint32_t (&w)[32]) {
   const int lane = threadIdx.x & 31;
-  if (lane == 0) ptx::bulk_wait_read<0>();
-  __syncwarp();
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int r = 4 * k + (lane >> 3), c = lane & 7;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (16 * h + r < rows && c < chunks) v = *reinterpret_cast<const uint4*>(in + (16 * h + r) * pitch + 16 * c);
-      *reinterpret_cast<uint4*>(stage + r * 128 + ((c ^ (r & 7)) << 4)) = v;
-    }
-    __syncwarp();
-    if ((lane >> 4) == h) {
-#pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        const uint4 v = *reinterpret_cast<const uint4*>(stage + (lane & 15) * 128 + ((c ^ (lane & 7)) << 4));
-        w[4 * c] = v.x; w[4 * c + 1] = v.y; w[4 * c + 2] = v.z; w[4 * c + 3] = v.w;
-      }
-    }
-    __syncwarp();
+  for (int c = 0; c < 8; ++c) {
+    const uint4 v = *reinterpret_cast<const uint4*>(buf + lane * 128 + ((c ^ (lane & 7)) << 4));
+    w[4 * c] = v.x; w[4 * c + 1] = v.y; w[4 * c + 2] = v.z; w[4 * c + 3] = v.w;
   }
 }
 
 // One chunk of a weight gradient's rows from the accumulator at `taddr`: 64
-// columns to bf16, or 32 to fp32.  `last`: then hands the accumulator back.
+// columns to bf16, or 32 to fp32; kAccumulate: added to `w`, what is there.  `last`: then
+// hands the accumulator back.
 template <bool kBf16, bool kAccumulate, typename Release>
-__device__ __forceinline__ void put_chunk(const ExpertArgs& p, const CUtensorMap* map, uint8_t* stage, uint32_t taddr,
-                                          int x, int y, int z, int rows, int cols, uint32_t& parts, bool add,
-                                          bool last, Release release) {
-  constexpr int kEsz = kBf16 ? 2 : 4;
-  uint32_t w[32], acc[32];
-  if (kAccumulate && !add)
-    get_rows(stage, w, static_cast<const uint8_t*>(p.out) + (z * p.out_stride + y * p.out_ld + x) * kEsz,
-             p.out_ld * kEsz, rows, min(8, cols * kEsz / 16));
+__device__ __forceinline__ void put_chunk(const CUtensorMap* map, uint8_t* stage, uint32_t (&w)[32], uint32_t taddr,
+                                          int x, int y, int z, int rows, uint32_t& parts, bool add, bool last,
+                                          Release release) {
+  uint32_t acc[32];
 #pragma unroll
   for (int h = 0; h < (kBf16 ? 2 : 1); ++h) {
     ptx::tmem_ld_32x32b_x32(taddr + 32 * h, acc);
@@ -495,7 +490,10 @@ __device__ __forceinline__ void put_tokens(const ExpertArgs& p, const CUtensorMa
 }
 
 // kBf16: the output's type.  kVec: its rows start on 16-byte boundaries.
-// kAccumulate: weight gradient.
+// kAccumulate: a weight gradient that adds to what is there, fetched while the products
+// run, at the price of two stages.  (128 x 1408 x 2048, 32768 tokens, us: bf16 300, fp32
+// 463, floors 250 and 468; with loads where the sum is made 452 and 810; tensor copies that
+// add in fp32 545.)
 template <int kMode, bool kBf16, bool kAccumulate, bool kVec>
 __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_constant__ ExpertArgs p,
                                                              const __grid_constant__ Maps maps) {
@@ -594,7 +592,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
   // Shared memory of a stage: A, then this CTA's half of B.
   const int wide = kWgrad ? sh.width_n : widest;
   const uint32_t stage_bytes = kBytesA + (kWgrad ? ceil_div(wide / 2, 64) * kMnBlock : rows_b(wide / 2) * 128);
-  const int stages = min(kMaxStages, kRingBytes(kMode) / (int)stage_bytes);
+  const int stages = min(kMaxStages, kRingBytes(kMode, kAccumulate) / (int)stage_bytes);
 
   if (warp == 0) {
     // -------------------------------------------------------------- producer
@@ -743,16 +741,50 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
     // Warp w reads TMEM lane quadrant w % 4; the two warps of a quadrant take
     // alternate chunks of 32 columns.
     const int quad = warp & 3, half = (warp - kFirstEpiWarp) >> 2;
-    uint8_t* const stage = smem_raw + (smem_base - ptx::smem_u32(smem_raw)) + kRingBytes(kMode) +
+    uint8_t* const stage = smem_raw + (smem_base - ptx::smem_u32(smem_raw)) + kRingBytes(kMode, kAccumulate) +
                            (warp - kFirstEpiWarp) * 2 * kPartBytes(kMode);
     constexpr int kEsz = kBf16 ? 2 : 4;
     constexpr int kWidth = kWgrad && kVec ? 128 / kEsz : 32;     // columns of a chunk
     uint32_t acc_it = 0, parts = 0;
+    // With kAccumulate what the output holds is fetched ahead, chunk by chunk in the order
+    // in which they are added to, from the coming tiles too.
+    struct Fetch {
+      Tile tl;
+      int c;
+      bool more;
+      uint32_t made, taken;
+    } fetch;
+    uint8_t* const fetch_buf = smem_raw + (smem_base - ptx::smem_u32(smem_raw)) + kRingBytes(kMode, kAccumulate) +
+                               kEpiWarps * 2 * kPartBytes(kMode) + (warp - kFirstEpiWarp) * kFetches * kFetchBytes;
+    TileWalk<kMode, !kBf16> ahead = walk;
+    auto fetch_next = [&]() {
+      fetch.c += 2 * kWidth;
+      while (fetch.more && fetch.c >= fetch.tl.n_mma) {
+        do fetch.more = ahead.next(fetch.tl);
+        while (fetch.more && (fetch.tl.k_len == 0 || fetch.tl.k_from > 0));
+        fetch.c = kWidth * half;
+      }
+      if (fetch.more) {
+        const int y = fetch.tl.m0 + (int)rank * kCtaM + quad * 32, x = fetch.tl.n0 + fetch.c;
+        fetch_rows(fetch_buf + (fetch.made & 1) * kFetchBytes,
+                   static_cast<const uint8_t*>(p.out) + (fetch.tl.z * p.out_stride + y * p.out_ld + x) * kEsz,
+                   p.out_ld * kEsz, sh.m - y, min(8, (fetch.tl.n - fetch.c) * kEsz / 16));
+      }
+      ptx::copy_async_commit();
+      ++fetch.made;
+    };
+    if constexpr (kAccumulate && kVec) {
+      fetch.tl.n_mma = 0;
+      fetch.c = 0;
+      fetch.more = true;
+      fetch.made = fetch.taken = 0;
+      for (int k = 0; k < kFetches; ++k) fetch_next();
+    }
     while (walk.next(tl)) {
       const int row0 = tl.m0 + (int)rank * kCtaM + quad * 32;
       const int64_t at0 = kWgrad ? tl.z * p.out_stride + row0 * p.out_ld + tl.n0 : 0;      // the warp's first row
       if (kWgrad && tl.k_len == 0) {
-        if (kAccumulate) continue;
+        if (p.accumulate) continue;
         uint32_t z[32];
 #pragma unroll
         for (int j = 0; j < 32; ++j) z[j] = 0;
@@ -777,7 +809,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
       };
       if (kWidth * half >= tl.n_mma) release();           // no chunk for this warp
       const bool add = !kBf16 && tl.k_from > 0;
-      if (kVec && add) {                                   // what is added to is there
+      if (kVec && !kBf16 && tl.k_from > 0) {               // what the last turn wrote is there
         if (lane == 0) ptx::bulk_wait_all();
         __syncwarp();
       }
@@ -785,8 +817,16 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
         const bool last = c + 2 * kWidth >= tl.n_mma;
         __syncwarp();
         if constexpr (kWgrad && kVec) {
-          put_chunk<kBf16, kAccumulate>(p, &maps.out, stage, t_row + c, tl.n0 + c, row0, tl.z, sh.m - row0, tl.n - c,
-                                        parts, add, last, release);
+          uint32_t w[32];
+          if (kAccumulate && !add) {
+            ptx::copy_async_wait<kFetches - 1>();
+            __syncwarp();
+            fetched_row(fetch_buf + (fetch.taken++ & 1) * kFetchBytes, w);
+            __syncwarp();
+            fetch_next();
+          }
+          put_chunk<kBf16, kAccumulate>(&maps.out, stage, w, t_row + c, tl.n0 + c, row0, tl.z, sh.m - row0, parts, add,
+                                        last, release);
           continue;
         }
         uint32_t r[32];
@@ -1099,7 +1139,8 @@ bool encode(CUtensorMap* map, const void* base, int64_t width, int64_t height, i
 
 template <int kMode, bool kBf16, bool kAccumulate, bool kVec>
 cudaError_t launch_kernel(const ExpertArgs& a, const Maps& maps, int64_t max_tiles, cudaStream_t s) {
-  constexpr size_t kSmemBytes = kRingBytes(kMode) + kEpiWarps * 2 * kPartBytes(kMode) + 1024;
+  constexpr size_t kSmemBytes = kRingBytes(kMode, kAccumulate) + kEpiWarps * 2 * kPartBytes(kMode) +
+                                (kAccumulate ? kEpiWarps * kFetches * kFetchBytes : 0) + 1024;
   const auto kernel = expert_kernel<kMode, kBf16, kAccumulate, kVec>;
   static std::mutex mu;
   static int resident[kMaxDevices] = {};      // CTA pairs on the device at once
