@@ -658,12 +658,14 @@ __global__ void __launch_bounds__(32 * kFixParts) embed_fix_kernel(const __grid_
   }
 }
 
-// Few ids: one launch, no sort.  A CTA takes a share of the vocabulary's rows and
-// 256 of the columns, reads all ids, lists those of its share in order, and
-// writes its rows: zeros, or the sum of a row's positions in ascending order,
-// one row a warp.  A row with many positions is added by the eight warps, an
-// eighth of them each.  (257 ids of 768 columns: 17 us a call through the sort and two more
-// launches.)
+// Few ids: one launch, no sort.  A CTA takes a share of the vocabulary's rows and 256
+// of the columns, reads all ids, lists those of its share in order, and writes its
+// rows: the sum of a row's positions in ascending order, one row a warp, or zeros.  A row
+// with many positions is added by the eight warps, an eighth of them each, and goes
+// first.  Bound by latency (ids, positions, rows, stores: 3 us for 64 ids of 256 columns)
+// or by writing zeros.  Through the sort and two more launches 257 ids of 768 columns take
+// 17 us, this way 9; 512 ids of 1024 into 32000 rows 25 and 25 (added: 14 and 6), all
+// of one token 27 and 45; 1024 of one token would take longer still.
 constexpr int kSmallIds = 512;
 constexpr int kSmallShare = 2048;          // rows of a share, at most: its bitmap
 constexpr int kSmallWarps = 8;
@@ -671,12 +673,13 @@ constexpr int kSmallCols = 32 * kCols;
 constexpr int kSmallRow = 32;              // positions of a row that one warp adds
 
 template <bool kInBf16, bool kOutBf16, bool kVec>
-__global__ void __launch_bounds__(32 * kSmallWarps) embed_small_kernel(const __grid_constant__ EmbedGradArgs a) {
+__global__ void __launch_bounds__(32 * kSmallWarps, kVec ? 4 : 3) embed_small_kernel(const __grid_constant__ EmbedGradArgs a) {
   __shared__ int16_t pos[kSmallIds], row[kSmallIds];      // listed positions, and their rows in the share
   __shared__ uint32_t named[kSmallShare / 32];
   __shared__ int warp_count[kSmallWarps];
   __shared__ float sums[kSmallWarps][kSmallCols];
-  constexpr int kAhead = 4;                               // rows in flight
+  __shared__ int16_t own[kSmallWarps][kSmallIds / kSmallWarps];    // positions that a warp adds
+  constexpr int kAhead = 4;         // rows in flight
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t c0 = (int64_t)blockIdx.y * kSmallCols;
   const int cols = (int)min((int64_t)kSmallCols, a.dim - c0);
@@ -714,39 +717,33 @@ __global__ void __launch_bounds__(32 * kSmallWarps) embed_small_kernel(const __g
   // adds the positions of row r from the first-th to the last-th
   float acc[kCols];
   auto add_positions = [&](int r, int first, int last) {
-#pragma unroll
-    for (int k = 0; k < kCols; ++k) acc[k] = 0.f;
     int seen = 0;
     for (int base = 0; base < count && seen < last; base += 32) {
-      unsigned mask = __ballot_sync(0xffffffffu, base + lane < count && row[base + lane] == r);
-      const int here = __popc(mask);
-      if (seen + here <= first) {
-        seen += here;
-        continue;
-      }
-      while (mask && seen < last) {
-        Row8<kInBf16, kVec> x[kAhead];
-        bool got[kAhead];
+      const bool in = base + lane < count && row[base + lane] == r;
+      const unsigned mask = __ballot_sync(0xffffffffu, in);
+      const int nth = seen + __popc(mask & ((1u << lane) - 1));
+      if (in && nth >= first && nth < last) own[warp][nth - first] = pos[base + lane];
+      seen += __popc(mask);
+    }
+    __syncwarp();
+    const int n = min(seen, last) - first;
 #pragma unroll
-        for (int b = 0; b < kAhead; ++b) {
-          got[b] = false;
-          if (!mask) continue;
-          const int l = __ffs(mask) - 1;
-          mask &= mask - 1;
-          got[b] = seen >= first && seen < last;
-          ++seen;
-          if (got[b]) x[b].load(a.dout, (int64_t)pos[base + l] * a.dout_ld + c0, lane, 32, cols);
-        }
+    for (int k = 0; k < kCols; ++k) acc[k] = 0.f;
+    for (int i = 0; i < n; i += kAhead) {
+      Row8<kInBf16, kVec> x[kAhead];
 #pragma unroll
-        for (int b = 0; b < kAhead; ++b) {
-          if (!got[b]) continue;
-          float v[8];
-          x[b].get(v);
+      for (int b = 0; b < kAhead; ++b)
+        if (i + b < n) x[b].load(a.dout, (int64_t)own[warp][i + b] * a.dout_ld + c0, lane, 32, cols);
 #pragma unroll
-          for (int k = 0; k < kCols; ++k) acc[k] = fmaf(a.scale, v[k], acc[k]);
-        }
+      for (int b = 0; b < kAhead; ++b) {
+        if (i + b >= n) break;
+        float v[8];
+        x[b].get(v);
+#pragma unroll
+        for (int k = 0; k < kCols; ++k) acc[k] = fmaf(a.scale, v[k], acc[k]);
       }
     }
+    __syncwarp();
   };
   auto put = [&](int r) {
     const int64_t at = (r0 + r) * a.grad_ld + c0;
@@ -767,36 +764,43 @@ __global__ void __launch_bounds__(32 * kSmallWarps) embed_small_kernel(const __g
     return m;
   };
 
-  // rows of a few positions and of none, a warp each
-  for (int r = warp; r < len; r += kSmallWarps) {
-    if (named[r >> 5] >> (r & 31) & 1) {
-      if (count > kSmallRow && positions_of(r) > kSmallRow) continue;
-      add_positions(r, 0, kSmallIds);
-      put(r);
-    } else if (!a.accumulate) {
+  // Rows of many positions, one at a time, first: theirs is the longest way.
+  const int words = (len + 31) / 32;
+  if (count > kSmallRow)
+    for (int w = 0; w < words; ++w)
+      for (uint32_t bits = named[w]; bits; bits &= bits - 1) {
+        const int r = 32 * w + __ffs(bits) - 1, m = positions_of(r);
+        if (m <= kSmallRow) continue;
+        add_positions(r, m * warp / kSmallWarps, m * (warp + 1) / kSmallWarps);
+        __syncthreads();
 #pragma unroll
-      for (int k = 0; k < kCols; ++k) acc[k] = 0.f;
-      store8<kOutBf16, kVec>(a.grad, (r0 + r) * a.grad_ld + c0, lane, 32, cols, acc);
-    }
-  }
-  if (count <= kSmallRow) return;
-  // rows of many positions, one at a time
-  for (int w = 0; w < (len + 31) / 32; ++w)
+        for (int k = 0; k < kCols; ++k) sums[warp][32 * k + lane] = acc[k];
+        __syncthreads();
+        if (warp != 0) continue;
+#pragma unroll
+        for (int q = 1; q < kSmallWarps; ++q)
+#pragma unroll
+          for (int k = 0; k < kCols; ++k) acc[k] += sums[q][32 * k + lane];
+        put(r);
+      }
+  // rows of a few, a warp each
+  int turn = warp;
+  for (int w = 0; w < words; ++w)
     for (uint32_t bits = named[w]; bits; bits &= bits - 1) {
-      const int r = 32 * w + __ffs(bits) - 1, m = positions_of(r);
-      if (m <= kSmallRow) continue;
-      add_positions(r, m * warp / kSmallWarps, m * (warp + 1) / kSmallWarps);
-      __syncthreads();
-#pragma unroll
-      for (int k = 0; k < kCols; ++k) sums[warp][32 * k + lane] = acc[k];
-      __syncthreads();
-      if (warp != 0) continue;
-#pragma unroll
-      for (int q = 1; q < kSmallWarps; ++q)
-#pragma unroll
-        for (int k = 0; k < kCols; ++k) acc[k] += sums[q][32 * k + lane];
+      if (turn-- > 0) continue;
+      turn = kSmallWarps - 1;
+      const int r = 32 * w + __ffs(bits) - 1;
+      if (count > kSmallRow && positions_of(r) > kSmallRow) continue;
+      add_positions(r, 0, kSmallRow);
       put(r);
     }
+  // rows of none
+  if (a.accumulate) return;
+#pragma unroll
+  for (int k = 0; k < kCols; ++k) acc[k] = 0.f;
+  for (int r = warp; r < len; r += kSmallWarps)
+    if (!(named[r >> 5] >> (r & 31) & 1))
+      store8<kOutBf16, kVec>(a.grad, (r0 + r) * a.grad_ld + c0, lane, 32, cols, acc);
 }
 
 // Rows of a tensor start on the vector's boundary: 16 bytes of bf16, 32 of fp32.
