@@ -126,6 +126,8 @@ __device__ __forceinline__ void store8(void* base, int64_t at, int tid, int thre
 }
 
 // ---------------------------------------------------------------------- lookup
+// 32768 rows of 2048, fp32 to bf16, with a text's frequencies: 37 us, bound by L2 (402 MB
+// in and out of the SMs, 11 TB/s; 150 MB of DRAM).  One row: 1.5 us.
 constexpr int kLookupRows = 4;             // rows of a thread, all loaded before the first store
 
 template <bool kWBf16, bool kOutBf16, bool kVec>

@@ -18,6 +18,9 @@
 // root in every thread, the second launch spent 4 us a CTA on them.  One warp
 // adds the partials, and one thread works out the coefficient.
 //
+// 872 M bf16 elements in 28 matrices: 783 us, 240 for the first launch (7.3 TB/s) and 533
+// for the second (6.4 TB/s, half of it writes).  135 k fp32 elements: 5.3 us.
+//
 // Bound by HBM (by launches, for a small set).  A chunk is 32 KB of one tensor,
 // eight 16-byte loads a thread, all issued before the first is used; a tensor
 // may start at any element, its chunks start at its first 16-byte boundary.

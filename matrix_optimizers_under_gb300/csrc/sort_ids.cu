@@ -14,7 +14,7 @@
 // Up to 65536 ids are sorted by one cluster of up to 8 CTAs in one launch: the
 // pairs stay in shared memory, the counts and the moves go through distributed
 // shared memory.  The work is latency, not bandwidth (32768 ids are 256 KB): two passes
-// as separate launches took 36 us with cold caches.  More ids take two launches a
+// as separate launches took 36 us with cold caches, so 13.  More ids take two launches a
 // pass, on up to kMaxTiles CTAs.
 #include <atomic>
 
