@@ -823,10 +823,17 @@ int64_t small_shares(int64_t vocab, int64_t dim) {
 }
 
 template <bool kIn, bool kOut>
-cudaError_t small_launch(const EmbedGradArgs& a, bool vec, cudaStream_t s) {
-  const dim3 grid((unsigned)small_shares(a.vocab, a.dim), (unsigned)((a.dim + kSmallCols - 1) / kSmallCols));
-  if (vec) embed_small_kernel<kIn, kOut, true><<<grid, 32 * kSmallWarps, 0, s>>>(a);
-  else embed_small_kernel<kIn, kOut, false><<<grid, 32 * kSmallWarps, 0, s>>>(a);
+cudaError_t small_launch(const EmbedGradArgs& all, bool vec, cudaStream_t s) {
+  constexpr int64_t kMost = (int64_t)65535 * kSmallCols;      // columns of a launch
+  for (int64_t c = 0; c < all.dim; c += kMost) {
+    EmbedGradArgs a = all;
+    a.dim = std::min(kMost, all.dim - c);
+    a.dout = static_cast<const uint8_t*>(all.dout) + c * (kIn ? 2 : 4);
+    a.grad = static_cast<uint8_t*>(all.grad) + c * (kOut ? 2 : 4);
+    const dim3 grid((unsigned)small_shares(a.vocab, a.dim), (unsigned)((a.dim + kSmallCols - 1) / kSmallCols));
+    if (vec) embed_small_kernel<kIn, kOut, true><<<grid, 32 * kSmallWarps, 0, s>>>(a);
+    else embed_small_kernel<kIn, kOut, false><<<grid, 32 * kSmallWarps, 0, s>>>(a);
+  }
   return cudaGetLastError();
 }
 

@@ -54,6 +54,22 @@ def test_embedding(mfsdp):
         within(grad[v], want, (len(rows) + 5) * U * mag + H * want.abs(), f"row {v}")
 
 
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_embedding_of_the_widest_rows(mfsdp, accumulate):
+    dim = 1 << 24
+    g = torch.Generator(device="cuda").manual_seed(9)
+    ids = torch.tensor([1, 4, 1], device="cuda")
+    w, dout = torch.randn(5, dim, generator=g, device="cuda"), torch.randn(3, dim, generator=g, device="cuda")
+    out = torch.empty(3, dim, device="cuda")
+    mfsdp.embedding_lookup(w, ids, out)
+    assert torch.equal(out, w[ids])
+    ws = scratch(mfsdp.embedding_grad_workspace_bytes(3, 5, dim))
+    want = (w.double() if accumulate else torch.zeros_like(w, dtype=torch.float64)).index_add(0, ids, dout.double())
+    mag = (w.abs().double() if accumulate else torch.zeros_like(w, dtype=torch.float64)).index_add(0, ids, dout.abs().double())
+    mfsdp.embedding_grad(dout, ids, w, ws, accumulate=accumulate)
+    within(w, want, 6 * U * mag, "gradient")
+
+
 def test_clip(mfsdp):
     n = ROWS * DIM + 5
     flat = torch.empty(n, dtype=torch.bfloat16, device="cuda").normal_(generator=torch.Generator(device="cuda").manual_seed(3))
