@@ -666,9 +666,11 @@ __global__ void __launch_bounds__(32 * kFixParts) embed_fix_kernel(const __grid_
 // with many positions is added by the eight warps, an eighth of them each, and goes
 // first.  Bound by latency (ids, positions, rows, stores: 3 us for 64 ids of 256 columns)
 // or by writing zeros.  Through the sort and two more launches 257 ids of 768 columns take
-// 17 us, this way 9; 512 ids of 1024 into 32000 rows 25 and 25 (added: 14 and 6), all
-// of one token 27 and 45; 1024 of one token would take longer still.
-constexpr int kSmallIds = 512;
+// 17 us, this way 9; 1024 ids of a text, 256 columns, into 1000 rows 16 and 8; 1024
+// columns into 32000 rows 28 and 31 (added: 16 and 11); 2048 columns into 5000 17
+// and 14.  1024 of one token take 19 to 34 and 23 to 63.  800 ids of 375 columns, which
+// no vector meets: 19 and 21.
+constexpr int kSmallIds = 1024;            // half of it for rows off the vectors' boundaries
 constexpr int kSmallShare = 2048;          // rows of a share, at most: its bitmap
 constexpr int kSmallWarps = 8;
 constexpr int kSmallCols = 32 * kCols;
@@ -899,11 +901,15 @@ size_t embed_grad_partial_bytes(int64_t n, int64_t vocab, int64_t dim) {
   return round_up(sp.slabs * sizeof(CutRow), 256) + (size_t)sp.slabs * 2 * round_up((size_t)dim, 8) * sizeof(float);
 }
 
-bool embed_grad_sorts(int64_t n) { return n > kSmallIds; }
+bool embed_grad_vec(const EmbedGradArgs& a) {
+  return vec_rows(a.dout, a.dout_ld, a.dim, a.dout_bf16) && vec_rows(a.grad, a.grad_ld, a.dim, a.grad_bf16);
+}
+
+bool embed_grad_sorts(const EmbedGradArgs& a) { return a.n > (embed_grad_vec(a) ? kSmallIds : kSmallIds / 2); }
 
 cudaError_t launch_embed_grad(const EmbedGradArgs& a, cudaStream_t s) {
-  const bool vec = vec_rows(a.dout, a.dout_ld, a.dim, a.dout_bf16) && vec_rows(a.grad, a.grad_ld, a.dim, a.grad_bf16);
-  if (!embed_grad_sorts(a.n))
+  const bool vec = embed_grad_vec(a);
+  if (!embed_grad_sorts(a))
     return a.dout_bf16 ? (a.grad_bf16 ? small_launch<true, true>(a, vec, s) : small_launch<true, false>(a, vec, s))
                        : (a.grad_bf16 ? small_launch<false, true>(a, vec, s) : small_launch<false, false>(a, vec, s));
   const SlabPlan sp = plan_slabs(a.n, a.vocab, a.dim);

@@ -420,7 +420,7 @@ extern "C" int mfsdp_embedding_grad(const void* dout, int32_t dout_dtype, int64_
   a.scale = (float)scale;
   a.header = s.zero = reinterpret_cast<int32_t*>(ws);
   const OpRange range("mfsdp embedding gradient");
-  cudaError_t e = embed_grad_sorts(n) ? launch_sort(s, stream) : cudaSuccess;
+  cudaError_t e = embed_grad_sorts(a) ? launch_sort(s, stream) : cudaSuccess;
   if (e == cudaSuccess) e = launch_embed_grad(a, stream);
   return cuda_status(e);
 }

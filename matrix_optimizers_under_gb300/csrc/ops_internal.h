@@ -122,8 +122,8 @@ struct EmbedGradArgs {
   float scale;
 };
 size_t embed_grad_partial_bytes(int64_t n, int64_t vocab, int64_t dim);
-// Whether the gradient of n ids takes them sorted (few it takes as they are).
-bool embed_grad_sorts(int64_t n);
+// Whether the gradient takes the ids sorted (few it takes as they are).
+bool embed_grad_sorts(const EmbedGradArgs& a);
 cudaError_t launch_embed_grad(const EmbedGradArgs& a, cudaStream_t s);
 
 // --------------------------------------------- products grouped by expert

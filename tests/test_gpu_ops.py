@@ -246,7 +246,8 @@ def test_embedding_grad(mfsdp, dout, grad, n, vocab, dim, kind, extra, accumulat
 @pytest.mark.parametrize("n,vocab,dim,kind", [(512, 3, 300, "one"), (513, 900, 264, "zipf"), (480, 5, 520, "uniform"),
                                               (200, 1_500_000, 8, "uniform"), (65_537, 30_000, 48, "zipf"),
                                               (90_000, 70_000, 17, "uniform"), (600, 1_300_000, 8, "uniform"),
-                                              (6000, 4000, 1100, "uniform"), (2500, 9, 2048, "zipf")])
+                                              (6000, 4000, 1100, "uniform"), (2500, 9, 2048, "zipf"),
+                                              (1024, 3, 264, "one"), (1025, 700, 264, "zipf"), (1000, 1, 8, "one")])
 @pytest.mark.parametrize("extra,accumulate", [(0, False), (0, True), (3, True)])
 def test_embedding_grad_lengths(mfsdp, dout, grad, n, vocab, dim, kind, extra, accumulate):
     """Few ids and many, few rows and many, on both sides of where the launches change."""
