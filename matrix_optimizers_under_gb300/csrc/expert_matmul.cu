@@ -962,10 +962,29 @@ struct PrepareArgs {
 };
 constexpr int kPrepareThreads = 256;
 
-// 8 elements from column c of a row of `width`, zero past it.
+// 8 elements from column c of a row of `width`, zero past it.  Inside a row that does not
+// start on a 16-byte boundary (not `vec`) they come out of the two 16-byte words that hold
+// them, which lie in the row; at its ends one by one.  (30776 x 1097 copied and multiplied:
+// 48 us with single elements everywhere, 42 so.)
 __device__ __forceinline__ uint4 load8(const uint16_t* row, int c, int width, bool vec) {
   if (vec) return *reinterpret_cast<const uint4*>(row + c);
-  uint32_t w[4];
+  uint32_t w[8];
+  if (c >= 8 && c + 16 <= width) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(row + c);
+    const uint4* const words = reinterpret_cast<const uint4*>(at & ~(uintptr_t)15);
+    const uint4 a = words[0], b = words[1];
+    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+    w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+    const bool by1 = at & 4, by2 = at & 8;
+#pragma unroll
+    for (int k = 0; k < 7; ++k) w[k] = by1 ? w[k + 1] : w[k];
+#pragma unroll
+    for (int k = 0; k < 5; ++k) w[k] = by2 ? w[k + 2] : w[k];
+    const uint32_t shift = at & 2 ? 16 : 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] = __funnelshift_r(w[k], w[k + 1], shift);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const uint32_t x = c + 2 * k < width ? row[c + 2 * k] : 0, y = c + 2 * k + 1 < width ? row[c + 2 * k + 1] : 0;
