@@ -195,7 +195,8 @@ SlabPlan plan_slabs(int64_t n, int64_t vocab, int64_t dim) {
   return s;
 }
 
-// A row cut by slab ends: the slabs its positions start and end in.
+// A row cut by slab ends: the slabs its positions start and end in.  It stands in
+// the place of its last slab; the places of other slabs have no row.
 struct CutRow {
   int32_t row, first, last;
 };
@@ -204,8 +205,8 @@ struct GradKernelArgs {
   EmbedGradArgs a;
   int64_t slab;
   int64_t part_ld;     // floats of a partial row
-  int32_t* n_cut;      // how many `cut` holds (zeroed by the sort)
-  CutRow* cut;         // in no fixed order: each is added by itself
+  int64_t slabs;
+  CutRow* cut;         // a place for each slab
   int32_t* status;     // first wait that gave up (0: none)
   int32_t threads;     // that add rows (the kernel may have more, which only look for unnamed rows)
   int32_t batch, stages, zero_bytes;   // rows of a batch, stages of the ring, bytes before it
@@ -311,14 +312,18 @@ __device__ __forceinline__ Slab slab_of(const GradKernelArgs& p, int64_t s) {
   return r;
 }
 
-// Notes a row that began in an earlier slab and ends in this one (whole warp).
+// Notes, in the slab's place, the row that began in an earlier slab and ends in this one, or
+// that there is none (whole warp).
 __device__ __forceinline__ void note_cut(const GradKernelArgs& p, const Slab& sl, int64_t s) {
   const EmbedGradArgs& a = p.a;
-  if (!sl.began) return;
-  const int32_t v = a.keys[sl.i0];
-  if (v >= a.vocab || (sl.goes_on && a.keys[sl.i1 - 1] == v)) return;
-  const int64_t first = warp_lower_bound(a.keys, sl.i0, v) / p.slab;
-  if ((threadIdx.x & 31) == 0) p.cut[atomicAdd(p.n_cut, 1)] = {v, (int32_t)first, (int32_t)s};
+  if (sl.i0 >= a.n) return;
+  CutRow cut = {-1, 0, (int32_t)s};
+  if (sl.began) {
+    const int32_t v = a.keys[sl.i0];
+    if (v < a.vocab && !(sl.goes_on && a.keys[sl.i1 - 1] == v))
+      cut = {v, (int32_t)(warp_lower_bound(a.keys, sl.i0, v) / p.slab), (int32_t)s};
+  }
+  if ((threadIdx.x & 31) == 0) p.cut[s] = cut;
 }
 
 // A row's sum leaves the slab: into dW, with accumulate added to what it holds
@@ -629,34 +634,48 @@ __global__ void __launch_bounds__(32 * kFixParts) embed_fix_kernel(const __grid_
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int blocks = (int)((a.dim + kFixCols - 1) / kFixCols);
   ptx::wait_dependencies();
-  const int64_t items = (int64_t)*p.n_cut * blocks;
-  for (int64_t it = (int64_t)warp * gridDim.x + blockIdx.x; it < items; it += (int64_t)kFixParts * gridDim.x) {
-    const CutRow cut = p.cut[it / blocks];
-    if (cut.last - cut.first >= kShortCut) continue;
-    const int64_t c = it % blocks * kFixCols + 4 * lane;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (c < p.part_ld) add_parts(p, cut, cut.first, cut.last + 1, c, acc);
-    store_fix<kOutBf16>(a, cut.row, c, acc);
-  }
-  for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-    const CutRow cut = p.cut[it / blocks];
-    if (cut.last - cut.first < kShortCut) continue;
-    const int64_t c = it % blocks * kFixCols + 4 * lane;
-    const int64_t slabs = cut.last - cut.first + 1;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (c < p.part_ld)
-      add_parts(p, cut, cut.first + (int)(slabs * warp / kFixParts),
-                cut.first + (int)(slabs * (warp + 1) / kFixParts), c, acc);
-    __syncthreads();
-    sum[warp][lane] = acc;
-    __syncthreads();
-    if (warp != 0) continue;
-#pragma unroll
-    for (int w = 1; w < kFixParts; ++w) {
-      const float4 x = sum[w][lane];
-      acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
+  const int64_t items = p.slabs * blocks;
+  // 32 items a look, one a lane: most places have no row
+  const int64_t step = (int64_t)kFixParts * gridDim.x;
+  for (int64_t at = (int64_t)warp * gridDim.x + blockIdx.x; at < items; at += 32 * step) {
+    CutRow mine = {-1, 0, 0};
+    if (at + lane * step < items) mine = p.cut[(at + lane * step) / blocks];
+    unsigned found = __ballot_sync(0xffffffffu, mine.row >= 0 && mine.last - mine.first < kShortCut);
+    for (; found; found &= found - 1) {
+      const int k = __ffs(found) - 1;
+      const CutRow cut = {__shfl_sync(0xffffffffu, mine.row, k), __shfl_sync(0xffffffffu, mine.first, k),
+                          __shfl_sync(0xffffffffu, mine.last, k)};
+      const int64_t c = (at + k * step) % blocks * kFixCols + 4 * lane;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (c < p.part_ld) add_parts(p, cut, cut.first, cut.last + 1, c, acc);
+      store_fix<kOutBf16>(a, cut.row, c, acc);
     }
-    store_fix<kOutBf16>(a, cut.row, c, acc);
+  }
+  for (int64_t at = blockIdx.x; at < items; at += 32 * (int64_t)gridDim.x) {
+    CutRow mine = {-1, 0, 0};
+    if (at + lane * (int64_t)gridDim.x < items) mine = p.cut[(at + lane * (int64_t)gridDim.x) / blocks];
+    unsigned found = __ballot_sync(0xffffffffu, mine.row >= 0 && mine.last - mine.first >= kShortCut);
+    for (; found; found &= found - 1) {                // the same in every warp
+      const int k = __ffs(found) - 1;
+      const CutRow cut = {__shfl_sync(0xffffffffu, mine.row, k), __shfl_sync(0xffffffffu, mine.first, k),
+                          __shfl_sync(0xffffffffu, mine.last, k)};
+      const int64_t c = (at + k * (int64_t)gridDim.x) % blocks * kFixCols + 4 * lane;
+      const int64_t slabs = cut.last - cut.first + 1;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (c < p.part_ld)
+        add_parts(p, cut, cut.first + (int)(slabs * warp / kFixParts),
+                  cut.first + (int)(slabs * (warp + 1) / kFixParts), c, acc);
+      __syncthreads();
+      sum[warp][lane] = acc;
+      __syncthreads();
+      if (warp != 0) continue;
+#pragma unroll
+      for (int w = 1; w < kFixParts; ++w) {
+        const float4 x = sum[w][lane];
+        acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
+      }
+      store_fix<kOutBf16>(a, cut.row, c, acc);
+    }
   }
 }
 
@@ -690,7 +709,7 @@ __global__ void __launch_bounds__(32 * kSmallWarps, kVec ? 4 : 3) embed_small_ke
   const int64_t share = (a.vocab + gridDim.x - 1) / gridDim.x;
   const int64_t r0 = blockIdx.x * share;
   const int len = (int)max((int64_t)0, min(share, a.vocab - r0));
-  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 2) a.header[threadIdx.x] = 0;
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *a.header = 0;
   for (int i = threadIdx.x; i < (len + 31) / 32; i += blockDim.x) named[i] = 0;
   __syncthreads();
   int count = 0;
@@ -919,7 +938,7 @@ cudaError_t launch_embed_grad(const EmbedGradArgs& a, cudaStream_t s) {
   p.part_ld = (int64_t)round_up((size_t)a.dim, 8);
   uint8_t* at = reinterpret_cast<uint8_t*>(a.partials);
   p.status = a.header;
-  p.n_cut = a.header + 1;
+  p.slabs = sp.slabs;
   p.cut = reinterpret_cast<CutRow*>(at);
   p.parts = reinterpret_cast<float*>(at + round_up(sp.slabs * sizeof(CutRow), 256));
   const cudaError_t e = a.dout_bf16 ? (a.grad_bf16 ? grad_launch<true, true>(p, sp.ctas, vec, s)

@@ -91,7 +91,7 @@ struct SortArgs {
   int32_t* keys_out;     // sorted keys [n]
   int32_t* order_out;    // the position each came from [n]
   void* scratch;         // sort_scratch_bytes(n, n_keys)
-  int32_t* zero;         // two words the sort sets to 0 (may be null)
+  int32_t* zero;         // a word the sort sets to 0 (may be null)
 };
 size_t sort_scratch_bytes(int64_t n, int64_t n_keys);
 constexpr int kSortSms = 8;            // SMs that a sort of few ids takes
@@ -116,7 +116,7 @@ struct EmbedGradArgs {
   const int32_t* keys;   // sorted
   const int32_t* order;
   float* partials;       // embed_grad_partial_bytes(n, vocab, dim)
-  int32_t* header;       // two words, zeroed before: status, a counter
+  int32_t* header;       // the status word, zeroed before
   int64_t n, vocab, dim, dout_ld, grad_ld;
   int32_t dout_bf16, grad_bf16, accumulate, ids64;
   float scale;

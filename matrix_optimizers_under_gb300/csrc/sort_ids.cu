@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) sort_cluster_kernel(const 
   const int rank = blockIdx.x, ctas = gridDim.x;                             // the grid is one cluster
   const int tile = a.steps * kClusterThreads;
   ptx::launch_dependents();
-  if (rank == 0 && threadIdx.x < 2 && a.zero) a.zero[threadIdx.x] = 0;
+  if (rank == 0 && threadIdx.x == 0 && a.zero) *a.zero = 0;
   const int local0 = warp * a.steps * 32 + lane;                             // this thread's first pair in the tile
   uint64_t pr[kClusterSteps];
 #pragma unroll
@@ -293,7 +293,7 @@ __device__ __forceinline__ void count_digits(const PassArgs& a, int (*cnt)[kDigi
 
 __global__ void __launch_bounds__(kThreads) sort_count_kernel(const __grid_constant__ PassArgs a) {
   __shared__ int cnt[kWarps][kDigits];
-  if (a.zero && blockIdx.x == 0 && threadIdx.x < 2) a.zero[threadIdx.x] = 0;
+  if (a.zero && blockIdx.x == 0 && threadIdx.x == 0) *a.zero = 0;
   count_digits(a, cnt);
   int s = 0;
 #pragma unroll
