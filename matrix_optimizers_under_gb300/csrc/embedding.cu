@@ -8,9 +8,9 @@
 // the gradient writes every row of dW once, or with `accumulate` adds to the
 // rows that tokens name.
 //
-// Both are bound by HBM.  A thread takes 8 columns with one 16- or 32-byte access
-// a row (layouts whose rows do not start on such a boundary: 8 columns a block
-// apart, so a warp's scalar accesses are still contiguous).
+// Both are bound by HBM, or by L2 where rows repeat.  A thread takes 8 columns with one
+// 16- or 32-byte access a row.  Layouts whose rows do not start on such a boundary are read in
+// the 16-byte words that hold their rows.
 //
 // Gradient, of more ids than a few, in three launches: the sort of positions by token
 // (stable), the rows, and the rows that the division of work cut.
@@ -32,6 +32,7 @@
 #include <cuda_bf16.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "ops_internal.h"
 #include "ops_ptx.cuh"
@@ -49,6 +50,11 @@ __device__ __forceinline__ void unpack8(const uint32_t (&w)[4], float (&x)[8]) {
     x[2 * k] = __uint_as_float(w[k] << 16);
     x[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
   }
+}
+
+template <bool kBf16>
+__device__ __forceinline__ float load_one(const void* p, int64_t i) {
+  return kBf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[i] << 16) : static_cast<const float*>(p)[i];
 }
 
 // The 8 columns of thread `tid` of `threads` in the column block starting at
@@ -77,14 +83,17 @@ struct Row8 {
     }
   }
   // From a row in shared memory whose first column is the block's.
-  __device__ __forceinline__ void load_shared(const uint8_t* row, int tid, int cols) {
-    static_assert(kVec, "rows in shared memory are read in vectors");
-    if (kCols * tid >= cols) return;
-    const uint4* q = reinterpret_cast<const uint4*>(row) + (kBf16 ? tid : 2 * tid);
+  __device__ __forceinline__ void load_shared(const uint8_t* row, int tid, int threads, int cols) {
+    if constexpr (kVec) {
+      if (kCols * tid >= cols) return;
+      const uint4* q = reinterpret_cast<const uint4*>(row) + (kBf16 ? tid : 2 * tid);
 #pragma unroll
-    for (int k = 0; k < (kBf16 ? 1 : 2); ++k) {
-      const uint4 u = q[k];
-      w[4 * k] = u.x; w[4 * k + 1] = u.y; w[4 * k + 2] = u.z; w[4 * k + 3] = u.w;
+      for (int k = 0; k < (kBf16 ? 1 : 2); ++k) {
+        const uint4 u = q[k];
+        w[4 * k] = u.x; w[4 * k + 1] = u.y; w[4 * k + 2] = u.z; w[4 * k + 3] = u.w;
+      }
+    } else {
+      load(row, 0, tid, threads, cols);
     }
   }
   __device__ __forceinline__ void get(float (&x)[8]) const {
@@ -130,7 +139,7 @@ __device__ __forceinline__ void store8(void* base, int64_t at, int tid, int thre
 // in and out of the SMs, 11 TB/s; 150 MB of DRAM).  One row: 1.5 us.
 constexpr int kLookupRows = 4;             // rows of a thread, all loaded before the first store
 
-template <bool kWBf16, bool kOutBf16, bool kVec>
+template <bool kWBf16, bool kOutBf16>
 __global__ void __launch_bounds__(kMaxThreads) lookup_kernel(const __grid_constant__ LookupArgs a) {
   const int64_t c0 = (int64_t)blockIdx.y * blockDim.x * kCols;
   const int cols = (int)min((int64_t)blockDim.x * kCols, a.dim - c0);
@@ -143,7 +152,7 @@ __global__ void __launch_bounds__(kMaxThreads) lookup_kernel(const __grid_consta
     if (t < a.n) id[r] = a.ids64 ? static_cast<const int64_t*>(a.ids)[t] : static_cast<const int32_t*>(a.ids)[t];
     if (id[r] >= a.vocab) id[r] = -1;
   }
-  Row8<kWBf16, kVec> row[kLookupRows];
+  Row8<kWBf16, true> row[kLookupRows];
 #pragma unroll
   for (int r = 0; r < kLookupRows; ++r)
     if (id[r] >= 0) row[r].load(a.w, id[r] * a.w_ld + c0, threadIdx.x, blockDim.x, cols);
@@ -155,7 +164,95 @@ __global__ void __launch_bounds__(kMaxThreads) lookup_kernel(const __grid_consta
     row[r].get(x);
 #pragma unroll
     for (int k = 0; k < kCols; ++k) x[k] = id[r] >= 0 ? a.scale * x[k] : 0.f;
-    store8<kOutBf16, kVec>(a.out, t * a.out_ld + c0, threadIdx.x, blockDim.x, cols, x);
+    store8<kOutBf16, true>(a.out, t * a.out_ld + c0, threadIdx.x, blockDim.x, cols, x);
+  }
+}
+
+// 8 columns from c on of a row of `dim` that may start anywhere: out of the 16-byte words that
+// hold them, where those lie in the row, else one by one.
+template <bool kBf16>
+__device__ __forceinline__ void load8_any(const void* base, int64_t at, int64_t c, int64_t dim, float (&x)[8]) {
+  constexpr int kPer = kBf16 ? 8 : 4, kWords = kBf16 ? 2 : 3;          // elements of a word; words that hold 8
+  const uint8_t* const p = static_cast<const uint8_t*>(base) + (at + c) * (kBf16 ? 2 : 4);
+  if (c >= kPer && c + kWords * kPer <= dim) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+    const uint4* const q = reinterpret_cast<const uint4*>(a & ~(uintptr_t)15);
+    uint32_t w[4 * kWords];
+#pragma unroll
+    for (int k = 0; k < kWords; ++k) {
+      const uint4 u = q[k];
+      w[4 * k] = u.x; w[4 * k + 1] = u.y; w[4 * k + 2] = u.z; w[4 * k + 3] = u.w;
+    }
+    const bool by1 = a & 4, by2 = a & 8;
+#pragma unroll
+    for (int k = 0; k < 4 * kWords - 1; ++k) w[k] = by1 ? w[k + 1] : w[k];
+#pragma unroll
+    for (int k = 0; k < 4 * kWords - 3; ++k) w[k] = by2 ? w[k + 2] : w[k];
+    if constexpr (kBf16) {
+      const uint32_t shift = a & 2 ? 16 : 0;
+      const uint32_t v[4] = {__funnelshift_r(w[0], w[1], shift), __funnelshift_r(w[1], w[2], shift),
+                             __funnelshift_r(w[2], w[3], shift), __funnelshift_r(w[3], w[4], shift)};
+      unpack8(v, x);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[k] = __uint_as_float(w[k]);
+    }
+    return;
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) x[k] = load_one<kBf16>(base, at + c + k);
+}
+
+// Rows that do not start on vector boundaries: a thread takes the 8 columns of an output row
+// that start on a 16-byte boundary of it, and the first threads its ends.  (35907 x 2709 of
+// bf16: 88 us; columns one by one 166.)
+constexpr int kAnyRows = 2;
+
+template <bool kWBf16, bool kOutBf16>
+__global__ void __launch_bounds__(kMaxThreads) lookup_any_kernel(const __grid_constant__ LookupArgs a) {
+  const int64_t j = (int64_t)blockIdx.y * blockDim.x + threadIdx.x;
+  const int64_t t0 = (int64_t)blockIdx.x * blockDim.y * kAnyRows + threadIdx.y;
+  int64_t id[kAnyRows], c[kAnyRows];
+  int head[kAnyRows];                                   // columns before the first boundary
+  float x[kAnyRows][8];
+#pragma unroll
+  for (int r = 0; r < kAnyRows; ++r) {
+    const int64_t t = t0 + r * blockDim.y;
+    id[r] = -1;
+    if (t < a.n) id[r] = a.ids64 ? static_cast<const int64_t*>(a.ids)[t] : static_cast<const int32_t*>(a.ids)[t];
+    if (id[r] >= a.vocab) id[r] = -1;
+    const uintptr_t o = reinterpret_cast<uintptr_t>(a.out) + t * a.out_ld * (kOutBf16 ? 2 : 4);
+    head[r] = (int)min((int64_t)((16 - (o & 15)) & 15) / (kOutBf16 ? 2 : 4), a.dim);
+    c[r] = head[r] + 8 * j;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[r][k] = 0.f;
+    if (id[r] >= 0 && c[r] + 8 <= a.dim) load8_any<kWBf16>(a.w, id[r] * a.w_ld, c[r], a.dim, x[r]);
+  }
+#pragma unroll
+  for (int r = 0; r < kAnyRows; ++r) {
+    const int64_t t = t0 + r * blockDim.y, row = t * a.out_ld;
+    if (t >= a.n) break;
+    if (c[r] + 8 <= a.dim) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[r][k] = id[r] >= 0 ? a.scale * x[r][k] : 0.f;
+      if constexpr (kOutBf16) {
+        store8<true, true>(a.out, row + c[r], 0, 1, kCols, x[r]);
+      } else {
+        float4* const o = reinterpret_cast<float4*>(static_cast<float*>(a.out) + row + c[r]);
+        o[0] = make_float4(x[r][0], x[r][1], x[r][2], x[r][3]);
+        o[1] = make_float4(x[r][4], x[r][5], x[r][6], x[r][7]);
+      }
+    }
+    if (j >= 8) continue;
+    const int64_t tail = head[r] + (a.dim - head[r]) / 8 * 8;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int64_t col = e == 0 ? j : tail + j;
+      if (col >= (e == 0 ? head[r] : a.dim)) continue;
+      const float v = id[r] >= 0 ? a.scale * load_one<kWBf16>(a.w, id[r] * a.w_ld + col) : 0.f;
+      if constexpr (kOutBf16) static_cast<__nv_bfloat16*>(a.out)[row + col] = __float2bfloat16_rn(v);
+      else static_cast<float*>(a.out)[row + col] = v;
+    }
   }
 }
 
@@ -163,7 +260,6 @@ __global__ void __launch_bounds__(kMaxThreads) lookup_kernel(const __grid_consta
 constexpr int kMaxBatch = 32;              // a lane each
 constexpr int kMaxStages = 8;
 constexpr int kBatchBytes = 32768;         // a batch's rows, about
-constexpr int kScalarBytes = 47104;        // rows of dout and dW as fp32, of layouts off the vectors' boundaries
 constexpr int kRingBytes = 98304;          // of the CTAs an SM holds: two, or more with less each
 constexpr uint64_t kWaitNs = 2000000000ull;   // a stage is due within microseconds: longer is an error
 constexpr int kFixCols = 128;              // columns of a CTA that adds partial rows
@@ -347,120 +443,18 @@ __device__ __forceinline__ void put_row(const GradKernelArgs& p, const Slab& sl,
   store8<kOutBf16, kVec>(a.grad, v * a.grad_ld + c0, tid, threads, cols, acc);
 }
 
-// Layouts whose rows do not start on vector boundaries.  The CTA brings a batch
-// of rows into shared memory as fp32, an element a thread and 16 of each in
-// flight, then each thread adds up its columns.  (7709 rows of 588 fp32 columns: 30 us a
-// call; 37 with threads that load their columns of four rows at a time and add them.)
-template <bool kBf16>
-__device__ __forceinline__ float load_one(const void* base, int64_t i) {
-  return kBf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(base)[i] << 16)
-               : static_cast<const float*>(base)[i];
-}
-
-// `rows` rows of `cols` columns, the r-th from element at(r) (< 0: none).
-template <bool kBf16, typename At>
-__device__ __forceinline__ void gather_rows(float* to, const void* base, int rows, int cols, At at) {
-  constexpr int kAhead = 16;
-  const int dr = kMaxThreads / cols, dc = kMaxThreads % cols, total = rows * cols;
-  int r = threadIdx.x / cols, c = threadIdx.x % cols;
-  for (int e0 = threadIdx.x; e0 < total; e0 += kAhead * kMaxThreads) {
-    float x[kAhead];
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const int64_t from = e0 + k * kMaxThreads < total ? at(r) : -1;
-      x[k] = from >= 0 ? load_one<kBf16>(base, from + c) : 0.f;
-      r += dr;
-      c += dc;
-      if (c >= cols) {
-        c -= cols;
-        ++r;
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k)
-      if (e0 + k * kMaxThreads < total) to[e0 + k * kMaxThreads] = x[k];
-  }
-}
-
-template <bool kInBf16, bool kOutBf16>
-__global__ void __launch_bounds__(kMaxThreads, 3) embed_grad_kernel(const __grid_constant__ GradKernelArgs p) {
-  extern __shared__ __align__(128) uint8_t smem[];     // p.batch rows of dout, and of dW with accumulate
-  __shared__ int32_t keys[kMaxBatch], order[kMaxBatch], before;
-  const EmbedGradArgs& a = p.a;
-  const int tid = threadIdx.x;
-  const int64_t c0 = (int64_t)blockIdx.y * kMaxThreads * kCols;
-  const int cols = (int)min((int64_t)kMaxThreads * kCols, a.dim - c0);
-  const int64_t s = blockIdx.x;
-  float* const rows = reinterpret_cast<float*>(smem);
-  float* const olds = rows + p.batch * cols;
-  zero_unnamed<true>(a, [&](int64_t r) {
-    for (int c = tid & 31; c < cols; c += 32) {
-      const int64_t at = r * a.grad_ld + c0 + c;
-      if constexpr (kOutBf16) static_cast<uint16_t*>(a.grad)[at] = 0;
-      else static_cast<float*>(a.grad)[at] = 0.f;
-    }
-  });
-  ptx::launch_dependents();
-  const Slab sl = slab_of(p, s);
-  float acc[kCols] = {};
-  Row8<kOutBf16, false> old;                           // what row v of dW holds
-  int v = -1;
-  bool first = true;                                   // row v is the slab's first
-  for (int64_t base = sl.i0; base < sl.i1; base += p.batch) {
-    const int cnt = (int)min((int64_t)p.batch, sl.i1 - base);
-    __syncthreads();
-    if (tid < cnt) {
-      keys[tid] = a.keys[base + tid];
-      order[tid] = a.order[base + tid];
-    }
-    if (tid == 0) before = v;                          // (the same in every thread)
-    __syncthreads();
-    gather_rows<kInBf16>(rows, a.dout, cnt, cols,
-                         [&](int r) { return keys[r] < a.vocab ? (int64_t)order[r] * a.dout_ld + c0 : (int64_t)-1; });
-    if (a.accumulate)
-      gather_rows<kOutBf16>(olds, a.grad, cnt, cols, [&](int r) {
-        return keys[r] < a.vocab && keys[r] != (r > 0 ? keys[r - 1] : before) ? (int64_t)keys[r] * a.grad_ld + c0
-                                                                              : (int64_t)-1;
-      });
-    __syncthreads();
-    for (int b = 0; b < cnt; ++b) {
-      const int key = keys[b];
-      if (key >= a.vocab) break;                       // masked: after every row
-      if (key != v) {
-        if (v >= 0) {
-          put_row<kOutBf16, false>(p, sl, s, c0, v, first, false, tid, kMaxThreads, cols, acc, old);
-          first = false;
-        }
-        v = key;
-#pragma unroll
-        for (int k = 0; k < kCols; ++k) {
-          acc[k] = 0.f;
-          const int c = tid + k * kMaxThreads;
-          if (a.accumulate && c < cols) old.w[k] = __float_as_uint(olds[b * cols + c]);
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < kCols; ++k) {
-        const int c = tid + k * kMaxThreads;
-        if (c < cols) acc[k] = fmaf(a.scale, rows[b * cols + c], acc[k]);
-      }
-    }
-  }
-  // (a masked key that goes on is no row: v is the last row before it)
-  if (v >= 0)
-    put_row<kOutBf16, false>(p, sl, s, c0, v, first, a.keys[sl.i1 - 1] == v, tid, kMaxThreads, cols, acc, old);
-  if (tid < 32 && blockIdx.y == 0) note_cut(p, sl, s);
-}
-
-// The same over rows on vector boundaries.  Warp 0 copies the slab's rows of
-// dout into the stages of a ring, a batch at a time (a lane each), and hands
-// on their keys; the other warps add the rows up, 8 columns a thread.
-
-template <bool kInBf16, bool kOutBf16>
-__global__ void __launch_bounds__(32 + kMaxThreads) embed_rows_kernel(const __grid_constant__ GradKernelArgs p) {
+// The rows.  Warp 0 copies the slab's rows of dout into the stages of a ring, a batch at a
+// time (a lane each), and hands on their keys; the other warps add the rows up, 8
+// columns a thread.  Layouts whose rows do not start on vector boundaries (not kVec): a row
+// comes as the 16-byte words that hold it, except past the tensor's end, and is read from
+// where it starts in them; with accumulate the adding threads fetch dW's row as theirs begins.
+// (48890 x 1365 bf16 into 1703 rows: 76 us, added 94; element by element 738.)
+template <bool kInBf16, bool kOutBf16, bool kVec>
+__global__ void __launch_bounds__(32 + kMaxThreads, 3) embed_rows_kernel(const __grid_constant__ GradKernelArgs p) {
   extern __shared__ __align__(128) uint8_t smem[];     // a zero row, then the ring
   __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages];
   __shared__ int32_t keys[kMaxStages][kMaxBatch];
+  __shared__ uint8_t starts[kMaxStages][kMaxBatch];    // where a row starts in its first 16 bytes
   __shared__ int32_t count[kMaxStages];                // positions of the batch; the last one: ~positions
   const EmbedGradArgs& a = p.a;
   const int threads = p.threads, lane = threadIdx.x & 31;
@@ -483,15 +477,25 @@ __global__ void __launch_bounds__(32 + kMaxThreads) embed_rows_kernel(const __gr
   const uint64_t first_out = ptx::policy_evict_first();   // (90 us with it, 93 without)
   uint8_t* const out = static_cast<uint8_t*>(a.grad) + c0 * (kOutBf16 ? 2 : 4);
   const int64_t out_stride = a.grad_ld * (kOutBf16 ? 2 : 4);
-  const uint32_t zeros = ptx::smem_u32(smem);
-  zero_unnamed<false>(a, [&](int64_t r) { ptx::bulk_store(out + r * out_stride, zeros, out_bytes, first_out); });
-  ptx::bulk_commit();
+  if constexpr (kVec) {
+    const uint32_t zeros = ptx::smem_u32(smem);
+    zero_unnamed<false>(a, [&](int64_t r) { ptx::bulk_store(out + r * out_stride, zeros, out_bytes, first_out); });
+    ptx::bulk_commit();
+  } else {
+    zero_unnamed<true>(a, [&](int64_t r) {
+      for (int c = lane; c < cols; c += 32) {
+        if constexpr (kOutBf16) reinterpret_cast<uint16_t*>(out + r * out_stride)[c] = 0;
+        else reinterpret_cast<float*>(out + r * out_stride)[c] = 0.f;
+      }
+    });
+  }
   ptx::launch_dependents();
   const Slab sl = slab_of(p, s);
 
   if (threadIdx.x < 32) {
     const int64_t in_stride = a.dout_ld * (kInBf16 ? 2 : 4);
     const uint8_t* in = static_cast<const uint8_t*>(a.dout) + c0 * (kInBf16 ? 2 : 4);
+    const uintptr_t in_end = reinterpret_cast<uintptr_t>(a.dout) + ((a.n - 1) * a.dout_ld + a.dim) * (kInBf16 ? 2 : 4);
     int stage = 0, use = 0;
     bool more = true;
     int64_t base = sl.i0;
@@ -518,20 +522,37 @@ __global__ void __launch_bounds__(32 + kMaxThreads) embed_rows_kernel(const __gr
       int left = __shfl_up_sync(0xffffffffu, this_key, 1);
       if (lane == 0) left = before;
       before = __shfl_sync(0xffffffffu, this_key, p.batch - 1);
-      const bool brings = a.accumulate && in_row && this_key != left;
-      const int olds = __popc(__ballot_sync(0xffffffffu, brings));
+      const bool brings = kVec && a.accumulate && in_row && this_key != left;
+      const uint8_t* from_row = in + this_from * in_stride;
+      uint8_t* const slot = ring + (size_t)(stage * p.batch + lane) * p.slot;
+      uint32_t bytes = in_row ? row_bytes : 0;
       if (in_row) keys[stage][lane] = this_key;
+      if (!kVec && in_row) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(from_row), first = at & ~(uintptr_t)15, end = at + row_bytes;
+        uintptr_t last = (end + 15) & ~(uintptr_t)15;
+        if (last > in_end) {                                           // the rest one by one
+          last = max(first, end & ~(uintptr_t)15);
+          for (uintptr_t e = max(last, at); e < end; e += kInBf16 ? 2 : 4) {
+            uint8_t* const to = slot + (e - first);
+            if constexpr (kInBf16) *reinterpret_cast<uint16_t*>(to) = *reinterpret_cast<const uint16_t*>(e);
+            else *reinterpret_cast<uint32_t*>(to) = *reinterpret_cast<const uint32_t*>(e);
+          }
+        }
+        starts[stage][lane] = (uint8_t)(at - first);
+        from_row = reinterpret_cast<const uint8_t*>(first);
+        bytes = (uint32_t)(last - first);
+      }
+      const uint32_t all = __reduce_add_sync(0xffffffffu, bytes + (brings ? out_bytes : 0));
+      __syncwarp();                                                    // the lanes' keys come before the arrival
       if (lane == 0) {
         count[stage] = more ? cnt : ~cnt;
-        ptx::mbar_arrive_expect_tx(ptx::smem_u32(&full[stage]), (uint32_t)cnt * row_bytes + (uint32_t)olds * out_bytes);
+        ptx::mbar_arrive_expect_tx(ptx::smem_u32(&full[stage]), all);
       }
       __syncwarp();
-      if (in_row)
-        ptx::bulk_load(ptx::smem_u32(ring) + (uint32_t)(stage * p.batch + lane) * p.slot, in + this_from * in_stride,
-                       row_bytes, ptx::smem_u32(&full[stage]));
+      if (bytes > 0) ptx::bulk_load(ptx::smem_u32(slot), from_row, bytes, ptx::smem_u32(&full[stage]));
       if (brings)
-        ptx::bulk_load(ptx::smem_u32(ring) + (uint32_t)(stage * p.batch + lane) * p.slot + p.row_slot,
-                       out + this_key * out_stride, out_bytes, ptx::smem_u32(&full[stage]));
+        ptx::bulk_load(ptx::smem_u32(slot) + p.row_slot, out + this_key * out_stride, out_bytes,
+                       ptx::smem_u32(&full[stage]));
       if (++stage == p.stages) { stage = 0; ++use; }
       base = next;
     }
@@ -539,7 +560,7 @@ __global__ void __launch_bounds__(32 + kMaxThreads) embed_rows_kernel(const __gr
   } else if ((int)threadIdx.x < 32 + threads) {
     const int tid = threadIdx.x - 32;
     float acc[kCols] = {};
-    Row8<kOutBf16, true> old;                          // what row v of dW holds
+    Row8<kOutBf16, kVec> old;                          // what row v of dW holds
     int v = -1;
     bool first = true;                                 // row v is the slab's first
     int stage = 0, use = 0;
@@ -554,23 +575,28 @@ __global__ void __launch_bounds__(32 + kMaxThreads) embed_rows_kernel(const __gr
       more = c >= 0;
       const int cnt = more ? c : ~c;
       const uint8_t* rows = ring + (size_t)stage * p.batch * p.slot;
-      constexpr int kAhead = 4;
+      constexpr int kAhead = kVec ? 4 : 1;
       for (int b0 = 0; b0 < cnt; b0 += kAhead) {
-        Row8<kInBf16, true> row[kAhead];
+        Row8<kInBf16, kVec> row[kAhead];
 #pragma unroll
         for (int b = 0; b < kAhead; ++b)
-          if (b0 + b < cnt) row[b].load_shared(rows + (size_t)(b0 + b) * p.slot, tid, cols);
+          if (b0 + b < cnt)
+            row[b].load_shared(rows + (size_t)(b0 + b) * p.slot + (kVec ? 0 : starts[stage][b0 + b]), tid, threads,
+                               cols);
 #pragma unroll
         for (int b = 0; b < kAhead; ++b) {
           if (b0 + b >= cnt) break;
           const int key = keys[stage][b0 + b];
           if (key != v) {
             if (v >= 0) {
-              put_row<kOutBf16, true>(p, sl, s, c0, v, first, false, tid, threads, cols, acc, old);
+              put_row<kOutBf16, kVec>(p, sl, s, c0, v, first, false, tid, threads, cols, acc, old);
               first = false;
             }
             v = key;
-            if (a.accumulate) old.load_shared(rows + (size_t)(b0 + b) * p.slot + p.row_slot, tid, cols);
+            if (a.accumulate) {
+              if constexpr (kVec) old.load_shared(rows + (size_t)(b0 + b) * p.slot + p.row_slot, tid, threads, cols);
+              else old.load(a.grad, (int64_t)v * a.grad_ld + c0, tid, threads, cols);
+            }
 #pragma unroll
             for (int k = 0; k < kCols; ++k) acc[k] = 0.f;
           }
@@ -586,7 +612,7 @@ __global__ void __launch_bounds__(32 + kMaxThreads) embed_rows_kernel(const __gr
     }
     // (a masked key that goes on is no row: v is the last row before it)
     if (ok && v >= 0)
-      put_row<kOutBf16, true>(p, sl, s, c0, v, first, a.keys[sl.i1 - 1] == v, tid, threads, cols, acc, old);
+      put_row<kOutBf16, kVec>(p, sl, s, c0, v, first, a.keys[sl.i1 - 1] == v, tid, threads, cols, acc, old);
   }
   ptx::bulk_wait_all();                                // the zero row is shared memory of this CTA
 }
@@ -696,7 +722,8 @@ constexpr int kSmallCols = 32 * kCols;
 constexpr int kSmallRow = 32;              // positions of a row that one warp adds
 
 template <bool kInBf16, bool kOutBf16, bool kVec>
-__global__ void __launch_bounds__(32 * kSmallWarps, kVec ? 4 : 3) embed_small_kernel(const __grid_constant__ EmbedGradArgs a) {
+__global__ void __launch_bounds__(32 * kSmallWarps, kVec ? 4 : 3)
+    embed_small_kernel(const __grid_constant__ EmbedGradArgs a) {
   __shared__ int16_t pos[kSmallIds], row[kSmallIds];      // listed positions, and their rows in the share
   __shared__ uint32_t named[kSmallShare / 32];
   __shared__ int warp_count[kSmallWarps];
@@ -831,9 +858,14 @@ bool vec_rows(const void* p, int64_t ld, int64_t dim, int32_t bf16) {
   return ld % kCols == 0 && dim % kCols == 0 && aligned(p, bf16 ? 16 : 32);
 }
 
-template <bool kA, bool kB, bool kVec>
-void lookup_launch(const LookupArgs& a, dim3 grid, dim3 block, cudaStream_t s) {
-  lookup_kernel<kA, kB, kVec><<<grid, block, 0, s>>>(a);
+template <bool kA, bool kB>
+void lookup_launch(const LookupArgs& a, bool vec, cudaStream_t s) {
+  const int64_t threads = vec ? threads_for(a.dim) : threads_for(a.dim + 8), rows = kMaxThreads / threads;
+  const int64_t per = rows * (vec ? kLookupRows : kAnyRows);
+  const dim3 block((unsigned)threads, (unsigned)rows);
+  const dim3 grid((unsigned)((a.n + per - 1) / per), (unsigned)((a.dim + threads * kCols - 1) / (threads * kCols)));
+  if (vec) lookup_kernel<kA, kB><<<grid, block, 0, s>>>(a);
+  else lookup_any_kernel<kA, kB><<<grid, block, 0, s>>>(a);
 }
 // Shares of the vocabulary for few ids: four CTAs an SM, more where a share would
 // not fit its bitmap.
@@ -858,22 +890,16 @@ cudaError_t small_launch(const EmbedGradArgs& all, bool vec, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-template <bool kIn, bool kOut>
-cudaError_t grad_launch(GradKernelArgs& p, int64_t ctas, bool vec, cudaStream_t s) {
+template <bool kIn, bool kOut, bool kVec>
+cudaError_t grad_launch(GradKernelArgs& p, int64_t ctas, cudaStream_t s) {
   const EmbedGradArgs& a = p.a;
   const int threads = threads_for(a.dim);
   const dim3 grid((unsigned)ctas, (unsigned)((a.dim + threads * kCols - 1) / (threads * kCols)));
   // The kernel writes dW before its wait, beside the sort, which is the kernel before it.
-  if (!vec) {
-    const size_t row = std::min<int64_t>(a.dim, (int64_t)kMaxThreads * kCols) * sizeof(float) * (a.accumulate ? 2 : 1);
-    p.batch = (int32_t)std::min<size_t>(kMaxBatch, kScalarBytes / row);
-    const dim3 blocks((unsigned)ctas, (unsigned)((a.dim + kMaxThreads * kCols - 1) / (kMaxThreads * kCols)));
-    return launch_overlapped(embed_grad_kernel<kIn, kOut>, blocks, dim3(kMaxThreads), p.batch * row, s, true, p);
-  }
   p.threads = threads;
   const int cols = (int)std::min<int64_t>(a.dim, (int64_t)threads * kCols);
-  p.row_slot = (uint32_t)round_up((size_t)cols * (kIn ? 2 : 4), 128);
-  p.zero_bytes = (int32_t)round_up((size_t)cols * (kOut ? 2 : 4), 128);
+  p.row_slot = (uint32_t)round_up((size_t)cols * (kIn ? 2 : 4) + (kVec ? 0 : 30), 128);
+  p.zero_bytes = kVec ? (int32_t)round_up((size_t)cols * (kOut ? 2 : 4), 128) : 0;
   p.slot = p.row_slot + (a.accumulate ? (uint32_t)p.zero_bytes : 0);
   const int ring = 2 * kRingBytes / ctas_per_sm(a.dim);
   p.batch = (int32_t)std::max<int64_t>(2, std::min<int64_t>({kMaxBatch, kBatchBytes / p.slot, ring / (2 * p.slot)}));
@@ -885,12 +911,13 @@ cudaError_t grad_launch(GradKernelArgs& p, int64_t ctas, bool vec, cudaStream_t 
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
   if (!ready[dev].load()) {
-    e = cudaFuncSetAttribute(embed_rows_kernel<kIn, kOut>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(embed_rows_kernel<kIn, kOut, kVec>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kRingBytes + 16384);
     if (e != cudaSuccess) return e;
     ready[dev].store(true);
   }
-  return launch_overlapped(embed_rows_kernel<kIn, kOut>, grid, dim3((unsigned)std::max(256, 32 + threads)), smem, s,
+  const dim3 block((unsigned)std::max(256, 32 + threads));
+  return launch_overlapped(embed_rows_kernel<kIn, kOut, kVec>, grid, block, smem, s,
                            true, p);
 }
 
@@ -898,20 +925,8 @@ cudaError_t grad_launch(GradKernelArgs& p, int64_t ctas, bool vec, cudaStream_t 
 
 cudaError_t launch_lookup(const LookupArgs& a, cudaStream_t s) {
   const bool vec = vec_rows(a.w, a.w_ld, a.dim, a.w_bf16) && vec_rows(a.out, a.out_ld, a.dim, a.out_bf16);
-  const int tx = threads_for(a.dim), ty = kMaxThreads / tx;
-  const dim3 block(tx, ty);
-  const dim3 grid((unsigned)((a.n + ty * kLookupRows - 1) / (ty * kLookupRows)),
-                  (unsigned)((a.dim + tx * kCols - 1) / (tx * kCols)));
-  if (vec)
-    a.w_bf16 ? (a.out_bf16 ? lookup_launch<true, true, true>(a, grid, block, s)
-                           : lookup_launch<true, false, true>(a, grid, block, s))
-             : (a.out_bf16 ? lookup_launch<false, true, true>(a, grid, block, s)
-                           : lookup_launch<false, false, true>(a, grid, block, s));
-  else
-    a.w_bf16 ? (a.out_bf16 ? lookup_launch<true, true, false>(a, grid, block, s)
-                           : lookup_launch<true, false, false>(a, grid, block, s))
-             : (a.out_bf16 ? lookup_launch<false, true, false>(a, grid, block, s)
-                           : lookup_launch<false, false, false>(a, grid, block, s));
+  a.w_bf16 ? (a.out_bf16 ? lookup_launch<true, true>(a, vec, s) : lookup_launch<true, false>(a, vec, s))
+           : (a.out_bf16 ? lookup_launch<false, true>(a, vec, s) : lookup_launch<false, false>(a, vec, s));
   return cudaGetLastError();
 }
 
@@ -941,10 +956,14 @@ cudaError_t launch_embed_grad(const EmbedGradArgs& a, cudaStream_t s) {
   p.slabs = sp.slabs;
   p.cut = reinterpret_cast<CutRow*>(at);
   p.parts = reinterpret_cast<float*>(at + round_up(sp.slabs * sizeof(CutRow), 256));
-  const cudaError_t e = a.dout_bf16 ? (a.grad_bf16 ? grad_launch<true, true>(p, sp.ctas, vec, s)
-                                                   : grad_launch<true, false>(p, sp.ctas, vec, s))
-                                    : (a.grad_bf16 ? grad_launch<false, true>(p, sp.ctas, vec, s)
-                                                   : grad_launch<false, false>(p, sp.ctas, vec, s));
+  const auto go = [&](auto in, auto out) {
+    return vec ? grad_launch<decltype(in)::value, decltype(out)::value, true>(p, sp.ctas, s)
+               : grad_launch<decltype(in)::value, decltype(out)::value, false>(p, sp.ctas, s);
+  };
+  const std::true_type yes;
+  const std::false_type no;
+  const cudaError_t e = a.dout_bf16 ? (a.grad_bf16 ? go(yes, yes) : go(yes, no))
+                                    : (a.grad_bf16 ? go(no, yes) : go(no, no));
   if (e != cudaSuccess) return e;
   const int64_t items = sp.slabs * ((a.dim + kFixCols - 1) / kFixCols);      // at most
   const dim3 fix((unsigned)std::min<int64_t>(items, 4 * std::max(1, sm_count())));

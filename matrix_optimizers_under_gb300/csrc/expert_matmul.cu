@@ -287,7 +287,8 @@ struct TileWalk {
   __device__ __forceinline__ TileWalk(const ExpertArgs& p_, const Shape& sh_, const int32_t* start_,
                                       const int32_t* first_, int pair0, int pairs_, int n_tiles_)
       : p(p_), sh(sh_), start(start_), first(first_), t(pair0), pairs(pairs_), n_tiles(n_tiles_), held(0), rest(0) {}
-  // The next tile, or the next turn of the same one, the same in all lanes (kShape: only its n_mma and k_len); false after the last.
+  // The next tile, or the next turn of the same one, the same in all lanes (kShape: only
+  // its n_mma and k_len); false after the last.
   template <bool kShape = false>
   __device__ __forceinline__ bool next(Tile& r) {
     if (kTurns && rest > 0) {
