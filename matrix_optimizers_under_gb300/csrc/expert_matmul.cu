@@ -338,6 +338,16 @@ __device__ __forceinline__ void put_plain(const ExpertArgs& p, uint8_t* stage, c
                                           int rows, int cols, bool add = false) {
   const int lane = threadIdx.x & 31;
   float* const part = reinterpret_cast<float*>(stage);      // 16 rows of 33 floats
+  // what is added to, all rows' loads in flight (one after the other: 27 us a tile)
+  uint32_t old[32];                                         // as they are: a conversion here would wait for its load
+  if ((kAccumulate || add) && lane < cols) {
+#pragma unroll
+    for (int r = 0; r < 32; ++r) {
+      const int64_t i = at + min(r, rows - 1) * p.out_ld + lane;
+      if constexpr (kBf16) old[r] = static_cast<const uint16_t*>(p.out)[i];
+      else old[r] = static_cast<const uint32_t*>(p.out)[i];
+    }
+  }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     __syncwarp();
@@ -347,18 +357,14 @@ __device__ __forceinline__ void put_plain(const ExpertArgs& p, uint8_t* stage, c
     }
     __syncwarp();
     if (lane >= cols) continue;
-#pragma unroll 4
+#pragma unroll
     for (int r = 0; r < 16; ++r) {
       if (16 * h + r >= rows) break;
-      const float x = part[r * 33 + lane];
+      float x = part[r * 33 + lane];
+      if (kAccumulate || add) x += __uint_as_float(kBf16 ? old[16 * h + r] << 16 : old[16 * h + r]);
       const int64_t i = at + (16 * h + r) * p.out_ld + lane;
-      if constexpr (kBf16) {
-        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + i;
-        *o = __float2bfloat16_rn(kAccumulate ? x + __bfloat162float(*o) : x);
-      } else {
-        float* o = static_cast<float*>(p.out) + i;
-        *o = kAccumulate || add ? x + *o : x;
-      }
+      if constexpr (kBf16) static_cast<__nv_bfloat16*>(p.out)[i] = __float2bfloat16_rn(x);
+      else static_cast<float*>(p.out)[i] = x;
     }
   }
 }
