@@ -369,6 +369,23 @@ __device__ __forceinline__ void put_plain(const ExpertArgs& p, uint8_t* stage, c
   }
 }
 
+// `bytes` of zeros (of elements of `esz`), by the epilogue's threads, in words of 16 bytes
+// but for the ends.
+__device__ __forceinline__ void put_zeros(uint8_t* to, int64_t bytes, int esz) {
+  const int tid = threadIdx.x - 32 * kFirstEpiWarp;
+  if (bytes <= 0) return;
+  const int64_t head = min((int64_t)(16 - (reinterpret_cast<uintptr_t>(to) & 15)) & 15, bytes);
+  const int64_t words = (bytes - head) / 16, tail = head + 16 * words;
+  for (int64_t i = tid; i < words; i += 32 * kEpiWarps)
+    __stcs(reinterpret_cast<uint4*>(to + head) + i, make_uint4(0, 0, 0, 0));
+  // fewer than 16 bytes at each end: a thread an element
+  const int64_t at = tid < 8 ? (int64_t)tid * esz : tail + (int64_t)(tid - 8) * esz;
+  if (tid < 16 && at < (tid < 8 ? head : bytes)) {
+    if (esz == 2) *reinterpret_cast<uint16_t*>(to + at) = 0;
+    else *reinterpret_cast<uint32_t*>(to + at) = 0;
+  }
+}
+
 // 128 bytes of each of a warp's 32 rows (64 bf16 or 32 fp32 columns, `x` on,
 // of rows `y` on of matrix `z`), lane l holding row l's in `w`.  The rows go, 16 at a
 // time, through the warp's two 2 KB of shared memory, out by tensor copies, which
@@ -766,7 +783,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
       int c;
       bool more;
       uint32_t made, taken;
-    } fetch;
+    } fetch{};
     uint8_t* const fetch_buf = smem_raw + (smem_base - ptx::smem_u32(smem_raw)) + kRingBytes(kMode, kAccumulate) +
                                kEpiWarps * 2 * kPartBytes(kMode) + (warp - kFirstEpiWarp) * kFetches * kFetchBytes;
     TileWalk<kMode, !kBf16> ahead = walk;
@@ -798,14 +815,17 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
       const int64_t at0 = kWgrad ? tl.z * p.out_stride + row0 * p.out_ld + tl.n0 : 0;      // the warp's first row
       if (kWgrad && tl.k_len == 0) {
         if (p.accumulate) continue;
-        uint32_t z[32];
+        if constexpr (kVec) {
+          uint32_t z[32];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) z[j] = 0;
-        for (int c = kWidth * half; c < tl.n; c += 2 * kWidth) {
-          if (kVec)
+          for (int j = 0; j < 32; ++j) z[j] = 0;
+          for (int c = kWidth * half; c < tl.n; c += 2 * kWidth)
             put_rows(stage, z, &maps.out, tl.n0 + c, row0, tl.z, sh.m - row0, parts);
-          else
-            put_plain<kBf16, false>(p, stage, z, at0 + c, sh.m - row0, tl.n - c);
+        } else if (tl.n0 == 0) {
+          // this CTA's rows, all their columns: they lie in one piece
+          const int first_row = tl.m0 + (int)rank * kCtaM;
+          put_zeros(static_cast<uint8_t*>(p.out) + (tl.z * p.out_stride + first_row * p.out_ld) * kEsz,
+                    (int64_t)min(kCtaM, sh.m - first_row) * p.out_ld * kEsz, kEsz);
         }
         continue;
       }
