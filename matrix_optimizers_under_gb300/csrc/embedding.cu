@@ -77,8 +77,7 @@ struct Row8 {
       for (int k = 0; k < kCols; ++k) {
         const int c = tid + k * threads;
         if (c < cols)
-          w[k] = kBf16 ? (uint32_t)static_cast<const uint16_t*>(base)[at + c] << 16
-                       : static_cast<const uint32_t*>(base)[at + c];
+          w[k] = kBf16 ? static_cast<const uint16_t*>(base)[at + c] : static_cast<const uint32_t*>(base)[at + c];
       }
     }
   }
@@ -100,8 +99,9 @@ struct Row8 {
     if constexpr (kBf16 && kVec) {
       unpack8(w, x);
     } else {
+      // (shifted here: at the load it would wait)
 #pragma unroll
-      for (int k = 0; k < kCols; ++k) x[k] = __uint_as_float(w[k]);
+      for (int k = 0; k < kCols; ++k) x[k] = __uint_as_float(kBf16 ? w[k] << 16 : w[k]);
     }
   }
 };
