@@ -71,11 +71,14 @@ constexpr int kRingBytes(int mode, bool accumulate) {
 }
 constexpr int kPartBytes(int mode) { return mode == kExpertWeightGrad ? 2048 : 1024; }
 // Contraction of an fp32 output that one accumulator takes.  The tensor cores' additions
-// cut off low bits, always towards zero: off by 1.0e-6 of the result (2-norms, normal operands)
-// at K = 1024, 2.1e-6 at 2048, 1.9e-5 at 16384, 7.6e-5 at 65536, where a loop of fp32
-// additions is off by 3e-7.  So a longer one is taken in turns, and the turns' sums
-// are added, rounded to nearest, where the output lies.  (A bf16 output is off by 1.7e-3.)
-constexpr int kMaxK = 2048;
+// cut off low bits, always towards zero: off by 1.0e-6 of the result (2-norms, normal
+// operands) at K = 1024, 2.1e-6 at 2048, 1.9e-5 at 16384, 7.6e-5 at 65536, where a loop of
+// fp32 additions is off by 3e-7.  So a longer one is taken in even turns, and the turns'
+// sums are added, rounded to nearest, where the output lies.  Turns of up to 2048 would be
+// faster (one expert, 32768 x 2048 x 2048: 163 us instead of 180; its weight gradient 180
+// instead of 211) and twice as far off; of up to 960, three here, 228 and 219 us.  (A bf16
+// output is off by 1.7e-3.)
+constexpr int kMaxK = 1024;
 constexpr int kEpiWarps = 8;
 constexpr int kFirstEpiWarp = 4;
 constexpr int kThreads = 32 * (kFirstEpiWarp + kEpiWarps);
@@ -281,19 +284,19 @@ struct TileWalk {
   const int32_t* first;
   int t, pairs, n_tiles;
   int held;               // tiles left in `mine`
-  int rest;               // kTurns: what is left of the tile's contraction
+  int rest, turn;         // kTurns: what is left of the tile's contraction, and a turn's share
   Tile mine;
 
   __device__ __forceinline__ TileWalk(const ExpertArgs& p_, const Shape& sh_, const int32_t* start_,
                                       const int32_t* first_, int pair0, int pairs_, int n_tiles_)
-      : p(p_), sh(sh_), start(start_), first(first_), t(pair0), pairs(pairs_), n_tiles(n_tiles_), held(0), rest(0) {}
+      : p(p_), sh(sh_), start(start_), first(first_), t(pair0), pairs(pairs_), n_tiles(n_tiles_), held(0), rest(0), turn(0) {}
   // The next tile, or the next turn of the same one, the same in all lanes (kShape: only
   // its n_mma and k_len); false after the last.
   template <bool kShape = false>
   __device__ __forceinline__ bool next(Tile& r) {
     if (kTurns && rest > 0) {
       r.k_from += r.k_len;
-      r.k_len = min(rest, kMaxK);
+      r.k_len = min(rest, turn);
       rest -= r.k_len;
       return true;
     }
@@ -317,8 +320,12 @@ struct TileWalk {
     r.k_len = __shfl_sync(0xffffffffu, mine.k_len, lane);
     r.k_from = 0;
     if (kTurns) {
-      rest = max(0, r.k_len - kMaxK);
-      r.k_len -= rest;
+      rest = 0;
+      if (r.k_len > kMaxK) {
+        turn = (ceil_div(r.k_len, ceil_div(r.k_len, kMaxK)) + kBlockK - 1) / kBlockK * kBlockK;
+        rest = r.k_len - turn;
+        r.k_len = turn;
+      }
     }
     --held;
     t += pairs;
