@@ -1126,7 +1126,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_kernel(const __grid_consta
           if (t < p.tile_end) {
             if (p.narrow) {
               if (!wait_or_abort(ptx::smem_u32(&dep_bar[seq % kTileRing]), (seq / kTileRing) & 1, ab,
-                                 wait_code(0, kRoleDependency)))
+                                 wait_code(tl.phase, kRoleDependency)))
                 break;
             } else if (!ready) {
               const int32_t need = t == p.stall_tile ? INT32_MAX : tl.need;
