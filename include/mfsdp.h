@@ -564,7 +564,8 @@ size_t mfsdp_grad_clip_workspace_bytes(int32_t n);
  *   norm = sqrt(sum over all tensors and elements of g^2)
  *   coef = min(1, max_norm / (norm + eps));  1 for an infinite max_norm or norm + eps = 0
  *   out[0] = norm, out[1] = coef            (device, two floats, 8-byte aligned)
- * A NaN anywhere gives NaN for both; an Inf gives norm Inf and coef 0.  Sums
+ * A NaN anywhere gives NaN for both, whatever max_norm is; an Inf gives norm Inf,
+ * and coef 0 for a finite max_norm (an infinite one clips nothing: 1).  Sums
  * run in fp32 over 64 elements and in double above that, and a sum that leaves
  * fp32's accurate range is taken again in double: any finite gradient has a
  * right norm (rounded to fp32, so Inf above its range; coef uses the double).

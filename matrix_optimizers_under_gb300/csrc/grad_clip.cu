@@ -6,6 +6,7 @@
 // before the step:
 //   S = sum over tensors t, elements i of g_ti^2,   norm = sqrt(S)
 //   coef = min(1, max_norm / (norm + eps)),         out_ti = round(coef * g_ti)
+// (an infinite limit clips nothing, not even an infinite norm; a NaN stays one).
 //
 // The norm has to be known before the first output, so the data is read twice.
 // The first launch leaves one partial sum per CTA, the second adds all
@@ -192,7 +193,8 @@ __device__ __forceinline__ void chunk_scale(const ClipTensor& t, const Span& s, 
 __device__ __forceinline__ float coefficient(const ClipHead& p, double sum, float* norm_out) {
   const double norm = sqrt(sum), den = norm + p.eps;
   double c = 1.0;                                   // an infinite limit, or nothing to scale
-  if (!isinf(p.max_norm) && den != 0.0) c = p.max_norm / den;
+  if (isnan(norm)) c = norm;                        // whatever the limit
+  else if (!isinf(p.max_norm) && den != 0.0) c = p.max_norm / den;
   if (c > 1.0) c = 1.0;                             // a NaN stays one
   *norm_out = (float)norm;
   return (float)c;

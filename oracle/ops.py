@@ -13,7 +13,9 @@ def grad_clip_ref(tensors, max_norm: float, eps: float):
     """(norm, coefficient, clipped tensors)."""
     ts = [np.asarray(t, np.float64) for t in tensors]
     norm = float(np.sqrt(sum(float(np.sum(t * t)) for t in ts)))
-    if np.isinf(max_norm) or norm + eps == 0.0:
+    if np.isnan(norm):
+        coef = norm                       # whatever the limit
+    elif np.isinf(max_norm) or norm + eps == 0.0:
         coef = 1.0
     else:
         coef = max_norm / (norm + eps)
