@@ -602,12 +602,12 @@ int mfsdp_sort_ids(const void* ids, int32_t id_type, int64_t n, int64_t n_keys, 
                    void* workspace, size_t workspace_bytes, void* stream);
 
 /* Embedding lookup with scaling: out[t, :] = scale * weight[ids[t], :], zeros
- * for a masked id; fp32 product, rounded once to out_dtype.
+ * for a masked id; fp32 product (scale rounded to fp32), rounded once to out_dtype.
  *   weight   vocab rows of dim elements, weight_ld >= dim elements apart.
  *   out      n rows of dim elements, out_ld >= dim apart; only those elements
  *            are written.
  * weight and out 16-byte aligned.  n = 0 is a no-op.  Errors: INVALID_ARG
- * (scale not finite), UNSUPPORTED_DTYPE, UNSUPPORTED_SHAPE (dim > 2^24, a
+ * (scale not finite in fp32), UNSUPPORTED_DTYPE, UNSUPPORTED_SHAPE (dim > 2^24, a
  * leading dimension below dim), MISALIGNED, OVERLAP, CUDA. */
 int mfsdp_embedding_lookup(const void* weight, int32_t weight_dtype, int64_t vocab, int64_t dim, int64_t weight_ld,
                            const void* ids, int32_t id_type, int64_t n, double scale, void* out, int32_t out_dtype,
@@ -617,7 +617,7 @@ size_t mfsdp_embedding_grad_workspace_bytes(int64_t n, int64_t vocab, int64_t di
 
 /* Gradient of the lookup by sorted tokens:
  *   grad[v, :] = scale * sum over t with ids[t] = v of dout[t, :]
- * summed in fp32 in a fixed order, rounded once to grad_dtype.  accumulate = 0 writes
+ * summed in fp32 (scale rounded to fp32) in a fixed order, rounded once to grad_dtype.  accumulate = 0 writes
  * every row (zeros where no id names it); accumulate = 1 adds to the rows that
  * ids name (read in grad_dtype, added in fp32) and leaves the others alone.
  *   dout   n rows of dim elements, dout_ld apart;  grad  vocab rows, grad_ld

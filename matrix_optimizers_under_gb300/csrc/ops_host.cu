@@ -232,6 +232,9 @@ EmbedLayout embed_layout(int64_t n, int64_t vocab, int64_t dim) {
   return l;
 }
 
+// The kernels take the scale in fp32: finite there too.
+bool scale_ok(double scale) { return std::isfinite((float)scale); }
+
 bool embed_shape_ok(int64_t n, int64_t vocab, int64_t dim) {
   return n >= 0 && n <= INT32_MAX && vocab >= 1 && vocab < INT32_MAX && dim >= 1 && dim <= (1 << 24);
 }
@@ -341,7 +344,7 @@ extern "C" int mfsdp_embedding_lookup(const void* weight, int32_t weight_dtype, 
   if (!known_dtype(weight_dtype) || !known_dtype(out_dtype)) return MFSDP_ERR_UNSUPPORTED_DTYPE;
   int st = check_ids(ids, id_type, n, vocab);
   if (st != MFSDP_OK) return st;
-  if (dim < 1 || !std::isfinite(scale)) return MFSDP_ERR_INVALID_ARG;
+  if (dim < 1 || !scale_ok(scale)) return MFSDP_ERR_INVALID_ARG;
   if (!embed_shape_ok(n, vocab, dim) || !rows_fit(vocab, weight_ld, dim) || !rows_fit(n, out_ld, dim))
     return MFSDP_ERR_UNSUPPORTED_SHAPE;
   if (n == 0) return MFSDP_OK;
@@ -379,7 +382,7 @@ extern "C" int mfsdp_embedding_grad(const void* dout, int32_t dout_dtype, int64_
   if (!known_dtype(dout_dtype) || !known_dtype(grad_dtype)) return MFSDP_ERR_UNSUPPORTED_DTYPE;
   int st = check_ids(ids, id_type, n, vocab);
   if (st != MFSDP_OK) return st;
-  if (dim < 1 || !std::isfinite(scale) || (accumulate != 0 && accumulate != 1)) return MFSDP_ERR_INVALID_ARG;
+  if (dim < 1 || !scale_ok(scale) || (accumulate != 0 && accumulate != 1)) return MFSDP_ERR_INVALID_ARG;
   if (!embed_shape_ok(n, vocab, dim) || !rows_fit(vocab, grad_ld, dim) || !rows_fit(n, dout_ld, dim))
     return MFSDP_ERR_UNSUPPORTED_SHAPE;
   if (!grad || (n > 0 && !dout)) return MFSDP_ERR_INVALID_ARG;
