@@ -612,7 +612,10 @@ def _int32(t, n: int, what: str):
 
 
 def _ws(workspace):
-    return _ptr(workspace), int(workspace.numel() if workspace is not None else 0)
+    """Address and bytes of a workspace (None: the library says whether it needs one)."""
+    if workspace is None:
+        return None, 0
+    return _ptr(_flat(workspace, "workspace")), workspace.numel() * workspace.element_size()
 
 
 class GradSet:
@@ -760,7 +763,7 @@ def op_device_status(workspace, stream=None) -> Tuple[int, int]:
     """(status, raw word) of the last grouped product or embedding gradient that ran with this
     workspace (synchronises)."""
     detail = _i32(0)
-    st = _lib.mfsdp_op_device_status(_ptr(workspace), _stream(stream), ctypes.byref(detail))
+    st = _lib.mfsdp_op_device_status(_ws(workspace)[0], _stream(stream), ctypes.byref(detail))
     return st, detail.value
 
 

@@ -1,6 +1,7 @@
 """Edges of the operators next to the owner step that need no GPU: the oracle's
 special values, and calls that the host turns away."""
 import numpy as np
+import pytest
 
 from oracle.ops import grad_clip_ref
 
@@ -28,3 +29,43 @@ def test_scales_that_fp32_does_not_hold_are_refused(mfsdp):
         assert lookup(scale) == grad(scale) == mfsdp.ERR_INVALID_ARG, scale
     for scale in (3.4e38, 0.0, -1e-60):                                # turned away later, for the output's alignment
         assert lookup(scale, c + 4) == grad(scale, c + 4) == mfsdp.ERR_MISALIGNED, scale
+
+
+def test_binding_refuses_workspaces_that_are_no_device_memory(mfsdp):
+    """On fakes of CUDA tensors, so that each call comes as far as its workspace."""
+    import torch
+
+    class Cuda:
+        """What the binding asks of a CUDA tensor."""
+        is_cuda = True
+
+        def __init__(self, *shape, dtype=torch.float32):
+            self.t = torch.empty(shape, dtype=dtype)
+            self.shape, self.dtype = self.t.shape, dtype
+
+        def __getattr__(self, name):
+            return getattr(self.t, name)
+
+    host, gaps = torch.empty(1 << 20, dtype=torch.uint8), Cuda(8, 8, dtype=torch.uint8)
+    gaps.t = gaps.t[:, :4]
+    f, b, i = Cuda(4, 8), Cuda(4, 8, dtype=torch.bfloat16), Cuda(4, dtype=torch.int32)
+    w, starts, out = Cuda(3, 8, 8, dtype=torch.bfloat16), Cuda(4, dtype=torch.int32), Cuda(2)
+    calls = {
+        "grad_norm": lambda ws: mfsdp.grad_norm(mfsdp.grad_set([f]), out, ws, stream=0),
+        "grad_clip": lambda ws: mfsdp.grad_clip(mfsdp.grad_set([f]), out, ws, max_norm=1.0, stream=0),
+        "sort_ids": lambda ws: mfsdp.sort_ids(i, 3, Cuda(4, dtype=torch.int32), starts, ws, stream=0),
+        "embedding_grad": lambda ws: mfsdp.embedding_grad(f, i, Cuda(9, 8), ws, stream=0),
+        "expert_matmul": lambda ws: mfsdp.expert_matmul(b, w, starts, Cuda(4, 8), ws, stream=0),
+        "expert_weight_grad": lambda ws: mfsdp.expert_weight_grad(b, b, starts, Cuda(3, 8, 8), ws, stream=0),
+        "op_device_status": lambda ws: mfsdp.op_device_status(ws, stream=0),
+    }
+    for name, call in calls.items():
+        with pytest.raises(ValueError, match="workspace must be a CUDA tensor"):
+            call(host)
+        with pytest.raises(ValueError, match="workspace must be contiguous"):
+            call(gaps)
+        if name != "op_device_status":
+            with pytest.raises(mfsdp.MfsdpError):                      # none at all: the library's own check
+                call(None)
+    assert mfsdp._ws(Cuda(64, dtype=torch.float32))[1] == 256          # bytes, whatever the type
+    assert mfsdp.op_device_status(None, stream=0)[0] == mfsdp.ERR_INVALID_ARG
