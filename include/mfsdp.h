@@ -643,7 +643,8 @@ size_t mfsdp_expert_workspace_bytes(int32_t n_experts, int64_t n_rows, int64_t r
  * bf16 operands (in_dtype must be BF16), fp32 accumulation on tensor cores, one
  * rounding to y_dtype (up to 16 tokens forward: fp32 arithmetic).  An fp32 output of a
  * contraction longer than 1024 is added up in turns where it lies, in a fixed order, and
- * is within 1e-6 of its 2-norm.
+ * is within 1e-6 of its 2-norm; a bf16 output is added up in fp32 over every 32768 of it
+ * before its one rounding.
  *   starts[n_experts + 1]  device int32, starts[0] = 0, ascending; read on the
  *          device (values outside [0, n_rows] are clamped).  Rows from
  *          starts[n_experts] on belong to no expert: their y is zero.

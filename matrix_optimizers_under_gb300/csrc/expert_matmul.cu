@@ -76,9 +76,10 @@ constexpr int kPartBytes(int mode) { return mode == kExpertWeightGrad ? 2048 : 1
 // fp32 additions is off by 3e-7.  So a longer one is taken in even turns, and the turns'
 // sums are added, rounded to nearest, where the output lies.  Turns of up to 2048 would be
 // faster (one expert, 32768 x 2048 x 2048: 163 us instead of 180; its weight gradient 180
-// instead of 211) and twice as far off; of up to 960, three here, 228 and 219 us.  (A bf16
-// output is off by 1.7e-3.)
-constexpr int kMaxK = 1024;
+// instead of 211) and twice as far off; of up to 960, three here, 228 and 219 us.
+// A bf16 output is off by 1.7e-3 of its rounding alone, which the cut bits would reach near
+// K = 2^20: it takes turns of up to 32768 (3.8e-5), whose sum stays in tensor memory.
+constexpr int kMaxK(bool bf16) { return bf16 ? 32768 : 1024; }
 constexpr int kEpiWarps = 8;
 constexpr int kFirstEpiWarp = 4;
 constexpr int kThreads = 32 * (kFirstEpiWarp + kEpiWarps);
@@ -276,7 +277,7 @@ __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xf
 // The tiles a pair takes: pair0, pair0 + pairs, ...  Finding a tile's place
 // takes divisions and a search, ~1000 cycles, of the ~3000 a small tile takes
 // in all; so a warp finds 32 tiles at a time, one a lane, and hands them out.
-template <int kMode, bool kTurns>
+template <int kMode, bool kBf16>
 struct TileWalk {
   const ExpertArgs& p;
   const Shape& sh;
@@ -284,7 +285,7 @@ struct TileWalk {
   const int32_t* first;
   int t, pairs, n_tiles;
   int held;               // tiles left in `mine`
-  int rest, turn;         // kTurns: what is left of the tile's contraction, and a turn's share
+  int rest, turn;         // what is left of the tile's contraction, and a turn's share
   Tile mine;
 
   __device__ __forceinline__ TileWalk(const ExpertArgs& p_, const Shape& sh_, const int32_t* start_,
@@ -294,7 +295,7 @@ struct TileWalk {
   // its n_mma and k_len); false after the last.
   template <bool kShape = false>
   __device__ __forceinline__ bool next(Tile& r) {
-    if (kTurns && rest > 0) {
+    if (rest > 0) {
       r.k_from += r.k_len;
       r.k_len = min(rest, turn);
       rest -= r.k_len;
@@ -319,13 +320,10 @@ struct TileWalk {
     r.n_mma = __shfl_sync(0xffffffffu, mine.n_mma, lane);
     r.k_len = __shfl_sync(0xffffffffu, mine.k_len, lane);
     r.k_from = 0;
-    if (kTurns) {
-      rest = 0;
-      if (r.k_len > kMaxK) {
-        turn = (ceil_div(r.k_len, ceil_div(r.k_len, kMaxK)) + kBlockK - 1) / kBlockK * kBlockK;
-        rest = r.k_len - turn;
-        r.k_len = turn;
-      }
+    if (r.k_len > kMaxK(kBf16)) {
+      turn = (ceil_div(r.k_len, ceil_div(r.k_len, kMaxK(kBf16))) + kBlockK - 1) / kBlockK * kBlockK;
+      rest = r.k_len - turn;
+      r.k_len = turn;
     }
     --held;
     t += pairs;
@@ -447,18 +445,32 @@ __device__ __forceinline__ void fetched_row(const uint8_t* buf, uint32_t (&w)[32
   }
 }
 
+// Adds the columns at `before` of the other accumulator, the sum of a tile's earlier turns
+// (16 at a time, for the registers).
+template <int kN>
+__device__ __forceinline__ void add_before(uint32_t before, uint32_t (&r)[kN]) {
+#pragma unroll
+  for (int h = 0; h < kN; h += 16) {
+    uint32_t b[16];
+    ptx::tmem_get_32x32b_x16(before + h, b);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) r[h + k] = __float_as_uint(__uint_as_float(r[h + k]) + __uint_as_float(b[k]));
+  }
+}
+
 // One chunk of a weight gradient's rows from the accumulator at `taddr`: 64
-// columns to bf16, or 32 to fp32; kAccumulate: added to `w`, what is there.  `last`: then
-// hands the accumulator back.
+// columns to bf16 (`sum`: with those at `before` added), or 32 to fp32; kAccumulate: added to
+// `w`, what is there.  `last`: then hands the accumulator back.
 template <bool kBf16, bool kAccumulate, typename Release>
 __device__ __forceinline__ void put_chunk(const CUtensorMap* map, uint8_t* stage, uint32_t (&w)[32], uint32_t taddr,
-                                          int x, int y, int z, int rows, uint32_t& parts, bool add, bool last,
-                                          Release release) {
+                                          uint32_t before, bool sum, int x, int y, int z, int rows, uint32_t& parts,
+                                          bool add, bool last, Release release) {
   uint32_t acc[32];
 #pragma unroll
   for (int h = 0; h < (kBf16 ? 2 : 1); ++h) {
     ptx::tmem_ld_32x32b_x32(taddr + 32 * h, acc);
     ptx::tmem_ld_wait();
+    if (kBf16 && sum) add_before(before + 32 * h, acc);
     if (last && h == (kBf16 ? 1 : 0)) release();
 #pragma unroll
     for (int k = 0; k < (kBf16 ? 16 : 32); ++k) {
@@ -624,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
     ptx::fence_proxy_async_global();
   }
   const int n_tiles = listed ? first[p.n_experts] : p.n_experts * sh.tiles_m * sh.tiles_n;
-  TileWalk<kMode, !kBf16> walk(p, sh, start, first, blockIdx.x >> 1, gridDim.x >> 1, n_tiles);
+  TileWalk<kMode, kBf16> walk(p, sh, start, first, blockIdx.x >> 1, gridDim.x >> 1, n_tiles);
   Tile tl;
   // Shared memory of a stage: A, then this CTA's half of B.
   const int wide = kWgrad ? sh.width_n : widest;
@@ -793,7 +805,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
     } fetch{};
     uint8_t* const fetch_buf = smem_raw + (smem_base - ptx::smem_u32(smem_raw)) + kRingBytes(kMode, kAccumulate) +
                                kEpiWarps * 2 * kPartBytes(kMode) + (warp - kFirstEpiWarp) * kFetches * kFetchBytes;
-    TileWalk<kMode, !kBf16> ahead = walk;
+    TileWalk<kMode, kBf16> ahead = walk;
     auto fetch_next = [&]() {
       fetch.c += 2 * kWidth;
       while (fetch.more && fetch.c >= fetch.tl.n_mma) {
@@ -840,14 +852,40 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
       if (!__all_sync(0xffffffffu, wait_bar<false>(ptx::smem_u32(&tfull_bar[a]), (acc_it >> 1) & 1, ab, kRoleAccFull)))
         break;
       ptx::tc_fence_after();
-      const uint32_t t_row = tmem_base + a * kAccCols + ((uint32_t)(quad * 32) << 16);
-      // this warp's reads of the accumulator are done: hand it back
-      auto release = [&]() {
+      const uint32_t t_lane = tmem_base + ((uint32_t)(quad * 32) << 16);
+      const uint32_t t_row = t_lane + a * kAccCols, t_before = t_lane + (a ^ 1) * kAccCols;
+      // A bf16 output's turns: the sum of the earlier ones stands in the other accumulator,
+      // whose turn to be filled comes next, and moves to this one.
+      const bool sum = kBf16 && tl.k_from > 0;
+      // this warp's reads of the accumulators are done: hand them back
+      auto hand_back = [&](bool this_one, bool before) {
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive_signal(ptx::mapa_shared(ptx::smem_u32(&tempty_bar[a]), 0));
+        if (lane == 0) {
+          if (before) ptx::mbar_arrive_signal(ptx::mapa_shared(ptx::smem_u32(&tempty_bar[a ^ 1]), 0));
+          if (this_one) ptx::mbar_arrive_signal(ptx::mapa_shared(ptx::smem_u32(&tempty_bar[a]), 0));
+        }
       };
-      if (kWidth * half >= tl.n_mma) release();           // no chunk for this warp
+      auto release = [&]() { hand_back(true, sum); };
+      if (kWidth * half >= tl.n_mma) {                    // no chunk for this warp
+        hand_back(true, false);
+      } else if (kBf16 && walk.rest > 0) {
+        if (sum) {
+          for (int c = kWidth * half; c < tl.n_mma; c += 2 * kWidth)
+#pragma unroll
+            for (int h = 0; h < kWidth; h += 16) {
+              uint32_t r[16];
+              ptx::tmem_get_32x32b_x16(t_row + (uint32_t)(c + h), r);
+              add_before(t_before + (uint32_t)(c + h), r);
+              ptx::tmem_put_32x32b_x16(t_row + (uint32_t)(c + h), r);
+            }
+          hand_back(false, true);
+        }
+      }
+      if (kBf16 && walk.rest > 0) {
+        ++acc_it;
+        continue;
+      }
       const bool add = !kBf16 && tl.k_from > 0;
       if (kVec && !kBf16 && tl.k_from > 0) {               // what the last turn wrote is there
         if (lane == 0) ptx::bulk_wait_all();
@@ -865,13 +903,14 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
             __syncwarp();
             fetch_next();
           }
-          put_chunk<kBf16, kAccumulate>(&maps.out, stage, w, t_row + c, tl.n0 + c, row0, tl.z, sh.m - row0, parts, add,
-                                        last, release);
+          put_chunk<kBf16, kAccumulate>(&maps.out, stage, w, t_row + c, t_before + c, sum, tl.n0 + c, row0, tl.z,
+                                        sh.m - row0, parts, add, last, release);
           continue;
         }
         uint32_t r[32];
         ptx::tmem_ld_32x32b_x32(t_row + (uint32_t)c, r);
         ptx::tmem_ld_wait();
+        if (sum) add_before(t_before + (uint32_t)c, r);
         if (last) release();
         if constexpr (kWgrad) {
           put_plain<kBf16, kAccumulate>(p, stage, r, at0 + c, sh.m - row0, tl.n - c, add);

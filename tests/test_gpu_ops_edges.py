@@ -5,7 +5,8 @@ import numpy as np
 import pytest
 
 from oracle.ops import grad_clip_ref
-from tests.test_gpu_ops import scratch
+from tests.test_gpu_ops import U, scratch, test_expert_matmul as check_matmul, \
+    test_expert_weight_grad as check_weight_grad
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -37,3 +38,71 @@ def test_norm_that_is_no_number(mfsdp, limit, bad, at):
     assert np.array_equal(out.tolist(), want, equal_nan=True)
     if bad == "nan":
         assert torch.isnan(s.dsts[0]).all()
+
+
+# ------------------------------------------------------- products by expert
+def positive(*shape, seed):
+    """Magnitudes of normal bf16 values: no sum of their products is larger than the whole."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.empty(shape, device="cuda").normal_(generator=g).abs_().bfloat16()
+
+
+def rounded_once(got, want, k, what):
+    """A bf16 output is the rounding of a value whose error comes from the sums alone: an accumulator
+    takes 32768 of the contraction at most, 2048 additions of 16 products that cut off 2 u
+    each, then a rounded addition for each accumulator.  Rounding is monotone, so the output
+    lies between the rounded ends of that interval."""
+    sums = (2 * 2048 + k / 32768 + 2) * U
+    low, high = ((want * (1 + s)).bfloat16() for s in (-sums, sums))
+    bad = (got < low) | (got > high)
+    rel = (got.double() - want) / want
+    assert not bad.any(), f"{what}: {int(bad.sum())} of {bad.numel()}, mean error {float(rel.mean()):.3e}"
+
+
+@pytest.mark.parametrize("rows,cols", [(96, 960), (93, 955)])
+def test_bf16_outputs_of_a_million_long_contraction(mfsdp, rows, cols):
+    """(93 and 955: no row of an output starts on a 16-byte boundary.)"""
+    k = 1 << 20
+    x, w = positive(64, k, seed=1), positive(1, rows, k, seed=2)
+    starts = torch.tensor([0, 64], dtype=torch.int32, device="cuda")
+    want = x.double() @ w[0].double().T
+    y = torch.empty(64, rows, dtype=torch.bfloat16, device="cuda")
+    ws = scratch(mfsdp.expert_workspace_bytes(1, rows, k, 64))
+    mfsdp.expert_matmul(x, w, starts, y, ws)
+    rounded_once(y, want, k, "forward")
+    wt = w.transpose(1, 2).contiguous()                                # the input gradient contracts over rows
+    ws = scratch(mfsdp.expert_workspace_bytes(1, k, rows, 64))
+    mfsdp.expert_matmul(x, wt, starts, y, ws, input_grad=True)
+    rounded_once(y, want, k, "input gradient")
+    del w, wt, want
+    # 2560 x 960: tiles for every SM, so that the contraction is not cut for theirs
+    base = positive(k, 80, seed=3)
+    xs = base.repeat(1, 12)[:, :cols].contiguous()
+    dy = x.T.contiguous().repeat(1, 40)
+    want = (x.double() @ base.double()).repeat(40, 12)[:, :cols]
+    starts[1] = k
+    ws = scratch(mfsdp.expert_workspace_bytes(1, 2560, cols, k))
+    dw = torch.empty(1, 2560, cols, dtype=torch.bfloat16, device="cuda")
+    mfsdp.expert_weight_grad(dy, xs, starts, dw, ws)
+    rounded_once(dw[0], want, k, "weight gradient")
+    before = dw.clone()
+    mfsdp.expert_weight_grad(dy, xs, starts, dw, ws, accumulate=True)
+    rounded_once(dw[0], want + before[0].double(), k, "weight gradient added")
+    assert mfsdp.op_device_status(ws)[0] == 0
+
+
+@pytest.mark.parametrize("counts,k", [([40, 300], 32_768), ([17, 0, 33], 32_769), ([260], 65_537), ([33, 5], 100_008)])
+@pytest.mark.parametrize("extra", [0, 3])
+def test_bf16_outputs_over_several_accumulators(mfsdp, counts, k, extra):
+    """On both sides of one accumulator's contraction, groups beside each other, and tiles of one
+    and of two chunks of columns."""
+    check_matmul(mfsdp, "bf16", counts, 72, k, extra, 2, False)
+    check_matmul(mfsdp, "bf16", counts, k, 40, extra, 2, True)
+
+
+@pytest.mark.parametrize("counts", [[32_768, 70], [40_001, 5, 65_700, 1030]])
+@pytest.mark.parametrize("extra,accumulate", [(0, False), (0, True), (3, False), (3, True)])
+def test_bf16_weight_gradients_over_several_accumulators(mfsdp, counts, extra, accumulate):
+    """Tiles of one accumulator among tiles of several; 300 x 1800 in tiles of 256 x 256, 16 of them, so
+    that groups are not cut for the GPU's sake."""
+    check_weight_grad(mfsdp, "bf16", accumulate, counts, 300, 1800, extra, 0)
