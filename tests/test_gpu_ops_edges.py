@@ -106,3 +106,65 @@ def test_bf16_weight_gradients_over_several_accumulators(mfsdp, counts, extra, a
     """Tiles of one accumulator among tiles of several; 300 x 1800 in tiles of 256 x 256, 16 of them, so
     that groups are not cut for the GPU's sake."""
     check_weight_grad(mfsdp, "bf16", accumulate, counts, 300, 1800, extra, 0)
+
+
+def relative(got, want):
+    return float((got.double() - want).norm() / want.norm())
+
+
+@pytest.mark.parametrize("k", [1025, 2048, 16_384, 70_000])
+def test_fp32_outputs_in_the_2_norm(mfsdp, k):
+    """Normal operands.  A turn of 1024 is 64 additions of 16 products; each cuts off up to a unit of
+    the partial sum p, half a unit in the mean, which is 0.72 u |p| (u = 2^-24; the mean of
+    a unit over p's place between two powers of two), always towards zero.  The partial sums
+    of N terms that are independent add up to N / sqrt(3) of the last one: 0.72 * 64 / sqrt(3) =
+    26.6 u of the turn's result, and 27 with the cuts' spread about their mean.  The
+    turns' errors are independent of each other, so they are 27 u of the whole; the T rounded
+    additions that join them are off by 0.42 u of the sums so far, 0.3 sqrt(T) u.  (Turns of 2048
+    would be 53 u by this count, and were measured at 35.)"""
+    g = torch.Generator(device="cuda").manual_seed(k)
+    normal = lambda *shape: torch.empty(shape, device="cuda").normal_(generator=g).bfloat16()
+    bound = (27 + 0.3 * (k / 1024 + 1) ** 0.5) * U
+    x, w = normal(64, k), normal(1, 96, k)
+    want = x.double() @ w[0].double().T
+    starts = torch.tensor([0, 64], dtype=torch.int32, device="cuda")
+    y = torch.empty(64, 96, device="cuda")
+    mfsdp.expert_matmul(x, w, starts, y, scratch(mfsdp.expert_workspace_bytes(1, 96, k, 64)))
+    assert relative(y, want) <= bound, "forward"
+    wt = w.transpose(1, 2).contiguous()                               # k rows: the input gradient's contraction
+    mfsdp.expert_matmul(x, wt, starts, y, scratch(mfsdp.expert_workspace_bytes(1, k, 96, 64)), input_grad=True)
+    assert relative(y, want) <= bound, "input gradient"
+    # few tokens: a lane adds k / 32 products one after the other, rounded, 0.42 u each of a sum that
+    # grows like their root: 0.3 sqrt(k / 32) u; a third more, and the lanes' five
+    starts[1] = 16
+    mfsdp.expert_matmul(x[:16], w, starts, y[:16], scratch(mfsdp.expert_workspace_bytes(1, 96, k, 16)))
+    assert relative(y[:16], want[:16]) <= (0.4 * (k / 32) ** 0.5 + 5) * U, "few tokens"
+    starts[1] = k
+    dy, xs = x.T.contiguous(), wt[0]
+    for rows, cols in ((64, 96), (2560, 960)):                        # cut for the GPU's sake, and not
+        a, b = dy.repeat(1, rows // 64), xs.repeat(1, cols // 96)
+        dw = torch.empty(1, rows, cols, device="cuda")
+        mfsdp.expert_weight_grad(a, b, starts, dw, scratch(mfsdp.expert_workspace_bytes(1, rows, cols, k)))
+        assert relative(dw[0], want.repeat(rows // 64, cols // 96)) <= bound, f"weight gradient {rows} x {cols}"
+
+
+@pytest.mark.parametrize("k", [1025, 2048, 16_384, 70_000])
+def test_fp32_outputs_element_by_element(mfsdp, k):
+    """Magnitudes: no partial sum is larger than the result.  A turn is 64 additions, and one more to
+    start with, which cut off 2 u each at most; joining T turns is T + 1 rounded additions."""
+    bound = (2 * 65 + k / 1024 + 2) * U
+    x, w = positive(64, k, seed=k), positive(1, 96, k, seed=k + 1)
+    want = x.double() @ w[0].double().T
+    starts = torch.tensor([0, 64], dtype=torch.int32, device="cuda")
+    y = torch.empty(64, 96, device="cuda")
+    mfsdp.expert_matmul(x, w, starts, y, scratch(mfsdp.expert_workspace_bytes(1, 96, k, 64)))
+    assert float(((y.double() - want) / want).abs().max()) <= bound, "forward"
+    wt = w.transpose(1, 2).contiguous()
+    mfsdp.expert_matmul(x, wt, starts, y, scratch(mfsdp.expert_workspace_bytes(1, k, 96, 64)), input_grad=True)
+    assert float(((y.double() - want) / want).abs().max()) <= bound, "input gradient"
+    starts[1] = k
+    a, b = x.T.repeat(1, 40).contiguous(), wt[0].repeat(1, 10)
+    dw = torch.empty(1, 2560, 960, device="cuda")
+    mfsdp.expert_weight_grad(a, b, starts, dw, scratch(mfsdp.expert_workspace_bytes(1, 2560, 960, k)))
+    want = want.repeat(40, 10)
+    assert float(((dw[0].double() - want) / want).abs().max()) <= bound, "weight gradient"
