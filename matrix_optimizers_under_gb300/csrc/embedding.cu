@@ -710,12 +710,8 @@ __global__ void __launch_bounds__(32 * kFixParts) embed_fix_kernel(const __grid_
 // rows: the sum of a row's positions in ascending order, one row a warp, or zeros.  A row
 // with many positions is added by the eight warps, an eighth of them each, and goes
 // first.  Bound by latency (ids, positions, rows, stores: 3 us for 64 ids of 256 columns)
-// or by writing zeros.  Through the sort and two more launches 257 ids of 768 columns take
-// 17 us, this way 9; 1024 ids of a text, 256 columns, into 1000 rows 16 and 8; 1024
-// columns into 32000 rows 28 and 31 (added: 16 and 11); 2048 columns into 5000 17
-// and 14.  1024 of one token take 19 to 34 and 23 to 63.  800 ids of 375 columns, which
-// no vector meets: 19 and 21.
-constexpr int kSmallIds = 1024;            // half of it for rows off the vectors' boundaries
+// or by writing zeros.
+constexpr int kSmallIds = 1024;            // at most (see embed_grad_sorts)
 constexpr int kSmallShare = 2048;          // rows of a share, at most: its bitmap
 constexpr int kSmallWarps = 8;
 constexpr int kSmallCols = 32 * kCols;
@@ -939,7 +935,33 @@ bool embed_grad_vec(const EmbedGradArgs& a) {
   return vec_rows(a.dout, a.dout_ld, a.dim, a.dout_bf16) && vec_rows(a.grad, a.grad_ld, a.dim, a.grad_bf16);
 }
 
-bool embed_grad_sorts(const EmbedGradArgs& a) { return a.n > (embed_grad_vec(a) ? kSmallIds : kSmallIds / 2); }
+// Few ids go in one launch; more, or many rows of zeros beside more than half of as many (a
+// quarter, off the vectors' boundaries), through the sort and two more.  The one launch's zeros wait
+// for the ids' list and its named rows, the sort hides behind the zeros.  From cold caches, GPU time
+// in us, one launch / sorted, fp32 rows, a text's ids (and half of the ids one token):
+//   512 ids,  2048 columns into  1000 rows    15.5 / 21.6  (23.6 / 19.6)
+//             2048              32000         50.3 / 54.4  (59.6 / 54.4)
+//   600,      2048              32000         51.3 / 55.4  (64.6 / 55.4)
+//   1024,      256               1000         17.5 / 21.6  (33.9 / 21.6)
+//              256              32000 (33 MB) 19.6 / 21.6  (31.9 / 21.6)
+//             2048               5000 (41 MB) 25.7 / 23.7  (40.1 / 23.7)
+//             2048              32000         56.4 / 56.4  (77.0 / 58.5)
+//             2048              32000, added  23.7 / 23.7  (40.1 / 23.7)
+//   off the vectors' boundaries
+//   1024,      375               1000         17.5 / 22.7  (28.8 / 24.7)
+//             1365               5000 (27 MB) 21.7 / 24.7  (34.0 / 25.7)
+//              375              32000 (48 MB) 23.7 / 23.6  (34.0 / 25.7)
+//             1365               5000, added  21.7 / 27.7  (31.9 / 27.8)
+//   512,       375              32000         21.7 / 23.7  (24.7 / 23.6)
+//             1365              32000, bf16 (87 MB) 33.9 / 31.9 (37.0 / 29.8)
+//             1365              32000         46.2 / 43.2  (50.3 / 42.1)
+//   256 (warm), 1365            32000         37.8 / 36.4  (all one token 41.9 / 36.2)
+bool embed_grad_sorts(const EmbedGradArgs& a) {
+  if (a.n > kSmallIds || a.accumulate) return a.n > kSmallIds;
+  const int64_t zeros = a.vocab * a.dim * (a.grad_bf16 ? 2 : 4);                  // bytes, at most
+  if (a.n > kSmallIds / 2) return zeros > 1 << 25;
+  return a.n > kSmallIds / 4 && zeros > 1 << 26 && !embed_grad_vec(a);
+}
 
 cudaError_t launch_embed_grad(const EmbedGradArgs& a, cudaStream_t s) {
   const bool vec = embed_grad_vec(a);

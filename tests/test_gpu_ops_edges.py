@@ -5,8 +5,8 @@ import numpy as np
 import pytest
 
 from oracle.ops import grad_clip_ref
-from tests.test_gpu_ops import U, scratch, test_expert_matmul as check_matmul, \
-    test_expert_weight_grad as check_weight_grad
+from tests.test_gpu_ops import U, scratch, test_embedding_grad as check_embedding_grad, \
+    test_expert_matmul as check_matmul, test_expert_weight_grad as check_weight_grad
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -168,3 +168,27 @@ def test_fp32_outputs_element_by_element(mfsdp, k):
     mfsdp.expert_weight_grad(a, b, starts, dw, scratch(mfsdp.expert_workspace_bytes(1, 2560, 960, k)))
     want = want.repeat(40, 10)
     assert float(((dw[0].double() - want) / want).abs().max()) <= bound, "weight gradient"
+
+
+# ----------------------------------------------------------------- embedding
+@pytest.mark.parametrize("n,vocab,dim,grad,accumulate,sorts", [
+    (512, 32_000, 2048, "f32", False, False), (513, 32_000, 2048, "f32", False, True),
+    (1024, 32_000, 1024, "f32", False, True), (1024, 32_000, 1024, "f32", True, False),
+    (1024, 32_000, 256, "f32", False, False), (1024, 32_768, 264, "f32", False, True),
+    (1024, 32_768, 264, "bf16", False, False), (1025, 1000, 64, "bf16", True, True),
+    (512, 32_000, 375, "f32", False, False), (257, 13_000, 1365, "f32", False, True),
+    (256, 13_000, 1365, "f32", False, False),
+    (512, 32_000, 1365, "f32", True, False), (513, 100, 9, "f32", True, False), (1025, 100, 9, "f32", True, True),
+    (1024, 5000, 1365, "f32", False, False), (1024, 6500, 1365, "f32", False, True), (0, 40_000, 2048, "f32", False, False),
+])
+def test_embedding_grad_of_few_ids_beside_many_rows(mfsdp, n, vocab, dim, grad, accumulate, sorts):
+    """On both sides of where few ids go through the sort: which way a call took shows in its
+    workspace, where the sort leaves its keys."""
+    check_embedding_grad(mfsdp, "bf16", grad, max(n, 1), vocab, dim, "zipf", 0, accumulate)
+    ids = torch.arange(n, device="cuda") % vocab
+    dout = torch.zeros(n, dim, device="cuda", dtype=torch.bfloat16)
+    g = torch.zeros(vocab, dim, device="cuda").to({"f32": torch.float32, "bf16": torch.bfloat16}[grad])
+    ws = scratch(mfsdp.embedding_grad_workspace_bytes(n, vocab, dim))
+    mfsdp.embedding_grad(dout, ids, g, ws, accumulate=accumulate)
+    assert mfsdp.op_device_status(ws)[0] == 0 or (n == 0 and accumulate)
+    assert bool((ws[256:256 + 4 * n] != 0xFF).any()) == sorts
