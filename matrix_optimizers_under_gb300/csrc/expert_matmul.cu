@@ -1343,18 +1343,34 @@ struct Prepare {
   }
 };
 
-// A weight gradient whose tiles leave half of the GPU idle has its contraction cut: chunks
+// A weight gradient whose tiles leave half of the GPU idle may have its contraction cut: chunks
 // of this many tokens (0: not cut), whose matrices go to the workspace in fp32 and are
 // added by a second kernel.  As many as the pairs take in one turn, 512 tokens at least.
-// With and without, us: 1 expert, 4096 tokens, 512 x 512: 14.3 and 24.0; 4 experts, 4096,
-// 256 x 1024: 17.3 and 16.8; 8 experts, 8192, 128 x 512: 15.8 and 17.7; 4 experts (two of them
-// with tokens), 11922, 112 x 1664: 23 and 41.
+// A pair takes 4 (bf16) to 6 ns (fp32) for a token.  Whole, the longest group sets the time: taken as
+// one and a half times the mean, which a cut has to make up for.  Cut, it is a chunk of fp32, the
+// second launch (5 us, 833 tokens' time) and the parts' way out and in (0.42 us a MB, 70 tokens').
+// Warm, GPU time in us, cut / whole, of bf16 gradients, groups even (and uneven, the longest about twice
+// the mean), * where the rule cuts:
+//    1 expert,   4096 tokens,  512 x  512   16.7 / 25.4 *
+//    1           4096         1024 x 2048   29.5 / 25.4
+//    1          16384         1024 x 1024   43.3 / 76.1 *
+//    2           8192          512 x 1024   22.8 / 25.4 (23.6 / 30.5) *
+//    4           4096          256 x 1024   18.5 / 13.1 (18.7 / 18.0)
+//    4          16384          256 x  512   19.2 / 25.4 (21.3 / 44.1) *
+//    8           8192          128 x  512   17.7 / 12.8 (17.7 / 18.2)
+//    8          16384          256 x  256   18.7 / 17.2 (18.2 / 26.7) *
+//   16          32768          256 x  512   29.0 / 18.5 (28.2 / 31.3)
+// Of 1260 such pairs, fp32 gradients among them, the rule's choice is 1.8 % above the better one
+// in the geometric mean; 1024 tokens an expert, whatever the matrices, 2.7 %, never cutting 68 %.
 int64_t split_chunk(int64_t experts, int64_t n, int64_t rows, int64_t cols) {
   const int64_t tiles = ((rows + kPairM - 1) / kPairM) * ((cols + kMaxN - 1) / kMaxN);
   const int64_t most = kSplitPairs / tiles;          // chunks in all
-  if (2 * experts > most || n < 4096 || n < 1024 * experts) return 0;
+  if (2 * experts > most || n < 4096) return 0;
   const int64_t parts = most - experts + 1;          // every expert's last chunk is short
-  return std::max<int64_t>(512, ((n + parts - 1) / parts + kBlockK - 1) / kBlockK * kBlockK);
+  const int64_t chunk = std::max<int64_t>(512, ((n + parts - 1) / parts + kBlockK - 1) / kBlockK * kBlockK);
+  const int64_t longest = experts == 1 ? n : 3 * n / (2 * experts);
+  const int64_t part_bytes = (2 * n / chunk + experts) * rows * up4(cols) * 2;       // n / chunk + experts / 2 parts
+  return longest > chunk + 833 + 70 * part_bytes / 1000000 ? chunk : 0;
 }
 // Chunks that there can be.
 int64_t split_slots(int64_t experts, int64_t n, int64_t chunk) { return n / chunk + experts; }

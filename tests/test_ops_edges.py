@@ -69,3 +69,16 @@ def test_binding_refuses_workspaces_that_are_no_device_memory(mfsdp):
                 call(None)
     assert mfsdp._ws(Cuda(64, dtype=torch.float32))[1] == 256          # bytes, whatever the type
     assert mfsdp.op_device_status(None, stream=0)[0] == mfsdp.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("experts,n,rows,cols,cut", [
+    (1, 4096, 512, 512, True), (1, 4095, 512, 512, False), (1, 4096, 1024, 2048, False), (1, 16_384, 1024, 1024, True),
+    (4, 4096, 256, 1024, False), (4, 16_384, 256, 512, True), (8, 8192, 128, 512, False), (16, 32_768, 256, 512, False),
+    (2, 8192, 512, 1024, True), (128, 32_768, 1408, 2048, False), (39, 1 << 20, 64, 64, False)])
+def test_weight_gradients_are_cut_where_that_pays(mfsdp, experts, n, rows, cols, cut):
+    """A cut contraction takes fp32 matrices in the workspace, beside the status word and the
+    groups' padded ends: the sizes on both sides of the rule, as measured."""
+    up = lambda b: -(-b // 256) * 256
+    plain = 256 + up(16 * experts * rows * 2) + up(16 * experts * cols * 2)
+    got = mfsdp.raw_lib().mfsdp_expert_workspace_bytes(experts, n, rows, cols, rows * cols, rows, cols)
+    assert got == plain if not cut else got >= plain + experts * rows * cols * 4, (got, plain)
