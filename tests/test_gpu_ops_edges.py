@@ -1,12 +1,14 @@
 """GPU cases of the operators next to the owner step that earlier tests leave out.
 (Helpers and the derivation of the tolerances: test_gpu_ops.py.)
 """
+import threading
+
 import numpy as np
 import pytest
 
 from oracle.ops import grad_clip_ref
 from tests.test_gpu_ops import U, scratch, test_embedding_grad as check_embedding_grad, \
-    test_expert_matmul as check_matmul, test_expert_weight_grad as check_weight_grad
+    test_expert_matmul as check_matmul, test_expert_weight_grad as check_weight_grad, test_sort_ids as check_sort
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -179,7 +181,8 @@ def test_fp32_outputs_element_by_element(mfsdp, k):
     (512, 32_000, 375, "f32", False, False), (257, 13_000, 1365, "f32", False, True),
     (256, 13_000, 1365, "f32", False, False),
     (512, 32_000, 1365, "f32", True, False), (513, 100, 9, "f32", True, False), (1025, 100, 9, "f32", True, True),
-    (1024, 5000, 1365, "f32", False, False), (1024, 6500, 1365, "f32", False, True), (0, 40_000, 2048, "f32", False, False),
+    (1024, 5000, 1365, "f32", False, False), (1024, 6500, 1365, "f32", False, True),
+    (0, 40_000, 2048, "f32", False, False),
 ])
 def test_embedding_grad_of_few_ids_beside_many_rows(mfsdp, n, vocab, dim, grad, accumulate, sorts):
     """On both sides of where few ids go through the sort: which way a call took shows in its
@@ -192,3 +195,138 @@ def test_embedding_grad_of_few_ids_beside_many_rows(mfsdp, n, vocab, dim, grad, 
     mfsdp.embedding_grad(dout, ids, g, ws, accumulate=accumulate)
     assert mfsdp.op_device_status(ws)[0] == 0 or (n == 0 and accumulate)
     assert bool((ws[256:256 + 4 * n] != 0xFF).any()) == sorts
+
+
+# ------------------------------------------------------------------- id sort
+@pytest.mark.parametrize("n", [20_001, 32_768, 40_000, 65_535, 65_536, 65_537])
+@pytest.mark.parametrize("keys", [3, 128, 32_000, 70_000])
+def test_sort_of_as_many_ids_as_a_cluster_holds(mfsdp, n, keys):
+    """Three to eight pairs a thread, and on both sides of the last length that one cluster sorts."""
+    check_sort(mfsdp, torch.int64, n, keys)
+
+
+# ------------------------------------------- streams, graphs, threads, repeats
+class Chain:
+    """Every operator once, at sizes that take the ways of several launches: a sort in a
+    cluster, slabs that cut rows, fp32 products in turns, a weight gradient that is cut and one that
+    adds, and clipping of more than one chunk a tensor.  dim 1101: no row starts on a 16-byte boundary."""
+
+    def __init__(self, m, dim, seed=0):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        self.m, vocab, n, e, rows = m, 3000, 6000, 2, 320
+
+        def normal(*shape, dtype=torch.float32):
+            return torch.empty(shape, device="cuda").normal_(generator=g).to(dtype)
+
+        def new(*shape, dtype=torch.float32):
+            return torch.full(shape, 7, dtype=dtype, device="cuda")
+
+        rng = np.random.default_rng(seed)
+        self.table, self.w = normal(vocab, dim), normal(e, rows, dim, dtype=torch.bfloat16)
+        self.ids = torch.from_numpy(np.minimum(rng.zipf(1.3, n) - 1, vocab)).cuda()      # some masked
+        self.expert = torch.from_numpy(rng.integers(0, e, n)).cuda()
+        self.order, self.starts = new(n, dtype=torch.int32), new(e + 1, dtype=torch.int32)
+        self.h, self.hs = new(n, dim, dtype=torch.bfloat16), new(n, dim, dtype=torch.bfloat16)
+        self.y, self.yb = new(n, rows), new(n, rows, dtype=torch.bfloat16)
+        self.dx, self.dw, self.dwb = new(n, dim), new(e, rows, dim), new(e, rows, dim, dtype=torch.bfloat16)
+        self.dtab, self.norm = new(vocab, dim), new(2)
+        self.clipped = [new(*t.shape) for t in (self.dw, self.dtab)]
+        self.set = m.grad_set([self.dw, self.dtab], self.clipped)
+        self.ws = [scratch(k) for k in (m.sort_ids_workspace_bytes(n, e), m.expert_workspace_bytes(e, rows, dim, n),
+                                        m.embedding_grad_workspace_bytes(n, vocab, dim),
+                                        m.grad_clip_workspace_bytes(self.set))]
+        plain = m.expert_workspace_bytes(e, rows, dim, 4095)
+        assert self.ws[1].numel() > plain + 4 * self.dw.numel()                  # the weight gradient is cut
+        torch.cuda.synchronize()
+
+    def run(self):
+        m = self.m
+        m.embedding_lookup(self.table, self.ids, self.h)
+        m.sort_ids(self.expert, 2, self.order, self.starts, self.ws[0])
+        m.embedding_lookup(self.h, self.order, self.hs)
+        m.expert_matmul(self.hs, self.w, self.starts, self.y, self.ws[1])
+        self.yb.copy_(self.y)
+        m.expert_matmul(self.yb, self.w, self.starts, self.dx, self.ws[1], input_grad=True)
+        m.expert_weight_grad(self.yb, self.hs, self.starts, self.dw, self.ws[1])
+        self.dwb.fill_(1.0)
+        m.expert_weight_grad(self.yb, self.hs, self.starts, self.dwb, self.ws[1], accumulate=True)
+        m.embedding_grad(self.dx, self.ids, self.dtab, self.ws[2])
+        m.embedding_grad(self.dx, self.ids, self.dtab, self.ws[2], accumulate=True)
+        m.grad_clip(self.set, self.norm, self.ws[3], max_norm=1.0)
+
+    def results(self):
+        return [self.order, self.starts, self.hs, self.y, self.dx, self.dw, self.dwb, self.dtab, self.norm,
+                *self.clipped]
+
+    def keep(self):
+        torch.cuda.synchronize()
+        return [t.clone() for t in self.results()]
+
+
+def same(chain, want):
+    torch.cuda.synchronize()
+    assert chain.m.op_device_status(chain.ws[1])[0] == chain.m.op_device_status(chain.ws[2])[0] == 0
+    for k, (a, b) in enumerate(zip(chain.results(), want)):
+        assert torch.equal(a, b), f"result {k}"
+        assert torch.isfinite(a.float()).all()
+
+
+@pytest.mark.parametrize("dim", [1104, 1101])
+def test_chain_repeats_bit_for_bit(mfsdp, dim):
+    """On one workspace, eagerly and replayed: no sum's order depends on timing."""
+    c = Chain(mfsdp, dim)
+    c.run()
+    want = c.keep()
+    for _ in range(5):
+        c.run()
+        same(c, want)
+    d = Chain(mfsdp, dim)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        d.run()
+    for _ in range(5):
+        graph.replay()
+        same(d, want)
+
+
+@pytest.mark.parametrize("dim", [1104, 1101])
+def test_two_chains_on_two_streams_at_once(mfsdp, dim):
+    chains = [Chain(mfsdp, dim, seed) for seed in (0, 1)]
+    want = []
+    for c in chains:
+        c.run()
+        want.append(c.keep())
+    streams = [torch.cuda.Stream() for _ in chains]
+    for _ in range(10):
+        for c, s in zip(chains, streams):
+            with torch.cuda.stream(s):
+                c.run()
+    for c, w in zip(chains, want):
+        same(c, w)
+
+
+def test_two_host_threads(mfsdp):
+    """Calls from two threads, each on its own stream and workspaces."""
+    chains = [Chain(mfsdp, 1104, seed) for seed in (2, 3)]
+    want, errors = [], []
+    for c in chains:
+        c.run()
+        want.append(c.keep())
+
+    def work(c):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(10):
+                    c.run()
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:                                # noqa: BLE001 (a thread's exceptions are lost)
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(c,)) for c in chains]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    for c, w in zip(chains, want):
+        same(c, w)
