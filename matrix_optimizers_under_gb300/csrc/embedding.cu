@@ -8,8 +8,8 @@
 // the gradient writes every row of dW once, or with `accumulate` adds to the
 // rows that tokens name.
 //
-// Both are bound by HBM, or by L2 where rows repeat.  A thread takes 8 columns with one
-// 16- or 32-byte access a row.  Layouts whose rows do not start on such a boundary are read in
+// Both are bound by how many loads are on their way, and the gradient of a batch by HBM's
+// writes.  A thread takes 8 columns with one 16- or 32-byte access a row.  Layouts whose rows do not start on such a boundary are read in
 // the 16-byte words that hold their rows.
 //
 // Gradient, of more ids than a few, in three launches: the sort of positions by token
@@ -25,10 +25,10 @@
 //     order.  The slabs depend on the sizes alone, so every sum has a fixed
 //     order: no atomics on sums, bitwise reproducible, in fp32.
 //   - Rows of dout arrive in shared memory as bulk copies, an instruction a row,
-//     and a zero row leaves as one.  32768 ids, 32000 x 2048 fp32: 86 us in all, of which
-//     ~10 before the zeros and ~10 after the rows; 396 MB in between at 6.3 TB/s (a
-//     fill alone writes at 6.2, a copy runs at 6.8).  With plain loads and stores after
-//     the sort, the rows alone took 72 us.
+//     and a zero row leaves as one.  32768 ids, 32000 x 2048 fp32: 86 us in all, 396 MB.
+//     The second kernel by itself, after the sort, takes 81 with DRAM at 55 % of its peak: its
+//     17 warps an SM, all that the rings leave room for, wait for loads two thirds of the time.
+//     With plain loads and stores after the sort, the rows alone took 72 us.
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -135,8 +135,10 @@ __device__ __forceinline__ void store8(void* base, int64_t at, int tid, int thre
 }
 
 // ---------------------------------------------------------------------- lookup
-// 32768 rows of 2048, fp32 to bf16, with a text's frequencies: 37 us, bound by L2 (402 MB
-// in and out of the SMs, 11 TB/s; 150 MB of DRAM).  One row: 1.5 us.
+// 32768 rows of 2048, fp32 to bf16, with a text's frequencies: 36.5 us, 402 MB in and out of the
+// SMs.  Bound by the loads' latency: the warps wait for a load in 57 % of their cycles, with DRAM at
+// 53 %, L2 at 42 % and L1 at 51 % of their peaks; 60 registers allow 32 warps an SM, and 26
+// are there.  (A call 39.6 us; 40.7 with stores that are not marked streaming.)  One row: 1.5 us.
 constexpr int kLookupRows = 4;             // rows of a thread, all loaded before the first store
 
 template <bool kWBf16, bool kOutBf16>
@@ -283,7 +285,7 @@ struct SlabPlan {
   int64_t ctas;
 };
 SlabPlan plan_slabs(int64_t n, int64_t vocab, int64_t dim) {
-  const int64_t want = (152 - kSortSms) * ctas_per_sm(dim);
+  const int64_t want = (kSms - kSortSms) * ctas_per_sm(dim);
   SlabPlan s;
   s.slab = std::max<int64_t>(4, (n + want - 1) / want);
   s.slabs = (n + s.slab - 1) / s.slab;
@@ -867,7 +869,7 @@ void lookup_launch(const LookupArgs& a, bool vec, cudaStream_t s) {
 // not fit its bitmap.
 int64_t small_shares(int64_t vocab, int64_t dim) {
   const int64_t blocks = (dim + kSmallCols - 1) / kSmallCols;
-  const int64_t want = std::min((vocab + 7) / 8, std::max<int64_t>(1, 608 / blocks));
+  const int64_t want = std::min((vocab + 7) / 8, std::max<int64_t>(1, 4 * kSms / blocks));
   return std::max((vocab + kSmallShare - 1) / kSmallShare, want);
 }
 

@@ -35,10 +35,11 @@
 // W.
 //
 // One expert, 32768 x 2048 x 2048: 156 us, 1757 TFLOP/s.  115 experts of 1408 x 2048 that
-// share 32768 tokens: forward 165 us, input gradient of 16383 tokens 129 (6.1 TB/s),
-// weight gradient of 128 in bf16 214.  These are bound by operands on their way
+// share 32768 tokens: forward 162 us, input gradient of 16383 tokens 127, weight gradient
+// of 128 in bf16 202, each kernel by itself; 180 to 184, 129 to 132 and 214 to 223 for calls back to
+// back on inputs that L2 does not hold.  These are bound by operands on their way
 // (a group of 285 tokens takes two tiles, which both read W: 115 of them 170 us, of 256
-// tokens 150) and by HBM, at 5.4 and 4.5 TB/s.
+// tokens 150) and by HBM, at 4.9, 5.9 and 4.4 TB/s.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -85,7 +86,7 @@ constexpr int kMaxK(bool bf16) { return bf16 ? 32768 : 1024; }
 constexpr int kEpiWarps = 8;
 constexpr int kFirstEpiWarp = 4;
 constexpr int kThreads = 32 * (kFirstEpiWarp + kEpiWarps);
-constexpr int kSplitPairs = 76;                       // pairs that a split contraction is cut for
+constexpr int kSplitPairs = kSms / 2;                 // pairs that a split contraction is cut for
 constexpr int kFewTokens = 16;                         // forward: so many go without tensor cores
 constexpr int kAccCols = 256;
 constexpr int kTmemCols = 512;
@@ -108,7 +109,7 @@ struct ChunkSumArgs {
   int32_t experts, chunk, slots, accumulate;
 };
 
-// First failing wait of a launch: (role << 0); the wait's limit.
+// First failing wait of a launch (its role), and the waits' limit.
 struct Abort {
   volatile int* flag;
   int32_t* status;
@@ -1457,7 +1458,7 @@ cudaError_t launch_expert(const ExpertArgs& in, cudaStream_t s) {
     const cudaError_t err = launch_mode<kExpertWeightGrad>(a, maps, stack * mt * ((a.cols + kMaxN - 1) / kMaxN), s);
     if (err != cudaSuccess || a.chunk == 0) return err;
     const int64_t items = (a.rows * (a.out_ld / 4) + 31) / 32;
-    const dim3 grid((unsigned)std::min<int64_t>(items, (1216 + a.n_experts - 1) / a.n_experts), (unsigned)a.n_experts);
+    const dim3 grid((unsigned)std::min<int64_t>(items, (8 * kSms + a.n_experts - 1) / a.n_experts), (unsigned)a.n_experts);
     return launch_overlapped(sum_bf16 ? sum_chunks_kernel<true> : sum_chunks_kernel<false>, grid, dim3(32 * kSumWarps),
                              0, s, true, sum);
   }

@@ -223,7 +223,7 @@ struct EmbedLayout {
 };
 EmbedLayout embed_layout(int64_t n, int64_t vocab, int64_t dim) {
   EmbedLayout l;
-  size_t off = 256;                                         // the status word and a counter
+  size_t off = 256;                                         // the status word
   l.keys = off; off += round_up((size_t)n * 4, 256);
   l.order = off; off += round_up((size_t)n * 4, 256);
   l.sort = off; off += round_up(sort_scratch_bytes(n, vocab), 256);

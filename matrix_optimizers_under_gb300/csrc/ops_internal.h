@@ -52,6 +52,11 @@ constexpr int kMaxDevices = 64;
 // SM count of the current device, looked up once per device (0: no device).
 int sm_count();
 
+// SMs of a GB300.  Sizes that a workspace's length follows from use it, since that length is asked
+// for where there may be no device; on another count the results stay right and the CTAs
+// meant to run at once may not.
+constexpr int kSms = 152;
+
 // ------------------------------------------------- gradient norm and clipping
 // One tensor of a gradient set and the chunks it is cut into.
 struct ClipTensor {
