@@ -617,8 +617,8 @@ size_t mfsdp_embedding_grad_workspace_bytes(int64_t n, int64_t vocab, int64_t di
 
 /* Gradient of the lookup by sorted tokens:
  *   grad[v, :] = scale * sum over t with ids[t] = v of dout[t, :]
- * summed in fp32 (scale rounded to fp32) in a fixed order, rounded once to grad_dtype.  accumulate = 0 writes
- * every row (zeros where no id names it); accumulate = 1 adds to the rows that
+ * summed in fp32 (scale rounded to fp32) in a fixed order, rounded once to
+ * grad_dtype.  accumulate = 0 writes every row (zeros where no id names it); accumulate = 1 adds to the rows that
  * ids name (read in grad_dtype, added in fp32) and leaves the others alone.
  *   dout   n rows of dim elements, dout_ld apart;  grad  vocab rows, grad_ld
  *          apart; both 16-byte aligned.

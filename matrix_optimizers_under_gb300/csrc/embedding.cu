@@ -9,8 +9,8 @@
 // rows that tokens name.
 //
 // Both are bound by how many loads are on their way, and the gradient of a batch by HBM's
-// writes.  A thread takes 8 columns with one 16- or 32-byte access a row.  Layouts whose rows do not start on such a boundary are read in
-// the 16-byte words that hold their rows.
+// writes too.  A thread takes 8 columns with one 16- or 32-byte access a row.  Layouts whose
+// rows do not start on such a boundary are read in the 16-byte words that hold their rows.
 //
 // Gradient, of more ids than a few, in three launches: the sort of positions by token
 // (stable), the rows, and the rows that the division of work cut.

@@ -1458,7 +1458,8 @@ cudaError_t launch_expert(const ExpertArgs& in, cudaStream_t s) {
     const cudaError_t err = launch_mode<kExpertWeightGrad>(a, maps, stack * mt * ((a.cols + kMaxN - 1) / kMaxN), s);
     if (err != cudaSuccess || a.chunk == 0) return err;
     const int64_t items = (a.rows * (a.out_ld / 4) + 31) / 32;
-    const dim3 grid((unsigned)std::min<int64_t>(items, (8 * kSms + a.n_experts - 1) / a.n_experts), (unsigned)a.n_experts);
+    const int64_t blocks = std::min<int64_t>(items, (8 * kSms + a.n_experts - 1) / a.n_experts);
+    const dim3 grid((unsigned)blocks, (unsigned)a.n_experts);
     return launch_overlapped(sum_bf16 ? sum_chunks_kernel<true> : sum_chunks_kernel<false>, grid, dim3(32 * kSumWarps),
                              0, s, true, sum);
   }
