@@ -209,7 +209,8 @@ struct LogprobArgs {
   float* top_logprob;
   int64_t n, vocab, x_ld;
   int32_t x_bf16, ids64, top_k;
-  float k2;              // scale in powers of two: scale * log2(e)
+  float scale;
+  float k2;              // the scale in powers of two: scale * log2(e)
 };
 cudaError_t launch_logprob(const LogprobArgs& a, int sms, cudaStream_t s);
 

@@ -251,7 +251,8 @@ struct Row {
 template <bool kBf16, bool kEntropy>
 __device__ __forceinline__ void put_row(const LogprobArgs& a, int64_t t, const void* row, const Stats& st) {
   const Row r(st, a.k2);
-  if (a.lse) a.lse[t] = r.bad ? NAN : r.empty ? -INFINITY : fmaf(r.m, a.k2, r.log2s) * kLn2;
+  // The gradient takes scale * x - lse: by the same scale, and rounded once.
+  if (a.lse) a.lse[t] = r.bad ? NAN : r.empty ? -INFINITY : fmaf(r.m, a.scale, r.log2s * kLn2);
   if (kEntropy) a.entropy[t] = r.bad ? NAN : r.empty ? 0.0f : (r.log2s - st.t / st.s) * kLn2;
   if (a.logprob) {
     const int64_t y = a.ids64 ? static_cast<const int64_t*>(a.targets)[t] : static_cast<const int32_t*>(a.targets)[t];

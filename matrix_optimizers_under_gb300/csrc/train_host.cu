@@ -300,6 +300,7 @@ extern "C" int mfsdp_token_logprob(const void* logits, int32_t logits_dtype, int
   a.x_bf16 = logits_dtype == MFSDP_DTYPE_BF16;
   a.ids64 = id_type == MFSDP_ID_I64;
   a.top_k = top_k;
+  a.scale = (float)scale;
   a.k2 = log2_scale(scale);
   const OpRange range("mfsdp token logprob");
   return cuda_status(launch_logprob(a, sms, static_cast<cudaStream_t>(stream)));
