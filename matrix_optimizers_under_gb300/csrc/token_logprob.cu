@@ -4,6 +4,9 @@
 //   lse = M + log S,   logprob = (z_y - M) - log S,   entropy = log S - T / S
 //   dx_j = scale (dlogprob ([j = y] - p_j) - dentropy p_j (log p_j + entropy))
 //
+// A sure token's S is barely above 1, and its logprob is -log S.  So what threads, warps and CTAs hand on is R = S - 1, the
+// sum without one of the largest logit's terms, which is 1 whatever that logit: log S = log1p(R).
+//
 // The embedding's other end: a training batch has gigabytes of logits, which go by once
 // (forward) or once in and once out (gradient).
 //
@@ -72,58 +75,62 @@ __device__ __forceinline__ float load_one(const void* p, int64_t i) {
   else return __ldg(static_cast<const float*>(p) + i);
 }
 
-// A running maximum (of x, not scaled), sum and weighted sum.  The maximum starts at -2^100, so that it
+// A running maximum (of x, not scaled), the sum without one of the maximum's terms (-1 where there is none: no live
+// logit yet), and the weighted sum, in which that term is 0.  The maximum starts at -2^100, so that it
 // times k2 is finite: an element below is 2^77 below at least, and adds nothing.
 struct Stats {
-  float m, s, t;
+  float m, rest, t;
 };
 
-// `st` against the maximum m >= st.m.  Here and below the difference comes before the product: the largest logit's is
-// then 0 and its term 1, whatever its size, and S of a row whose target is sure is no further off than 1 is.
-__device__ __forceinline__ void rebase(Stats& st, float m, float k2) {
-  const float d = (st.m - m) * k2;            // <= 0; NaN only where both are +inf, and S is NaN already
-  const float c = ptx::exp2_approx(d);
-  st.t = c * (st.t + st.s * fmaxf(d, kLeast));
-  st.s *= c;
-  st.m = m;
-}
-__device__ __forceinline__ Stats join(Stats a, Stats b, float k2) {
-  const float m = fmaxf(a.m, b.m);
-  rebase(a, m, k2);
-  rebase(b, m, k2);
-  return {m, a.s + b.s, a.t + b.t};
+// Here and below the difference comes before the product: the largest logit's is then 0 and its term 1, whatever its size.
+__device__ __forceinline__ Stats join(const Stats& a, const Stats& b, float k2) {
+  const bool first = a.m >= b.m;
+  const float d = (first ? b.m - a.m : a.m - b.m) * k2;      // <= 0; NaN only where both are +inf, and R is NaN already
+  const float c = ptx::exp2_approx(d), less = 1.0f + (first ? b.rest : a.rest);
+  return {fmaxf(a.m, b.m), fmaf(c, less, first ? a.rest : b.rest),
+          fmaf(c, fmaf(less, fmaxf(d, kLeast), first ? b.t : a.t), first ? a.t : b.t)};
 }
 
-// A thread's own sums: of pairs of elements, so that they take two operations an instruction.
-template <bool kEntropy>
+// A thread's own sums: of pairs of elements, so that they take two operations an instruction.  kApart: the batch of vectors
+// that has the maximum is summed apart, so that no sum of many terms has the maximum's 1 beside them.
+template <bool kEntropy, bool kApart>
 struct Sums {
   float m;
-  float2 s, t;
-  __device__ __forceinline__ Sums() : m(-kRange), s(make_float2(0.0f, 0.0f)), t(make_float2(0.0f, 0.0f)) {}
+  float2 s, t;       // s: without that batch, whose sum is b
+  float b;
+  int at;            // its first vector; -1: it is a single element, or none
+  __device__ __forceinline__ Sums() : m(-kRange), s(make_float2(0.0f, 0.0f)), t(make_float2(0.0f, 0.0f)), b(0.0f), at(-1) {}
   __device__ __forceinline__ void raise(float to, float k2) {          // to > m
-    const float d = (m - to) * k2;             // NaN only where both are +inf, and S is NaN already
+    const float d = (m - to) * k2;             // NaN only where both are +inf, and the sum is NaN already
     const float2 c = both(ptx::exp2_approx(d));
+    if (kApart) s.x += b;
     if (kEntropy) t = mul2(c, fma2(s, both(fmaxf(d, kLeast)), t));
     s = mul2(c, s);
     m = to;
   }
-  __device__ __forceinline__ void add(float2 x, float k2, float2 less_m) {
+  __device__ __forceinline__ void add(float2 x, float k2, float2 less_m, float2& sum) {
     const float2 d = mul2(add2(x, less_m), both(k2));
     const float2 e = make_float2(ptx::exp2_approx(d.x), ptx::exp2_approx(d.y));
-    s = add2(s, e);
+    sum = add2(sum, e);
     if (kEntropy) t = fma2(e, d, t);
   }
   __device__ __forceinline__ void add_one(float x, float k2) {
     if (kEntropy) x = ptx::max_nan(x, kFloor);
-    if (x > m) raise(x, k2);
+    const bool up = x > m;
+    if (up) raise(x, k2);
     const float d = (x - m) * k2, e = ptx::exp2_approx(d);
-    s.x += e;
     if (kEntropy) t.x = fmaf(e, d, t.x);
+    if (kApart && up) {
+      b = e;
+      at = -1;
+    } else {
+      s.x += e;
+    }
   }
-  // Some vectors at once: one look for a new maximum.  With the entropy, masked logits become -2^101, which
-  // adds 0 times a finite number.
+  // Some vectors at once, the first of them vector i: one look for a new maximum.  With the entropy, masked logits
+  // become -2^101, which adds 0 times a finite number.
   template <bool kBf16, int kVecs>
-  __device__ __forceinline__ void add(uint4 (&v)[kVecs], float k2) {
+  __device__ __forceinline__ void add(uint4 (&v)[kVecs], float k2, int64_t i) {
     float top;
     if constexpr (kBf16) {
       uint32_t mm = 0xFF7FFF7Fu;               // the lowest number twice
@@ -152,21 +159,31 @@ struct Sums {
                                fmaxf(__uint_as_float(v[b].z), __uint_as_float(v[b].w))));
       }
     }
-    if (top > m) raise(top, k2);
+    const bool up = top > m;
+    if (up) raise(top, k2);
     const float2 less_m = both(-m);
+    float2 sum = kApart ? make_float2(0.0f, 0.0f) : s;
 #pragma unroll
     for (int b = 0; b < kVecs; ++b) {
       const uint32_t w[4] = {v[b].x, v[b].y, v[b].z, v[b].w};
       if constexpr (kBf16) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) add(make_float2(lo16(w[j]), hi16(w[j])), k2, less_m);
+        for (int j = 0; j < 4; ++j) add(make_float2(lo16(w[j]), hi16(w[j])), k2, less_m, sum);
       } else {
-        add(make_float2(__uint_as_float(w[0]), __uint_as_float(w[1])), k2, less_m);
-        add(make_float2(__uint_as_float(w[2]), __uint_as_float(w[3])), k2, less_m);
+        add(make_float2(__uint_as_float(w[0]), __uint_as_float(w[1])), k2, less_m, sum);
+        add(make_float2(__uint_as_float(w[2]), __uint_as_float(w[3])), k2, less_m, sum);
       }
     }
+    if (!kApart) {
+      s = sum;
+    } else if (up) {
+      b = sum.x + sum.y;
+      at = (int)i;
+    } else {
+      s = add2(s, sum);
+    }
   }
-  __device__ __forceinline__ Stats stats() const { return {m, s.x + s.y, t.x + t.y}; }
+  __device__ __forceinline__ Stats stats() const { return {m, s.x + s.y + (b - 1.0f), t.x + t.y}; }
 };
 
 // A run of a row: `head` single elements up to the first 16-byte boundary, vectors, and `tail`
@@ -207,16 +224,16 @@ __device__ __forceinline__ void each_element(const void* row, const Span& sp, F&
 }
 
 // This thread's sums over a span that `threads` threads share, kVecs vectors at a time.
-template <bool kBf16, bool kEntropy, int kVecs>
-__device__ __forceinline__ Sums<kEntropy> sums_of(const uint8_t* row, const Span& sp, int tid, int threads, float k2) {
-  Sums<kEntropy> st;
+template <bool kBf16, bool kEntropy, int kVecs, bool kApart>
+__device__ __forceinline__ Sums<kEntropy, kApart> sums_of(const uint8_t* row, const Span& sp, int tid, int threads, float k2) {
+  Sums<kEntropy, kApart> st;
   const uint4* q = reinterpret_cast<const uint4*>(row + (sp.from + sp.head) * (kBf16 ? 2 : 4));
   int64_t i = tid;
   for (; i + (int64_t)(kVecs - 1) * threads < sp.vecs; i += (int64_t)kVecs * threads) {
     uint4 v[kVecs];
 #pragma unroll
     for (int b = 0; b < kVecs; ++b) v[b] = __ldg(q + i + b * threads);
-    st.template add<kBf16>(v, k2);
+    st.template add<kBf16>(v, k2, i);
   }
   if (i < sp.vecs) {                           // fewer: vectors that are not there are masked
     uint4 v[kVecs];
@@ -225,7 +242,7 @@ __device__ __forceinline__ Sums<kEntropy> sums_of(const uint8_t* row, const Span
       v[b] = i + b * threads < sp.vecs ? __ldg(q + i + b * threads)
              : kBf16                   ? make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u)
                                        : make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u);
-    st.template add<kBf16>(v, k2);
+    st.template add<kBf16>(v, k2, i);
   }
   if (tid < sp.head) st.add_one(load_one<kBf16>(row, sp.from + tid), k2);
   if (tid < sp.tail) st.add_one(load_one<kBf16>(row, sp.from + sp.head + sp.vecs * kPer<kBf16> + tid), k2);
@@ -235,38 +252,80 @@ __device__ __forceinline__ Sums<kEntropy> sums_of(const uint8_t* row, const Span
 // A row's joined sums as what they stand for.
 struct Row {
   bool empty, bad;
-  float m, log2s;
-  __device__ __forceinline__ Row(const Stats& st, float k2)
-      : empty(st.s == 0.0f),                   // every logit is masked
-        bad(!(st.s < INFINITY) || st.m > kRange),            // a NaN or +inf
-        m(st.m), log2s(log2f(st.s)) {}
-  __device__ __forceinline__ float logprob(float x, float k2) const {
+  float m, logs;
+  __device__ __forceinline__ explicit Row(const Stats& st)
+      : empty(st.rest < -0.5f),                // -1: every logit is masked
+        bad(!(st.rest < INFINITY) || st.m > kRange),         // a NaN or +inf
+        m(st.m), logs(log1pf(st.rest)) {}
+  __device__ __forceinline__ float logprob(float x, float scale) const {
     if (bad) return NAN;
     if (empty || x < -kRange) return -INFINITY;
-    return ((x - m) * k2 - log2s) * kLn2;
+    return fmaf(x - m, scale, -logs);
   }
 };
 
 // What a row has one of.
 template <bool kBf16, bool kEntropy>
 __device__ __forceinline__ void put_row(const LogprobArgs& a, int64_t t, const void* row, const Stats& st) {
-  const Row r(st, a.k2);
+  const Row r(st);
   // The gradient takes scale * x - lse: by the same scale, and rounded once.
-  if (a.lse) a.lse[t] = r.bad ? NAN : r.empty ? -INFINITY : fmaf(r.m, a.scale, r.log2s * kLn2);
-  if (kEntropy) a.entropy[t] = r.bad ? NAN : r.empty ? 0.0f : (r.log2s - st.t / st.s) * kLn2;
+  if (a.lse) a.lse[t] = r.bad ? NAN : r.empty ? -INFINITY : fmaf(r.m, a.scale, r.logs);
+  if (kEntropy) a.entropy[t] = r.bad ? NAN : r.empty ? 0.0f : fmaf(st.t / (1.0f + st.rest), -kLn2, r.logs);
   if (a.logprob) {
     const int64_t y = a.ids64 ? static_cast<const int64_t*>(a.targets)[t] : static_cast<const int32_t*>(a.targets)[t];
-    a.logprob[t] = y < 0 || y >= a.vocab ? 0.0f : r.logprob(load_one<kBf16>(row, y), a.k2);
+    a.logprob[t] = y < 0 || y >= a.vocab ? 0.0f : r.logprob(load_one<kBf16>(row, y), a.scale);
   }
 }
 
-__device__ __forceinline__ Stats join_warp(Stats st, float k2) {
+// The sums of a warp from its threads', each over a span's vectors tid, tid + threads and so on, kVecs at a time.  The thread
+// with the largest logit has that one's 1 among its terms, which lose what is below 2^-24 beside it.  Where all else is
+// small against the 1, they are summed once more without it: the vectors of one thread, near as a rule, or (kApart) one
+// batch of them.
+constexpr float kSmallRest = 0.5f;
+template <bool kBf16, int kVecs, bool kEntropy, bool kApart>
+__device__ __forceinline__ Stats warp_sums(const Sums<kEntropy, kApart>& sums, const uint8_t* row, const Span& sp, int tid,
+                                           int threads, float k2) {
+  constexpr uint32_t kAll = 0xFFFFFFFFu;
+  const int lane = tid & 31;
+  const Stats mine = sums.stats();
+  const int order = __float_as_int(mine.m) ^ (__float_as_int(mine.m) >> 31 & 0x7FFFFFFF);      // ordered as the maxima are
+  const bool largest = order == __reduce_max_sync(kAll, order);
+  const int owner = __ffs(__ballot_sync(kAll, largest)) - 1;
+  Stats st;
+  st.m = __shfl_sync(kAll, mine.m, owner);
+  const float d = (mine.m - st.m) * k2, c = ptx::exp2_approx(d), all = 1.0f + mine.rest;       // d: see join
+  st.rest = lane == owner ? 0.0f : c * all;
+  st.t = lane == owner ? mine.t : c * fmaf(all, fmaxf(d, kLeast), mine.t);
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const Stats other = {__shfl_xor_sync(0xFFFFFFFFu, st.m, o), __shfl_xor_sync(0xFFFFFFFFu, st.s, o),
-                         __shfl_xor_sync(0xFFFFFFFFu, st.t, o)};
-    st = join(st, other, k2);
+    st.rest += __shfl_xor_sync(kAll, st.rest, o);
+    if (kEntropy) st.t += __shfl_xor_sync(kAll, st.t, o);
   }
+  const float others = st.rest;
+  st.rest += __shfl_sync(kAll, mine.rest, owner);
+  if (!(st.m > -kRange && st.rest < kSmallRest)) return st;  // (a maximum at -2^100 came in no batch)
+  const int at = kApart ? __shfl_sync(kAll, sums.at, owner) : tid - lane + owner;
+  float sum = kApart && lane == owner ? sums.s.x + sums.s.y : 0.0f;
+  const auto add = [&](float x) {
+    if (x != st.m) sum += ptx::exp2_approx((x - st.m) * k2);   // one element is st.m: of two the rest would be 1
+  };
+  const auto add_vector = [&](int64_t i) {
+    float x[kPer<kBf16>];
+    unpack<kBf16>(__ldg(reinterpret_cast<const uint4*>(row + (sp.from + sp.head) * (kBf16 ? 2 : 4)) + i), x);
+#pragma unroll
+    for (int j = 0; j < kPer<kBf16>; ++j) add(x[j]);
+  };
+  const int64_t i = at + (int64_t)lane * threads;
+  if constexpr (kApart) {
+    if (at >= 0 && lane < kVecs && i < sp.vecs) add_vector(i);
+  } else {
+    for (int64_t k = i; k < sp.vecs; k += (int64_t)32 * threads) add_vector(k);
+    if (lane == 0 && at < sp.head) add(load_one<kBf16>(row, sp.from + at));
+    if (lane == 0 && at < sp.tail) add(load_one<kBf16>(row, sp.from + sp.head + sp.vecs * kPer<kBf16> + at));
+  }
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(kAll, sum, o);
+  st.rest = others + sum;
   return st;
 }
 
@@ -287,7 +346,9 @@ __global__ void __launch_bounds__(kRowThreads, 4) logprob_rows_kernel(const Logp
   for (int64_t t = (int64_t)blockIdx.x * teams + team; t < a.n; t += (int64_t)gridDim.x * teams) {
     const uint8_t* row = static_cast<const uint8_t*>(a.x) + t * a.x_ld * (kBf16 ? 2 : 4);
     const Span sp = span_of<kBf16>(row, a.vocab, 0, 1);
-    Stats st = join_warp(sums_of<kBf16, kEntropy, kBf16 ? 4 : 8>(row, sp, tid, threads, a.k2).stats(), a.k2);
+    constexpr int kVecs = kBf16 ? 4 : 8;
+    Stats st = warp_sums<kBf16, kVecs>(sums_of<kBf16, kEntropy, kVecs, true>(row, sp, tid, threads, a.k2), row, sp, tid,
+                                       threads, a.k2);
     if (team_warps > 1) {                      // in turns: one barrier a row
       if (lane == 0) warp_stats[turn][warp] = st;
       asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(threads) : "memory");
@@ -418,9 +479,12 @@ __global__ void __launch_bounds__(kThreads) logprob_kernel(const LogprobArgs a, 
   const uint8_t* row = static_cast<const uint8_t*>(a.x) + t * a.x_ld * (kBf16 ? 2 : 4);
   const Span sp = span_of<kBf16>(row, a.vocab, part, parts);
   if (parts > 1) ptx::cluster_arrive();
-  const Sums<kEntropy> sums = sums_of<kBf16, kEntropy, 4>(row, sp, tid, kThreads, a.k2);
+  // Apart in narrow CTAs of bf16 (8000 x 32000: 98.8 us, else 101.2; 30000 x 150: 96.4, else 102.5).  An fp32 batch has half the
+  // elements for the same selects (517 x 31999: 22.1 apart, 21.2 not), a wide CTA few batches and no register to spare.
+  constexpr bool kApart = kBf16 && kThreads == kNarrowThreads;
+  const Sums<kEntropy, kApart> sums = sums_of<kBf16, kEntropy, 4, kApart>(row, sp, tid, kThreads, a.k2);
   const float mine = sums.m;
-  Stats st = join_warp(sums.stats(), a.k2);
+  Stats st = warp_sums<kBf16, 4>(sums, row, sp, tid, kThreads, a.k2);
   if ((tid & 31) == 0) sh.warp[tid >> 5] = st;
   __syncthreads();
   if (parts > 1) ptx::cluster_wait();         // every CTA runs: the first one's shared memory may be written
@@ -431,7 +495,7 @@ __global__ void __launch_bounds__(kThreads) logprob_kernel(const LogprobArgs a, 
     } else {
       const uint32_t to = ptx::mapa_shared(ptx::smem_u32(&sh.part[part]), 0);
       ptx::st_shared_cluster_s32(to, __float_as_int(st.m));
-      ptx::st_shared_cluster_s32(to + 4, __float_as_int(st.s));
+      ptx::st_shared_cluster_s32(to + 4, __float_as_int(st.rest));
       ptx::st_shared_cluster_s32(to + 8, __float_as_int(st.t));
     }
   }
@@ -461,10 +525,10 @@ __global__ void __launch_bounds__(kThreads) logprob_kernel(const LogprobArgs a, 
   st = sh.row;
   if (tid == 0) put_row<kBf16, kEntropy>(a, t, row, st);
   if (tid < a.top_k) {
-    const Row r(st, a.k2);
+    const Row r(st);
     const uint64_t key = sh.top[tid];
     if (a.top_ids) a.top_ids[t * a.top_k + tid] = r.bad ? -1 : index_of(key);
-    if (a.top_logprob) a.top_logprob[t * a.top_k + tid] = r.logprob(logit_of(key), a.k2);
+    if (a.top_logprob) a.top_logprob[t * a.top_k + tid] = r.logprob(logit_of(key), a.scale);
   }
 }
 
