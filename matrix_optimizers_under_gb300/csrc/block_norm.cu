@@ -1083,6 +1083,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) norm_join_kernel(const NormGr
   __shared__ float sum[kJoinWarps][kJoinCols];
   const NormArgs& a = g.f;
   ptx::wait_dependencies();
+  if (a.n == 0 && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *g.status = 0;       // no other kernel runs
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   float* to = nullptr;
   const float* parts = nullptr;
