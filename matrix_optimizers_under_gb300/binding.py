@@ -1033,8 +1033,9 @@ def block_norm_grad(norm: BlockNorm, residual, stats, *, branch=None, d_residual
     side = branch if branch is not None else d_normed
     (spec, n), rows = norm._call(residual, side), norm._rows
     dim = norm.dim
+    gates = norm.gates(n) * dim if n or d_gate is None else d_gate.numel()       # without rows no gate is touched
     g = BlockNormGrads(_floats(d_post_weight, dim, "d_post_weight"), _floats(d_post_bias, dim, "d_post_bias"),
-                       _floats(d_gate, dim * norm.gates(n), "d_gate"), _floats(d_pre_weight, dim, "d_pre_weight"),
+                       _floats(d_gate, gates, "d_gate"), _floats(d_pre_weight, dim, "d_pre_weight"),
                        _floats(d_pre_bias, dim, "d_pre_bias"), 1 if accumulate else 0)
     _check(_lib.mfsdp_block_norm_grad(spec, n, *rows(residual, n, residual), *rows(branch, n, side),
                                       _floats(stats, 4 * n, "stats"), *rows(d_residual_out, n, residual),

@@ -24,3 +24,16 @@ def test_status_word_is_cleared(mfsdp, wanted):
     mfsdp.block_norm_grad(norm, rows, stats, branch=rows, d_residual_out=rows, d_normed=rows, workspace=ws, **{wanted: d})
     assert not d.any()
     assert mfsdp.op_device_status(ws) == (mfsdp.OK, 0)
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_binding_takes_the_usual_buffers(mfsdp, accumulate):
+    """What a training step passes for any batch, d_gate of the gate's size among it, which stays as it is."""
+    norm, ws, rows, stats = setup(mfsdp, 5)
+    d_gate, d = (torch.full((DIM,), 7.0, device="cuda") for _ in range(2))
+    mfsdp.block_norm_grad(norm, rows, stats, branch=rows, d_residual_out=rows, d_normed=rows, d_residual=rows, d_branch=rows,
+                          d_gate=d_gate, d_pre_weight=d, accumulate=accumulate, workspace=ws)
+    assert (d_gate == 7.0).all() and (d == (7.0 if accumulate else 0.0)).all()
+    with pytest.raises(ValueError):
+        mfsdp.block_norm_grad(norm, rows, stats, branch=rows, d_residual_out=rows, d_normed=rows,
+                              d_gate=d_gate.bfloat16(), workspace=ws)
