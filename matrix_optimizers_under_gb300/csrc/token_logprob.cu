@@ -552,6 +552,13 @@ __device__ __forceinline__ float grad_of(float x, int64_t i, const LogprobGradAr
   return a.scale * (i == r.y ? d + r.dlp : d);
 }
 
+// Not by the read-only path (load_one): in place, other threads write the same line.
+template <bool kBf16>
+__device__ __forceinline__ float load_own(const void* p, int64_t i) {
+  if constexpr (kBf16) return __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[i] << 16);
+  else return static_cast<const float*>(p)[i];
+}
+
 template <bool kBf16>
 __device__ __forceinline__ void store_one(void* p, int64_t i, float v) {
   if constexpr (kBf16) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
@@ -595,7 +602,7 @@ __global__ void __launch_bounds__(kGradThreads) logprob_grad_kernel(const Logpro
     if (r.y < 0) r.dlp = 0.0f;
     const bool zero = (r.dlp == 0.0f && r.dent == 0.0f) || r.lse == -INFINITY;
     const auto single = [&](int64_t i) {
-      store_one<kBf16>(out, i, zero ? 0.0f : grad_of(load_one<kBf16>(row, i), i, a, r));
+      store_one<kBf16>(out, i, zero ? 0.0f : grad_of(load_own<kBf16>(row, i), i, a, r));
     };
     // vectors where both rows reach their 16-byte boundaries together
     if (((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(out)) & 15) != 0) {
