@@ -18,8 +18,7 @@
 // With 8-bit states the instructions count as much as the bytes, so sums and products run on pairs of elements, and the
 // quotient is the hardware's reciprocal's (2^-22).  A code has to be what the formula in fp32 gives, whoever
 // computes it, since the next step's quotient may hang on it: the moments take no fused operations, and their root is
-// the IEEE one, by a Newton step on its residual (Markstein 1990) from the hardware's reciprocal root.  It
-// is equal to CUDA's for every float from 2^-100 up to 2^120, and zero; others take CUDA's.
+// the IEEE one (ptx::root).
 //
 // Bound by HBM: 28 bytes an element (fp32), 16 with a bf16 gradient, an 8-bit state and a bf16
 // copy.  Measured: 131 M elements, fp32 states: 513 us at 7.2 TB/s; 8-bit states, 2.1 GB: 325 us at 6.5 TB/s.
@@ -187,20 +186,6 @@ __device__ __forceinline__ float2 add_apart(float2 a, float2 b) {
   return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y));
 }
 
-// The square root, rounded to nearest.
-__device__ __forceinline__ float2 root_of(float2 v) {
-  float2 y = make_float2(fminf(ptx::rsqrt_approx(v.x), 0x1p64f), fminf(ptx::rsqrt_approx(v.y), 0x1p64f));   // of 0: finite
-  const float2 s = mul2(v, y), rest = fma2(make_float2(-s.x, -s.y), s, v);
-  float2 r = fma2(rest, mul2(y, both(0.5f)), s);
-  constexpr uint32_t kLow = (127u - 100) << 23, kSpan = 220u << 23;
-  const uint32_t bx = __float_as_uint(v.x), by = __float_as_uint(v.y);
-  if ((bx - kLow >= kSpan && bx != 0) || (by - kLow >= kSpan && by != 0)) {
-    r.x = __fsqrt_rn(v.x);
-    r.y = __fsqrt_rn(v.y);
-  }
-  return r;
-}
-
 // The block's codes and scale of x (kRoot: x >= 0, and what is not zero keeps a code that is not).
 template <bool kRoot>
 __device__ __forceinline__ float encode_block(const float2 (&x)[2][2], uint32_t (&c)[2]) {
@@ -279,7 +264,7 @@ __device__ __forceinline__ void step_block(const AdamwTensor& t, const AdamwHead
       g[j] = mul2(g[j], both(coef));
       m[j] = add_apart(mul2(m[j], both(a.beta1)), mul2(g[j], both(a.omb1)));
       v[j] = add_apart(mul2(v[j], both(a.beta2)), mul2(mul2(g[j], both(a.omb2)), g[j]));
-      const float2 root = k8 ? root_of(v[j]) : make_float2(ptx::sqrt_approx(v[j].x), ptx::sqrt_approx(v[j].y));
+      const float2 root = k8 ? ptx::root(v[j]) : make_float2(ptx::sqrt_approx(v[j].x), ptx::sqrt_approx(v[j].y));
       const float2 den = fma2(root, both(a.inv_sqrt_bc2), both(a.eps));
       const float2 inv = make_float2(ptx::rcp_approx(den.x), ptx::rcp_approx(den.y));
       p[j] = fma2(mul2(m[j], inv), both(-t.step_size), mul2(p[j], both(t.decay)));

@@ -192,5 +192,21 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return y;
 }
 
+// The square roots, rounded to nearest: a Newton step on the root's residual (Markstein 1990) from the hardware's reciprocal
+// root.  That the step rounds as the IEEE root does hangs on the approximation, so it is checked number by number:
+// equal to CUDA's for every float from 2^-100 up to 2^120, and zero; others take CUDA's.
+__device__ __forceinline__ float2 root(float2 v) {
+  const float2 y = make_float2(fminf(rsqrt_approx(v.x), 0x1p64f), fminf(rsqrt_approx(v.y), 0x1p64f));   // of 0: finite
+  const float2 s = mul2(v, y), rest = fma2(make_float2(-s.x, -s.y), s, v);
+  float2 r = fma2(rest, mul2(y, both(0.5f)), s);
+  constexpr uint32_t kLow = (127u - 100) << 23, kSpan = 220u << 23;
+  const uint32_t bx = __float_as_uint(v.x), by = __float_as_uint(v.y);
+  if ((bx - kLow >= kSpan && bx != 0) || (by - kLow >= kSpan && by != 0)) {
+    r.x = __fsqrt_rn(v.x);
+    r.y = __fsqrt_rn(v.y);
+  }
+  return r;
+}
+
 }  // namespace ptx
 }  // namespace mfsdp
