@@ -774,7 +774,9 @@ int mfsdp_token_logprob(const void* logits, int32_t logits_dtype, int64_t n, int
 /* Its gradient:
  *   dlogits_j = scale * (dlogprob * ([j = y] - p_j) - dentropy * p_j * (log p_j + entropy))
  * rounded once to the logits' dtype, with lse (and, for dentropy, entropy) as the
- * call above left them: lse is one rounding of fp32, which p has as a relative error.  An ignored target takes no dlogprob.  A row whose
+ * call above left them.  Both are of the products scale * x as fp32 rounds them: p is off by the
+ * roundings of its product and of lse, 2^-24 of their size, and by none where one logit has
+ * nearly all the probability.  An ignored target takes no dlogprob.  A row whose
  * dlogprob (or target) and dentropy are zero is zeroed without being read, a row
  * of only masked logits is zeroed.  dlogits may be logits, with the same leading
  * dimension (in place); otherwise they must not overlap.  dlogprob or dentropy may

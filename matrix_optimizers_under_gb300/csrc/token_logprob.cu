@@ -268,8 +268,8 @@ struct Row {
 template <bool kBf16, bool kEntropy>
 __device__ __forceinline__ void put_row(const LogprobArgs& a, int64_t t, const void* row, const Stats& st) {
   const Row r(st);
-  // The gradient takes scale * x - lse: by the same scale, and rounded once.
-  if (a.lse) a.lse[t] = r.bad ? NAN : r.empty ? -INFINITY : fmaf(r.m, a.scale, r.logs);
+  // From the rounded product, as the gradient takes it: a sure token's is then lse itself.
+  if (a.lse) a.lse[t] = r.bad ? NAN : r.empty ? -INFINITY : __fadd_rn(__fmul_rn(r.m, a.scale), r.logs);
   if (kEntropy) a.entropy[t] = r.bad ? NAN : r.empty ? 0.0f : fmaf(st.t / (1.0f + st.rest), -kLn2, r.logs);
   if (a.logprob) {
     const int64_t y = a.ids64 ? static_cast<const int64_t*>(a.targets)[t] : static_cast<const int32_t*>(a.targets)[t];
@@ -543,13 +543,21 @@ struct RowTerms {
   int64_t y;         // the target, -1 where it is masked
 };
 
-__device__ __forceinline__ float grad_of(float x, int64_t i, const LogprobGradArgs& a, const RowTerms& r) {
-  const float logp = fmaf(x, a.scale, -r.lse);
-  const float p = ptx::exp2_approx(logp * kLog2e);
-  float c = -r.dlp;
-  if (r.dent != 0.0f) c -= r.dent * (logp + r.entropy);
-  const float d = p > 0.0f || p != p ? p * c : 0.0f;         // a NaN stays one
-  return a.scale * (i == r.y ? d + r.dlp : d);
+// Of elements i and i + 1.  The product with the scale is rounded before lse is taken away, as it was when lse was made: the
+// two roundings of a row's largest logit are one and the same, and p of a sure token is 1.  (Not on pairs: the assembler
+// would fuse them.)
+__device__ __forceinline__ float2 grad_of(float2 x, int64_t i, const LogprobGradArgs& a, const RowTerms& r) {
+  const float2 logp = make_float2(__fsub_rn(__fmul_rn(x.x, a.scale), r.lse), __fsub_rn(__fmul_rn(x.y, a.scale), r.lse));
+  const float2 power = mul2(logp, both(kLog2e));
+  const float2 p = make_float2(ptx::exp2_approx(power.x), ptx::exp2_approx(power.y));
+  float2 c = both(-r.dlp);
+  if (r.dent != 0.0f) c = fma2(both(-r.dent), add2(logp, both(r.entropy)), c);
+  float2 d = mul2(p, c);
+  d.x = p.x > 0.0f || p.x != p.x ? d.x : 0.0f;               // c may be infinite; a NaN stays one
+  d.y = p.y > 0.0f || p.y != p.y ? d.y : 0.0f;
+  if (i == r.y) d.x = __fadd_rn(d.x, r.dlp);
+  if (i + 1 == r.y) d.y = __fadd_rn(d.y, r.dlp);
+  return mul2(d, both(a.scale));
 }
 
 // Not by the read-only path (load_one): in place, other threads write the same line.
@@ -602,7 +610,7 @@ __global__ void __launch_bounds__(kGradThreads) logprob_grad_kernel(const Logpro
     if (r.y < 0) r.dlp = 0.0f;
     const bool zero = (r.dlp == 0.0f && r.dent == 0.0f) || r.lse == -INFINITY;
     const auto single = [&](int64_t i) {
-      store_one<kBf16>(out, i, zero ? 0.0f : grad_of(load_own<kBf16>(row, i), i, a, r));
+      store_one<kBf16>(out, i, zero ? 0.0f : grad_of(both(load_own<kBf16>(row, i)), i, a, r).x);
     };
     // vectors where both rows reach their 16-byte boundaries together
     if (((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(out)) & 15) != 0) {
@@ -631,7 +639,11 @@ __global__ void __launch_bounds__(kGradThreads) logprob_grad_kernel(const Logpro
         float x[kStep];
         unpack<kBf16>(v[b], x);
 #pragma unroll
-        for (int j = 0; j < kStep; ++j) x[j] = grad_of(x[j], first + (i + b * 32) * kStep + j, a, r);
+        for (int j = 0; j < kStep; j += 2) {
+          const float2 d = grad_of(make_float2(x[j], x[j + 1]), first + (i + b * 32) * kStep + j, a, r);
+          x[j] = d.x;
+          x[j + 1] = d.y;
+        }
         __stcs(o + b * 32, pack<kBf16>(x));
       }
     }

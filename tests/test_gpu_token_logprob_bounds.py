@@ -7,11 +7,11 @@ h = sum p d, m2 = sum p d^2.
   it is rescaled at most 42 times (7 batches of a thread, 5 shuffles, 15 warps, 15 CTAs), 5u each, and added at most 72 times.
   S is then within (3 h + 4 + 210 + 72 = 286)u of itself, taken as 3 h + 290, and log S has that and 2u of its value.
   logprob = (x_y - M) scale - log S: 2 d_y u beside it:  L = (2 d_y + 3 h + 300 + 2 log S)u.
-  lse = M scale + log S, rounded once: (|lse| + 3 h + 300 + 2 log S)u.
+  lse = M scale + log S, the product and the sum rounded: (|M scale| + |lse| + 3 h + 300 + 2 log S)u.
   entropy = log S + h: h's weights are off by (3 d + 290)u each, its divisor by (3 h + 290)u, its factors by 3u and
   some: (3 m2 + 3 h^2 + 600 h)u beside log S's.
-  Gradient: log p = z - lse has lse's error, u of itself, 2u more on the way to exp2 and exp2's 4u, so p is
-  (|lse| + 3 h + 300 + 2 log S + 3 |log p| + 4)u of itself off; log p + entropy the sum of its summands' absolute errors; four
+  Gradient: log p = z - lse has lse's error and the product's, u |z|, u of itself, 2u more on the way to exp2 and exp2's 4u, so
+  p is that of lse and (|z| + 3 |log p| + 4)u of itself off; log p + entropy the sum of its summands' absolute errors; four
   roundings more.
 A bf16 output is rounded once more, by 2^-8 of its value at most.
 """
@@ -56,9 +56,9 @@ def definition(x, y, scale):
     at = torch.where(live, y, 0)[:, None]
     mine, dy = logp.gather(1, at)[:, 0], d.gather(1, at)[:, 0]
     base = 3 * h + 300 + 2 * log_s
-    b = {"logp": torch.where(torch.isfinite(dy) & live, 2 * dy + base, 0.0) * U, "lse": ((top[:, 0] + log_s).abs() + base) * U,
+    b = {"logp": torch.where(torch.isfinite(dy) & live, 2 * dy + base, 0.0) * U, "lse": (top[:, 0].abs() + (top[:, 0] + log_s).abs() + base) * U,
          "entropy": (base + 3 * m2 + 3 * h * h + 600 * h) * U}
-    return dict(logp=torch.where(live, mine, 0.0), lse=top[:, 0] + log_s, entropy=log_s + h, all=logp, p=p, at=at, live=live,
+    return dict(z=torch.where(p > 0, z, 0.0), logp=torch.where(live, mine, 0.0), lse=top[:, 0] + log_s, entropy=log_s + h, all=logp, p=p, at=at, live=live,
                 b=b, base=base)
 
 
@@ -105,9 +105,9 @@ def test_values_and_gradient(mfsdp, n, vocab, pad, dtype, offset, masked):
             one = torch.zeros_like(p).scatter_(1, w["at"], 1.0)
             factor = lp + w["entropy"][:, None]
             want = s * (a * (one - p) - c * p * factor)
-            rel = w["b"]["lse"][:, None] + (3 * lp.abs() + 4) * U
+            rel = w["b"]["lse"][:, None] + (w["z"].abs() + 3 * lp.abs() + 4) * U
             slack = s * p * (a.abs() * (rel + 6 * U)
                              + c.abs() * (factor.abs() * (rel + 8 * U)
-                                          + w["b"]["lse"][:, None] + U * lp.abs() + w["b"]["entropy"][:, None]))
+                                          + w["b"]["lse"][:, None] + U * (w["z"].abs() + lp.abs()) + w["b"]["entropy"][:, None]))
             slack = slack + (4 * U + (2.0 ** -8 if dtype == torch.bfloat16 else 0.0)) * want.abs() + 2.0 ** -100
             check(dx, want, slack, ("gradient", use_dlp, use_dent))
