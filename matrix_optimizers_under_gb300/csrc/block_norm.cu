@@ -24,7 +24,7 @@
 // 32768 x 2048 bf16 with RMS: forward 90 us (537 MB, 5.9 TB/s), gradient 142 (805 MB, 5.7 TB/s).  HBM bounds
 // neither alone: a warp has 270 and 330 instructions a row, at 0.7 and 0.5 of the issue rate, and a row's one (RMS
 // forward: two) exchange between warps is latency that the gradient's 16 warps an SM, all that its registers allow, do
-// not hide.  Before: sums by single columns with looked up forms took 404 and 622 instructions, 119 and 236 us.
+// not hide.  Before: sums by single columns with looked up forms took 404 and 622 instructions, 141 and 248 us.
 #include <cuda_bf16.h>
 
 #include <algorithm>

@@ -20,11 +20,12 @@
 // threads, bound the k-th largest logit from below (k <= 32 groups' maxima are k
 // elements).  Only the elements of threads whose own maximum reaches that bound are read again, by all threads,
 // and what reaches the bound is sorted by counting: some 20 to 50 candidates as a rule.  Where more
-// than the list holds reach it (a row of equal logits), the k largest are taken one by one
-// over the row, which is slow and right.  A cluster's CTAs sort their own, the first merges.
+// than the list holds reach it, the k largest are taken one by one over the row, which is slow and right: a row of
+// equal logits, or one with fewer than k groups that have a live logit, whose bound is -inf (20 alternatives of 32000 logits:
+// 10 live 26.7 us for one row and 3.1 ms for 8000, 300 live 10.3 and 120).  A cluster's CTAs sort their own, the first merges.
 //
-// Bound by HBM: 32768 x 32000 bf16 take 302 us forward (6.9 TB/s) and 624 us for the gradient (6.7 TB/s, the issue slots
-// some 80 % full).  One row of a generated token is latency: 7.6 us in a graph.
+// Bound by HBM: 32768 x 32000 bf16 take 308 us forward (6.8 TB/s) and 623 us for the gradient (6.7 TB/s, the issue slots
+// some 80 % full).  One row of a generated token is latency: 7.7 us in a graph.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -333,8 +334,8 @@ __device__ __forceinline__ Stats warp_sums(const Sums<kEntropy, kApart>& sums, c
 // stops the loads of the others.
 constexpr int kRowThreads = 256;
 constexpr int kRowTurns = 6;                  // rows that a team takes at least, before it grows
-// CTAs for every one that runs at once: a fresh CTA's loads are under way while others end (32768 x 32000 bf16: 302 us,
-// with one 308, with 16 303; gradient 624, with one 641, two 635,
+// CTAs for every one that runs at once: a fresh CTA's loads are under way while others end (32768 x 32000 bf16, when this
+// was chosen: 302 us, with one 308, with 16 303; gradient 624, with one 641, two 635,
 // 16 624; few long rows lose 2 to 3 %: 2000 x 100000 74.5, with one 72.3).
 constexpr int kRounds = 4;
 template <bool kBf16, bool kEntropy>
